@@ -43,6 +43,8 @@ EXPORTS = [
     "gns_dion3_workspace_bytes", "gns_dion3_step", "gns_tuned_tile", "gns_autotune_clear",
     "gns_call_plan", "gns_check_finite", "gns_select_count", "gns_safety_scale",
     "gns_gram_batched_noalloc",
+    "gns_tensor_list_bytes", "gns_tensor_list_build", "gns_tensor_list_workspace_bytes",
+    "gns_grad_norm", "gns_grad_clip", "gns_adamw_step",
 ]
 
 
@@ -132,6 +134,18 @@ def lib() -> ctypes.CDLL:
     L.gns_safety_scale.restype = ctypes.c_int
     L.gns_safety_scale.argtypes = [ctypes.POINTER(ctypes.c_double), ctypes.c_int, ctypes.c_double,
                                    ctypes.POINTER(ctypes.c_double)]
+    # lists of tensors (tensors.py); the structures are passed by address
+    L.gns_tensor_list_bytes.restype = sz
+    L.gns_tensor_list_bytes.argtypes = [vp, ctypes.c_int, i64]
+    L.gns_tensor_list_build.restype = ctypes.c_int
+    L.gns_tensor_list_build.argtypes = [vp, ctypes.c_int, i64, vp, vp, vp, sz, vp]
+    L.gns_tensor_list_workspace_bytes.restype = sz
+    L.gns_tensor_list_workspace_bytes.argtypes = [vp]
+    for f in (L.gns_grad_norm, L.gns_grad_clip):
+        f.restype = ctypes.c_int
+        f.argtypes = [vp, vp, ctypes.c_int, dbl, dbl, vp, vp, vp, vp, sz, vp]
+    L.gns_adamw_step.restype = ctypes.c_int
+    L.gns_adamw_step.argtypes = [vp, vp, i64, dbl, dbl, dbl, dbl, dbl, vp, vp]
     L.gns_timing_enable.argtypes = [ctypes.c_int]
     L.gns_timing_enable.restype = None
     L.gns_timing_reset.restype = None

@@ -17,7 +17,7 @@ LIB = os.path.join(HERE, "libgns.so")
 # measurement build: every GEMM workgroup records timestamps (GNS_TIMELINE in
 # gns_kernels.hip); read by gram_newton_schulz_amd.timeline
 TIMELINE_LIB = os.path.join(HERE, "libgns_timeline.so")
-SOURCES = ["gns_kernels.hip", "gns_host.cpp", "gns_noalloc.cpp"]
+SOURCES = ["gns_kernels.hip", "gns_tensors.hip", "gns_host.cpp", "gns_tensors.cpp", "gns_noalloc.cpp"]
 ARCH = "gfx950"
 
 

@@ -17,6 +17,7 @@
 
 #include "../../include/gns.h"
 #include "gns_kernels.h"
+#include "gns_timing.h"
 
 namespace {
 
@@ -200,12 +201,8 @@ bool make_plan(int cdt, int64_t batch, int64_t rows, int64_t m, int n_square, in
 // --------------------------------------------------------------------------
 // optional per-launch timing (benchmarking aid)
 // --------------------------------------------------------------------------
-struct TimedLaunch {
-  const char *name;
-  const char *kernel;
-  double flops, bytes;
-  hipEvent_t start, stop;
-};
+using gns::LaunchScope;
+using gns::TimedLaunch;
 std::mutex g_tmu;
 bool g_timing = false;
 std::vector<TimedLaunch> g_launches;
@@ -222,24 +219,24 @@ hipEvent_t pooled_event() {
   return e;
 }
 
-struct LaunchScope {
-  hipStream_t s;
-  TimedLaunch rec{};
-  bool on = false;
-  LaunchScope(hipStream_t st, const char *name, const char *kernel, double flops, double bytes)
-      : s(st) {
-    if (!g_timing) return;
-    rec = TimedLaunch{name, kernel, flops, bytes, pooled_event(), pooled_event()};
-    if (rec.start && rec.stop && hipEventRecord(rec.start, s) == hipSuccess) on = true;
+}  // namespace
+
+gns::LaunchScope::LaunchScope(hipStream_t st, const char *name, const char *kernel, double flops, double bytes)
+    : s(st) {
+  if (!g_timing) return;
+  rec = TimedLaunch{name, kernel, flops, bytes, pooled_event(), pooled_event()};
+  if (rec.start && rec.stop && hipEventRecord(rec.start, s) == hipSuccess) on = true;
+}
+
+void gns::LaunchScope::done() {
+  if (!on) return;
+  if (hipEventRecord(rec.stop, s) == hipSuccess) {
+    std::lock_guard<std::mutex> lk(g_tmu);
+    g_launches.push_back(rec);
   }
-  void done() {
-    if (!on) return;
-    if (hipEventRecord(rec.stop, s) == hipSuccess) {
-      std::lock_guard<std::mutex> lk(g_tmu);
-      g_launches.push_back(rec);
-    }
-  }
-};
+}
+
+namespace {
 
 // --------------------------------------------------------------------------
 // launch helpers

@@ -146,4 +146,63 @@ hipError_t launch_dion3_update(float *W, float *M, const float *O, const int64_t
                                const double *factor, int64_t batch, int64_t n, int64_t m, int64_t k,
                                float decay, double lr, float mu, hipStream_t s);
 
+// --------------------------------------------------------------------------
+// lists of tensors (gns_tensors.hip): norm, clip, AdamW
+// --------------------------------------------------------------------------
+constexpr int kListArrays = 5;
+constexpr int kListUnit = 8;        // elements per unit of work
+
+// One entry of the device table.  Array a holds rows x cols elements, element
+// (r, c) at data[a][r * pitch[a] + c]; an entry whose arrays are all dense has
+// one row.  Its units are pieces of up to kListUnit consecutive elements of
+// one row, numbered row by row, per_row of them to a row.
+struct ListEntry {
+  void *data[kListArrays];
+  int64_t pitch[kListArrays];
+  int64_t cols;
+  int64_t per_row;
+  int64_t units;
+  uint32_t first_chunk, chunks;     // its chunks of the list
+  float lr_scale, wd_scale;
+  uint8_t dtype[kListArrays];
+  uint8_t pad[11];
+};
+static_assert(sizeof(ListEntry) == 136, "table layout");
+
+// Chunk c of the list is units [index * chunk_units, ...) of one entry.
+struct ListChunk {
+  uint32_t entry, index;
+};
+
+// The device table: entries, then chunks.
+struct ListView {
+  const ListEntry *entries;
+  const ListChunk *chunks;
+  int64_t count;
+  int64_t n_chunks;
+  int64_t chunk_units;
+};
+
+// partials[c] of every chunk: its sum of squares of array 0 (fp64), or with
+// `max` the bits of its largest magnitude (as a float's, NaN largest).
+hipError_t launch_list_partials(const ListView &v, bool max, uint64_t *partials, hipStream_t s);
+// result[0] = norm of all chunks times *inv_scale (1 when null), result[1] =
+// clip coefficient; tensor_norms[i] (when not null) of every entry.
+hipError_t launch_list_finish(const ListView &v, bool max, const uint64_t *partials, const float *inv_scale,
+                              double max_norm, double eps, float *result, float *tensor_norms, hipStream_t s);
+// array `dst` <- *factor * array 0, rounded once; nothing when *factor is not
+// finite, or when it is 1 and dst is 0.
+hipError_t launch_list_scale(const ListView &v, int dst, const float *factor, hipStream_t s);
+// AdamW over the entries' arrays {gradient, parameter, first moment, second
+// moment[, copy]}; nothing when grad_scale is given and not finite.
+struct AdamwScalars {
+  double lr, weight_decay;
+  float beta1, one_minus_beta1, beta2, one_minus_beta2;
+  double bias1;          // 1 - beta1^t
+  float inv_sqrt_bias2;  // 1 / sqrt(1 - beta2^t)
+  float eps;
+};
+hipError_t launch_list_adamw(const ListView &v, bool copy, const AdamwScalars &h, const float *grad_scale,
+                             hipStream_t s);
+
 }  // namespace gns

@@ -1,0 +1,237 @@
+"""Lists of tensors: global gradient norm, clipping and AdamW over every
+tensor of a model in a few launches (the C ABI's gns_tensor_list,
+gns_grad_norm, gns_grad_clip and gns_adamw_step).
+
+A :class:`TensorList` names its tensors once and is then passed to the calls,
+which take no per-tensor arguments.  It holds their addresses, so it serves
+while the tensors keep their memory: build it again after anything that
+replaces a ``.grad`` or a parameter.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+import math
+from typing import Optional, Sequence, Union
+
+import torch
+
+
+from .binding import GnsError, _check, _device_tensor, _dtype_code, _ptr, lib
+
+NORM_L2, NORM_MAX = 0, 1
+_NORMS = {2: NORM_L2, math.inf: NORM_MAX}
+
+
+class Tensor(ctypes.Structure):
+    """gns_tensor."""
+    _fields_ = [("data", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("pitch", ctypes.c_int64), ("dtype", ctypes.c_int)]
+
+
+class ListInfo(ctypes.Structure):
+    """gns_tensor_list."""
+    _fields_ = [("arrays", ctypes.c_int), ("count", ctypes.c_int64), ("elements", ctypes.c_int64),
+                ("chunks", ctypes.c_int64), ("chunk_units", ctypes.c_int64), ("table_bytes", ctypes.c_size_t),
+                ("dtypes", ctypes.c_uint * 5), ("bytes", ctypes.c_double * 5), ("overlaps", ctypes.c_uint)]
+
+
+def _rows(group: Sequence[torch.Tensor]):
+    """Common rows x cols form of tensors of one shape: (rows, cols, pitches),
+    or None when their strides have none."""
+    if all(t.is_contiguous() for t in group):
+        n = group[0].numel()
+        return 1, n, [n] * len(group)
+    strides = [t.stride() for t in group]
+    dims = sorted((d for d, size in enumerate(group[0].shape) if size != 1),
+                  key=lambda d: [-s[d] if s[d] else -math.inf for s in strides])   # repeated dimensions outermost
+    merged = []                       # (size, strides), outermost first
+    for d in dims:
+        size, st = group[0].shape[d], [s[d] for s in strides]
+        if merged and all(a == b * size for a, b in zip(merged[-1][1], st)):
+            merged[-1] = (merged[-1][0] * size, st)
+        else:
+            merged.append((size, st))
+    if len(merged) == 1:
+        size, st = merged[0]
+        return (1, size, [size] * len(group)) if all(s == 1 for s in st) else (size, 1, st)
+    if len(merged) == 2 and all(s == 1 for s in merged[1][1]):
+        return merged[0][0], merged[1][0], merged[0][1]
+    return None
+
+
+class TensorList:
+    """Arrays of tensors of the same shapes, ready for the calls on them (see
+    :func:`tensor_list` and :func:`adamw_list`).  Keeps the tensors alive."""
+
+    def __init__(self, arrays: Sequence[Sequence[torch.Tensor]], names: Sequence[str],
+                 lr_scales: Optional[Sequence[float]] = None, wd_scales: Optional[Sequence[float]] = None):
+        if torch.cuda.is_available() and torch.cuda.is_current_stream_capturing():
+            raise GnsError(10, "build the list of tensors before the capture (its table is copied to the GPU)")
+        arrays = [list(a) for a in arrays]
+        count = len(arrays[0])
+        for name, a in zip(names, arrays):
+            if len(a) != count:
+                raise GnsError(2, f"{len(a)} {name}, {count} {names[0]}")
+        for name, scales in (("lr_scales", lr_scales), ("wd_scales", wd_scales)):
+            if scales is not None and len(scales) != count:
+                raise GnsError(2, f"{len(scales)} {name}, {count} {names[0]}")
+        self.arrays, self.tensors, self.device = len(arrays), arrays, None
+        entries = (Tensor * max(1, self.arrays * count))()
+        for i, group in enumerate(zip(*arrays)):
+            for name, t in zip(names, group):
+                if not isinstance(t, torch.Tensor) or t.layout != torch.strided:
+                    raise GnsError(1, f"{name}[{i}] is not a dense tensor: {type(t).__name__}")
+                if t.shape != group[0].shape:
+                    raise GnsError(2, f"{name}[{i}] has shape {tuple(t.shape)}, "
+                                      f"{names[0]}[{i}] has {tuple(group[0].shape)}")
+                _device_tensor(f"{name}[{i}]", t, self.device)
+                self.device = t.device
+            if group[0].numel() == 0:
+                form = 0, 0, [0] * self.arrays
+            else:
+                form = _rows(group)
+            if form is None:
+                raise GnsError(2, f"{names[0]}[{i}]: strides {[t.stride() for t in group]} are not rows of "
+                                  "consecutive elements that are the same for every array")
+            for a, t in enumerate(group):
+                entries[a * count + i] = Tensor(t.data_ptr(), form[0], form[1], form[2][a], _dtype_code(t.dtype))
+        L = lib()
+        nbytes = int(L.gns_tensor_list_bytes(entries, self.arrays, count))
+        self.info = ListInfo()
+        image = torch.empty(max(nbytes, 16), dtype=torch.uint8, pin_memory=self.device is not None)
+        as_floats = [None if s is None else (ctypes.c_float * max(1, count))(*s) for s in (lr_scales, wd_scales)]
+        _check(L.gns_tensor_list_build(entries, self.arrays, count, *as_floats, image.data_ptr(), image.numel(),
+                                       ctypes.byref(self.info)))
+        self.count = count
+        self.workspace_bytes = int(L.gns_tensor_list_workspace_bytes(ctypes.byref(self.info)))
+        self._info = ctypes.byref(self.info)
+        if self.device is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        # the copy runs on the current stream; calls on other streams wait for it
+        self._home = torch.cuda.current_stream(self.device)
+        self.table = image.to(self.device, non_blocking=True)
+        self._ready = torch.cuda.Event()
+        self._ready.record(self._home)
+        self._table = self.table.data_ptr()
+
+    def __len__(self) -> int:
+        return self.count
+
+    def _external(self, raw: int):
+        return torch.cuda.ExternalStream(raw, device=self.device)
+
+    def _on(self, stream) -> int:
+        """The raw stream a call runs on, ordered after the table's copy."""
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        elif isinstance(stream, int):
+            stream = self._external(stream)
+        if stream != self._home:
+            if not torch.cuda.is_current_stream_capturing():
+                stream.wait_event(self._ready)
+            self.table.record_stream(stream)
+        return stream.cuda_stream
+
+
+def tensor_list(grads: Sequence[torch.Tensor], out: Optional[Sequence[torch.Tensor]] = None) -> TensorList:
+    """A list of gradients, and where clipping writes them when ``out`` is
+    given (any mix of fp32, bf16 and fp16 in both).  Strided views are taken
+    where they are rows of consecutive elements."""
+    if out is None:
+        return TensorList([grads], ["grads"])
+    return TensorList([grads, out], ["grads", "out"])
+
+
+def adamw_list(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
+               exp_avgs: Sequence[torch.Tensor], exp_avg_sqs: Sequence[torch.Tensor], *,
+               copies: Optional[Sequence[torch.Tensor]] = None,
+               lr_scales: Optional[Sequence[float]] = None,
+               wd_scales: Optional[Sequence[float]] = None) -> TensorList:
+    """A list for :func:`adamw_step` (and the norm of its gradients): fp32
+    parameters and moments, gradients of any type, and optionally 16-bit
+    ``copies`` that every step refreshes.  ``lr_scales`` and ``wd_scales`` are
+    factors per tensor on the learning rate and the weight decay."""
+    arrays, names = [grads, params, exp_avgs, exp_avg_sqs], ["grads", "params", "exp_avgs", "exp_avg_sqs"]
+    if copies is not None:
+        arrays, names = arrays + [copies], names + ["copies"]
+    return TensorList(arrays, names, lr_scales, wd_scales)
+
+
+class GradNorm:
+    """What a norm or a clipping call leaves on the GPU: ``norm`` and ``clip``
+    (the factor to pass as ``grad_scale``) as float32 scalars, and with
+    ``per_tensor`` every tensor's norm."""
+    __slots__ = ("result", "tensor_norms")
+
+    def __init__(self, result: torch.Tensor, tensor_norms: Optional[torch.Tensor]):
+        self.result, self.tensor_norms = result, tensor_norms
+
+    @property
+    def norm(self) -> torch.Tensor:
+        return self.result[0]
+
+    @property
+    def clip(self) -> torch.Tensor:
+        return self.result[1]
+
+
+def _scalar(name: str, t: Optional[torch.Tensor], device) -> Optional[int]:
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or t.numel() != 1:
+        raise GnsError(3, f"{name} must be one float32 on the GPU")
+    _device_tensor(name, t, device)
+    return t.data_ptr()
+
+
+def _norm_call(fn, grads, max_norm, ord, eps, inv_scale, per_tensor, workspace, stream) -> GradNorm:
+    lst = grads if isinstance(grads, TensorList) else tensor_list(grads)
+    if ord not in _NORMS:
+        raise GnsError(11, f"ord must be 2 or inf, got {ord}")
+    s = lst._on(stream)
+    ws = workspace
+    # allocated for the stream that the call runs on
+    with contextlib.nullcontext() if stream is None else torch.cuda.stream(lst._external(s)):
+        result = torch.empty(2, dtype=torch.float32, device=lst.device)
+        norms = torch.empty(lst.count, dtype=torch.float32, device=lst.device) if per_tensor else None
+        if ws is None:
+            ws = torch.empty(lst.workspace_bytes, dtype=torch.uint8, device=lst.device)
+    _check(fn(lst._info, lst._table, _NORMS[ord], float(max_norm), float(eps),
+              _scalar("inv_scale", inv_scale, lst.device), result.data_ptr(), _ptr(norms),
+              ws.data_ptr(), ws.numel(), s))
+    return GradNorm(result, norms)
+
+
+def grad_norm(grads: Union[TensorList, Sequence[torch.Tensor]], *, ord: float = 2, max_norm: float = math.inf,
+              eps: float = 1e-6, inv_scale: Optional[torch.Tensor] = None, per_tensor: bool = False,
+              workspace: Optional[torch.Tensor] = None, stream=None) -> GradNorm:
+    """Norm of all gradients as one vector (``ord`` 2 or inf, over the
+    gradients times ``inv_scale``) and the factor that unscales them and clips
+    them to ``max_norm`` (gns_grad_norm).  Nothing synchronises: pass the
+    result's ``clip`` to :func:`adamw_step` and ``dion3_step`` as
+    ``grad_scale``, which then clip while they read the gradients.  When a
+    gradient is not finite, ``clip`` is NaN and those steps change nothing."""
+    return _norm_call(lib().gns_grad_norm, grads, max_norm, ord, eps, inv_scale, per_tensor, workspace, stream)
+
+
+def clip_grad_norm_(grads: Union[TensorList, Sequence[torch.Tensor]], max_norm: float, *, ord: float = 2,
+                    eps: float = 1e-6, inv_scale: Optional[torch.Tensor] = None, per_tensor: bool = False,
+                    workspace: Optional[torch.Tensor] = None, stream=None) -> GradNorm:
+    """:func:`grad_norm`, then the gradients times its ``clip``: in place, or
+    into the outputs of a list built with ``out`` (gns_grad_clip).  Gradients
+    whose norm is not finite are left as they are."""
+    return _norm_call(lib().gns_grad_clip, grads, max_norm, ord, eps, inv_scale, per_tensor, workspace, stream)
+
+
+def adamw_step(tensors: TensorList, step: int, *, lr: float, betas: Sequence[float] = (0.9, 0.999),
+               eps: float = 1e-8, weight_decay: float = 0.01, grad_scale: Optional[torch.Tensor] = None,
+               stream=None) -> None:
+    """One AdamW update of every parameter of an :func:`adamw_list`, the
+    ``step``-th (from 1), with decoupled weight decay (gns_adamw_step).
+    ``grad_scale`` (a float32 on the GPU) multiplies the gradients; when it is
+    not finite nothing changes."""
+    s = tensors._on(stream)
+    _check(lib().gns_adamw_step(tensors._info, tensors._table, int(step), float(lr), float(betas[0]),
+                                float(betas[1]), float(eps), float(weight_decay),
+                                _scalar("grad_scale", grad_scale, tensors.device), s))

@@ -368,6 +368,140 @@ gns_status gns_dion3_step(float *W, const void *G, float *M, float *v, int64_t b
                           size_t workspace_bytes, void *stream);
 
 /*
+ * Operators over lists of tensors: the parts of an optimiser step that go over
+ * every tensor of a model, whatever its shape, beside the matrices that the
+ * entry points above update.  A list names its tensors once; the calls on it
+ * take no per-tensor arguments and launch the same few kernels for any number
+ * of tensors, sizes and dtypes.
+ *
+ * A list has `arrays` arrays of `count` entries.  Entry i of every array has
+ * the same rows x cols elements, (r, c) at data[r * pitch + c]; any of them may
+ * be empty (rows or cols 0).  What the arrays are:
+ *   1  {gradient}                                     norm, clipping in place
+ *   2  {gradient, output}                             norm, clipping into output
+ *   4  {gradient, parameter, exp_avg, exp_avg_sq}     norm, clipping, AdamW
+ *   5  the same and {copy}                            (a 16-bit copy of the
+ *                                                     parameter, or fp32)
+ * Gradients, outputs and copies may be GNS_F32, GNS_BF16 or GNS_F16, mixed
+ * freely; parameters and moments are GNS_F32.
+ */
+typedef struct {
+  void *data;     /* (device) element (0, 0); may be NULL when empty; aligned to
+                     the element size, no further                              */
+  int64_t rows, cols;
+  int64_t pitch;  /* elements from one row to the next (0 is allowed: every row
+                     the same memory; such an array is never written)          */
+  gns_dtype dtype;
+} gns_tensor;
+
+#define GNS_LIST_MAX_ARRAYS 5
+
+/* What the calls read of a list on the host (filled by gns_tensor_list_build). */
+typedef struct {
+  int arrays;
+  int64_t count;
+  int64_t elements;      /* over all entries of one array                      */
+  int64_t chunks;        /* pieces of work: about one workgroup each           */
+  int64_t chunk_units;   /* 8-element units per chunk                          */
+  size_t table_bytes;
+  unsigned dtypes[GNS_LIST_MAX_ARRAYS];  /* per array: bit d set when an entry
+                                            has dtype d                        */
+  double bytes[GNS_LIST_MAX_ARRAYS];     /* per array: bytes of its elements   */
+  unsigned overlaps;     /* bit 5 a + b (a <= b): some of array a's memory may
+                            be array b's too (or, a = b, another entry's or
+                            another row's)                                     */
+} gns_tensor_list;
+
+/*
+ * A list is used through its table in device memory.  gns_tensor_list_bytes
+ * gives the table's size (0 for arguments that gns_tensor_list_build refuses);
+ * gns_tensor_list_build writes the table into host memory (`table`,
+ * `table_bytes` of it, 16-byte aligned) and fills *list.  The caller copies it to device memory
+ * (16-byte aligned) and passes that address with every call; the table holds the tensors' addresses,
+ * so it is valid while they stay where they are.  It is only read: any
+ * number of calls, on any streams, may share one.
+ *   tensors      (host) [arrays][count].
+ *   lr_scale, wd_scale (host) [count] factors on the learning rate and on the
+ *                weight decay of every entry (AdamW), or NULL for all ones.
+ * GNS_E_SHAPE (arrays not 1, 2, 4 or 5, count outside 0..2^20, a negative or
+ * overflowing size or pitch, entries of different shape), GNS_E_DTYPE,
+ * GNS_E_NULL, GNS_E_PARAM (a misaligned address, or a scale that is not
+ * finite), GNS_E_WORKSPACE (table_bytes too small).
+ */
+size_t gns_tensor_list_bytes(const gns_tensor *tensors, int arrays, int64_t count);
+gns_status gns_tensor_list_build(const gns_tensor *tensors, int arrays, int64_t count, const float *lr_scale,
+                                 const float *wd_scale, void *table, size_t table_bytes,
+                                 gns_tensor_list *list);
+
+/* Workspace bytes of gns_grad_norm and gns_grad_clip on this list. */
+size_t gns_tensor_list_workspace_bytes(const gns_tensor_list *list);
+
+typedef enum {
+  GNS_NORM_L2 = 0,  /* square root of the sum of squares */
+  GNS_NORM_MAX = 1  /* largest magnitude                 */
+} gns_norm;
+
+/*
+ * Norm of every element of the list's gradients, as of one vector, and the
+ * factor that clips them:
+ *   norm = || s g ||            s = *inv_scale (1 when NULL)
+ *   clip = s min(1, max_norm / (norm + eps))
+ * so that clip * g has the norm min(norm, max_norm) up to eps.  An empty list
+ * has norm 0.
+ *   table        (device) the list's table.
+ *   max_norm     >= 0; INFINITY gives clip = s.
+ *   eps          >= 0.
+ *   inv_scale    (device) one float or NULL: the inverse of the loss scale.
+ *   result       (device) two floats, written: {norm, clip}.  Where a gradient
+ *                is Inf or NaN the norm is (the same as in a sum over them),
+ *                and clip is NaN, which the calls that take it as a factor
+ *                treat as "skip".
+ *   tensor_norms (device) [count] floats, written: every tensor's own norm
+ *                (times s), or NULL.
+ *   workspace    (device) >= gns_tensor_list_workspace_bytes(list) bytes,
+ *                256-byte aligned; clobbered.
+ * Squares and sums are fp64 in a fixed order, so no gradient overflows or
+ * underflows on the way and the result is the same in every run.
+ * GNS_E_NULL, GNS_E_PARAM (max_norm or eps negative or NaN, eps infinite, an
+ * unknown norm), GNS_E_WORKSPACE.
+ */
+gns_status gns_grad_norm(const gns_tensor_list *list, const void *table, gns_norm kind, double max_norm,
+                         double eps, const float *inv_scale, float *result, float *tensor_norms,
+                         void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * gns_grad_norm, then the gradients times clip (fp32 product, rounded once to
+ * the type that is written): in place, or with a list of two arrays into the
+ * output.  In place, clip = 1 writes nothing.  With a norm that is not finite
+ * nothing is written either (the gradients, or the output, keep what they
+ * had).
+ * GNS_E_ALIAS when written memory overlaps other memory of the list.
+ */
+gns_status gns_grad_clip(const gns_tensor_list *list, const void *table, gns_norm kind, double max_norm,
+                         double eps, const float *inv_scale, float *result, float *tensor_norms,
+                         void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * One AdamW update (decoupled weight decay) of every parameter of a list of
+ * four or five arrays: for each element, with t = step and the entry's
+ * eta = lr * lr_scale, wd = weight_decay * wd_scale,
+ *   g <- (*grad_scale) g               (1 when grad_scale is NULL)
+ *   m <- beta1 m + (1 - beta1) g
+ *   v <- beta2 v + (1 - beta2) g^2
+ *   p <- (1 - eta wd) p - eta / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ *   copy <- p                          (rounded to its type; five arrays)
+ * in fp32 arithmetic; the gradients are read only.  grad_scale is a (device)
+ * float such as gns_grad_norm's clip; when it is not finite the update is
+ * skipped: nothing is written.
+ * GNS_E_SHAPE (a list of other arrays), GNS_E_DTYPE (parameters or moments
+ * not fp32), GNS_E_PARAM (step < 1, a hyperparameter that is not finite, betas
+ * outside [0, 1), eps <= 0), GNS_E_NULL, GNS_E_ALIAS.
+ */
+gns_status gns_adamw_step(const gns_tensor_list *list, const void *table, int64_t step, double lr,
+                          double beta1, double beta2, double eps, double weight_decay,
+                          const float *grad_scale, void *stream);
+
+/*
  * Enqueue a check of a row subset: writes to *result (device int32) 0 when
  * every row_idx[b][i] is in [0, n) and the k indices of each matrix are
  * distinct, 1 when an index is out of range, 2 when an index repeats.

@@ -8,3 +8,4 @@ from .newton_schulz import (  # noqa: F401
     composed_poly, spectral_map, polar, dion3_select, dion3_rows, dion3_step, normuon_rows,
     flops_standard, flops_gram, restart_model, restart_sweep,
 )
+from .tensor_ops import adamw, grad_norm  # noqa: F401
