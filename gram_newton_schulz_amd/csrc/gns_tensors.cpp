@@ -26,13 +26,21 @@ using gns::ListView;
 static_assert(kListArrays == GNS_LIST_MAX_ARRAYS, "header and library agree on the arrays");
 
 constexpr int64_t kMaxCount = int64_t(1) << 20;
-constexpr int64_t kMaxElements = int64_t(1) << 48;   // per list: every byte offset fits an int64
+constexpr int64_t kMaxElements = int64_t(1) << 42;   // per list
+constexpr int64_t kMaxSpan = int64_t(1) << 58;       // elements between an entry's first and last: byte
+                                                     // offsets fit an int64
+
+// One workgroup of 256 threads per chunk: a grid holds 2^24 of them.  Pieces
+// of whole chunks are at most 2^42 / 2^23 (dense) or, with one element to a
+// row, 2^42 / 2^20; the rest is at most one short chunk per entry.
+constexpr int64_t kMaxChunks = (int64_t(1) << 24) - 1;
 
 // Units per chunk: about 16384 chunks for a large list, at least 1024 units
-// (8192 elements).
+// (8192 elements), at most 2^20 (so that offsets within a dense chunk fit 32
+// bits).
 int64_t chunk_units_for(int64_t units) {
   int64_t c = 1024;
-  while (c * 16384 < units) c *= 2;
+  while (c * 16384 < units && c < (int64_t(1) << 20)) c *= 2;
   return c;
 }
 
@@ -53,7 +61,7 @@ gns_status entry_shape(const gns_tensor *tensors, int arrays, int64_t count, int
     if (x.rows != t.rows || x.cols != t.cols) return GNS_E_SHAPE;
     if (x.dtype != GNS_F32 && x.dtype != GNS_BF16 && x.dtype != GNS_F16) return GNS_E_DTYPE;
     if (sh->elements == 0) continue;
-    if (x.pitch < 0 || (x.rows > 1 && x.pitch > kMaxElements / x.rows)) return GNS_E_SHAPE;
+    if (x.pitch < 0 || (x.rows > 1 && x.pitch > kMaxSpan / x.rows)) return GNS_E_SHAPE;
     if (!x.data) return GNS_E_NULL;
     if (reinterpret_cast<uintptr_t>(x.data) % gns::dtype_size(x.dtype)) return GNS_E_PARAM;
     if (x.rows > 1 && x.pitch != x.cols) sh->dense = false;
@@ -92,6 +100,7 @@ gns_status list_totals(const gns_tensor *tensors, int arrays, int64_t count, Tot
     entry_shape(tensors, arrays, count, i, &sh);
     tt->chunks += ceil_div(sh.units, tt->chunk_units);
   }
+  if (tt->chunks > kMaxChunks) return GNS_E_SHAPE;
   tt->bytes = sizeof(ListEntry) * count + sizeof(ListChunk) * tt->chunks;
   return GNS_OK;
 }
@@ -156,7 +165,7 @@ ListView view_of(const gns_tensor_list *l, const void *table) {
 
 bool valid_list(const gns_tensor_list *l) {
   return (l->arrays == 1 || l->arrays == 2 || l->arrays == 4 || l->arrays == 5) && l->count >= 0 &&
-         l->count <= kMaxCount && l->chunks >= 0 && l->chunks <= INT32_MAX && l->chunk_units >= 1 &&
+         l->count <= kMaxCount && l->chunks >= 0 && l->chunks <= kMaxChunks && l->chunk_units >= 1 &&
          l->table_bytes == sizeof(ListEntry) * l->count + sizeof(ListChunk) * l->chunks;
 }
 
@@ -220,7 +229,6 @@ gns_status gns_tensor_list_build(const gns_tensor *tensors, int arrays, int64_t 
   for (int64_t i = 0; i < count; ++i)
     if ((lr_scale && !std::isfinite(lr_scale[i])) || (wd_scale && !std::isfinite(wd_scale[i]))) return GNS_E_PARAM;
   if (table_bytes < tt.bytes || (reinterpret_cast<uintptr_t>(table) & 15)) return GNS_E_WORKSPACE;
-  if (tt.chunks > INT32_MAX) return GNS_E_SHAPE;
   gns_tensor_list l{};
   l.arrays = arrays;
   l.count = count;

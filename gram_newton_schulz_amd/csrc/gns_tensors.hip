@@ -6,6 +6,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "gns_elem.h"
 #include "gns_kernels.h"
 
@@ -15,27 +17,132 @@ namespace {
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ float load_elem(const void *p, int64_t i, int dtype) {
-  if (dtype == DT_F32) return static_cast<const float *>(p)[i];
-  const uint16_t h = static_cast<const uint16_t *>(p)[i];
-  return dtype == DT_BF16 ? bf16_to_f32(h) : f16_to_f32(h);
+// V consecutive elements as they lie in memory.  The addresses are aligned to
+// the element only: gfx950 loads and stores 8 and 16 bytes from any address,
+// and a wave's accesses are consecutive, so a misaligned tensor costs one more
+// cache line per wave and instruction, not another path.
+template <int BYTES> struct Raw;
+template <> struct Raw<8> {
+  typedef uint32_t T __attribute__((ext_vector_type(2), aligned(2)));
+  T v[1];
+};
+template <> struct Raw<16> {
+  typedef uint32_t T __attribute__((ext_vector_type(4), aligned(2)));
+  T v[1];
+};
+template <> struct Raw<32> {
+  typedef uint32_t T __attribute__((ext_vector_type(4), aligned(2)));
+  T v[2];
+};
+template <class E, int V> using RawOf = Raw<V * static_cast<int>(sizeof(typename E::S))>;
+
+// A tensor's address comes out of the table, where the compiler does not see
+// that it is global memory: said here, so that these are no flat accesses.
+#define GNS_GLOBAL __attribute__((address_space(1)))
+template <class S> __device__ __forceinline__ S ld_one(const S *p) { return *(const GNS_GLOBAL S *)p; }
+template <class S> __device__ __forceinline__ void st_one(S *p, S v) { *(GNS_GLOBAL S *)p = v; }
+
+template <class E, int V>
+__device__ __forceinline__ RawOf<E, V> ld_raw(const typename E::S *p) {
+  using R = RawOf<E, V>;
+  R r;
+  const GNS_GLOBAL typename R::T *q = (const GNS_GLOBAL typename R::T *)p;
+#pragma unroll
+  for (unsigned i = 0; i < sizeof(R) / sizeof(typename R::T); ++i) r.v[i] = q[i];
+  return r;
+}
+template <class E, int V>
+__device__ __forceinline__ void st_raw(typename E::S *p, const RawOf<E, V> &r) {
+  using R = RawOf<E, V>;
+  GNS_GLOBAL typename R::T *q = (GNS_GLOBAL typename R::T *)p;
+#pragma unroll
+  for (unsigned i = 0; i < sizeof(R) / sizeof(typename R::T); ++i) q[i] = r.v[i];
+}
+template <class R> __device__ __forceinline__ uint32_t word(const R &r, int i) {
+  constexpr int W = sizeof(typename R::T) / 4;
+  return r.v[i / W][i % W];
+}
+template <class E, int V>
+__device__ __forceinline__ void decode(const RawOf<E, V> &r, float (&x)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    if constexpr (E::code == DT_F32) x[i] = __uint_as_float(word(r, i));
+    else x[i] = E::ld(static_cast<uint16_t>(word(r, i / 2) >> (16 * (i & 1))));
+  }
+}
+template <class E, int V>
+__device__ __forceinline__ RawOf<E, V> encode(const float (&x)[V]) {
+  RawOf<E, V> r;
+  constexpr int W = sizeof(typename RawOf<E, V>::T) / 4;
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(r)) / 4; ++i) {
+    if constexpr (E::code == DT_F32) r.v[i / W][i % W] = __float_as_uint(x[i]);
+    else r.v[i / W][i % W] = E::st2(x[2 * i], x[2 * i + 1]);
+  }
+  return r;
 }
 
-__device__ __forceinline__ void store_elem(void *p, int64_t i, int dtype, float v) {
-  if (dtype == DT_F32) static_cast<float *>(p)[i] = v;
-  else static_cast<uint16_t *>(p)[i] = dtype == DT_BF16 ? f32_to_bf16(v) : f32_to_f16(v);
-}
-
-// Calls f(row, column) for every element of chunk c that this thread has.
+// Calls f with a value of the element type that a table names.
 template <class F>
-__device__ __forceinline__ void each_element(const ListEntry &e, uint32_t index, int64_t chunk_units, F f) {
+__device__ __forceinline__ void with_type(int dtype, F f) {
+  if (dtype == DT_BF16) f(EBF16{});
+  else if (dtype == DT_F16) f(EF16{});
+  else f(EF32{});
+}
+
+// A chunk of an entry.  Dense: `n` elements from element `first` of the only
+// row.  Otherwise units [u0, u0 + n_units), found row by row.
+struct Span {
+  int64_t first;
+  int n;
+  bool dense;
+};
+__device__ __forceinline__ Span span_of(const ListEntry &e, uint32_t index, int64_t chunk_units) {
+  Span s;
   const int64_t u0 = static_cast<int64_t>(index) * chunk_units;
-  const int64_t u1 = u0 + chunk_units < e.units ? u0 + chunk_units : e.units;
-  for (int64_t u = u0 + threadIdx.x; u < u1; u += kThreads) {
-    const int64_t row = u / e.per_row;
-    const int64_t c0 = (u - row * e.per_row) * kListUnit;
-    const int64_t c1 = c0 + kListUnit < e.cols ? c0 + kListUnit : e.cols;
-    for (int64_t c = c0; c < c1; ++c) f(row, c);
+  s.dense = e.units == e.per_row;
+  const int64_t left = s.dense ? e.cols - u0 * kListUnit : e.units - u0;
+  const int64_t most = s.dense ? chunk_units * kListUnit : chunk_units;
+  s.first = s.dense ? u0 * kListUnit : u0;
+  s.n = static_cast<int>(left < most ? left : most);
+  return s;
+}
+
+// A dense chunk by this thread: whole(i) takes the V elements from i (called
+// for U pieces at a time by block(i, stride), which can issue all their loads
+// first), and one(i) each element of the last, partial piece.
+template <int V, int U, class Block, class Whole, class One>
+__device__ __forceinline__ void each_dense(int n, Block block, Whole whole, One one) {
+  constexpr int step = kThreads * V;
+  const int end = n / V * V;
+  int i = threadIdx.x * V;
+  for (; i + (U - 1) * step < end; i += U * step) block(i, step);
+  for (; i < end; i += step) whole(i);
+  if (i == end)
+    for (int j = end; j < n; ++j) one(j);
+}
+
+// A chunk of units by this thread: f(row, column, elements of the unit).
+template <class F>
+__device__ __forceinline__ void each_unit(const ListEntry &e, const Span &s, F f) {
+  const int64_t row0 = s.first / e.per_row;
+  const int64_t at0 = s.first - row0 * e.per_row;
+  const bool narrow = e.per_row < (int64_t(1) << 30);   // 32-bit division
+  for (int u = threadIdx.x; u < s.n; u += kThreads) {
+    int64_t r, q;
+    if (narrow) {
+      const uint32_t at = static_cast<uint32_t>(at0) + u;
+      const uint32_t d = at / static_cast<uint32_t>(e.per_row);
+      r = row0 + d;
+      q = at - d * static_cast<uint32_t>(e.per_row);
+    } else {
+      const int64_t d = (at0 + u) / e.per_row;
+      r = row0 + d;
+      q = at0 + u - d * e.per_row;
+    }
+    const int64_t c = q * kListUnit;
+    const int64_t left = e.cols - c;
+    f(r, c, static_cast<int>(left < kListUnit ? left : kListUnit));
   }
 }
 
@@ -64,26 +171,78 @@ __device__ __forceinline__ uint32_t block_max(uint32_t x) {
 // above infinity: an integer maximum keeps a NaN.
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
+// What one thread has of a chunk's norm: a sum of squares, or the largest
+// magnitude.
+template <class E, bool MAX> struct NormPart;
+template <class E> struct NormPart<E, false> {
+  double acc = 0.0, acc2 = 0.0;
+  template <int V> __device__ void add(const RawOf<E, V> &r) {
+    float x[V];
+    decode<E, V>(r, x);
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      acc = fma(static_cast<double>(x[i]), static_cast<double>(x[i]), acc);
+      acc2 = fma(static_cast<double>(x[i + 1]), static_cast<double>(x[i + 1]), acc2);
+    }
+  }
+  __device__ void add_one(typename E::S v) {
+    const double x = E::ld(v);
+    acc = fma(x, x, acc);
+  }
+  __device__ void finish(uint64_t *out) {
+    const double t = block_sum(acc + acc2);
+    if (threadIdx.x == 0) *out = __double_as_longlong(t);
+  }
+};
+template <class E> struct NormPart<E, true> {
+  uint32_t top = 0;
+  template <int V> __device__ void add(const RawOf<E, V> &r) {
+    float x[V];
+    decode<E, V>(r, x);
+#pragma unroll
+    for (int i = 0; i < V; ++i) top = max(top, magnitude(x[i]));
+  }
+  __device__ void add_one(typename E::S v) { top = max(top, magnitude(E::ld(v))); }
+  __device__ void finish(uint64_t *out) {
+    const uint32_t t = block_max(top);
+    if (threadIdx.x == 0) *out = t;
+  }
+};
+
 template <bool MAX>
 __global__ void __launch_bounds__(kThreads) list_partials(ListView v, uint64_t *partials) {
   const ListChunk ch = v.chunks[blockIdx.x];
   const ListEntry &e = v.entries[ch.entry];
-  if constexpr (MAX) {
-    uint32_t top = 0;
-    each_element(e, ch.index, v.chunk_units, [&](int64_t r, int64_t c) {
-      top = max(top, magnitude(load_elem(e.data[0], r * e.pitch[0] + c, e.dtype[0])));
-    });
-    top = block_max(top);
-    if (threadIdx.x == 0) partials[blockIdx.x] = top;
-  } else {
-    double acc = 0.0;
-    each_element(e, ch.index, v.chunk_units, [&](int64_t r, int64_t c) {
-      const double x = load_elem(e.data[0], r * e.pitch[0] + c, e.dtype[0]);
-      acc += x * x;
-    });
-    acc = block_sum(acc);
-    if (threadIdx.x == 0) partials[blockIdx.x] = __double_as_longlong(acc);
-  }
+  const Span s = span_of(e, ch.index, v.chunk_units);
+  with_type(e.dtype[0], [&](auto type) {
+    using E = decltype(type);
+    using S = typename E::S;
+    constexpr int V = 16 / sizeof(S);
+    const S *base = static_cast<const S *>(e.data[0]);
+    NormPart<E, MAX> part;
+    if (s.dense) {
+      const S *p = base + s.first;
+      each_dense<V, kUnroll>(
+          s.n,
+          [&](int i, int step) {
+            RawOf<E, V> r[kUnroll];
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) r[u] = ld_raw<E, V>(p + i + u * step);
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) part.template add<V>(r[u]);
+          },
+          [&](int i) { part.template add<V>(ld_raw<E, V>(p + i)); }, [&](int i) { part.add_one(ld_one(p + i)); });
+    } else {
+      const int64_t pitch = e.pitch[0];
+      each_unit(e, s, [&](int64_t r, int64_t c, int n) {
+        const S *p = base + r * pitch + c;
+        if (n == kListUnit) part.template add<kListUnit>(ld_raw<E, kListUnit>(p));
+        else
+          for (int j = 0; j < n; ++j) part.add_one(ld_one(p + j));
+      });
+    }
+    part.finish(partials + blockIdx.x);
+  });
 }
 
 // Norm of chunks [first, first + n) (thread 0's).
@@ -126,33 +285,151 @@ __global__ void __launch_bounds__(kThreads) list_scale(ListView v, int dst, cons
   if (!isfinite(f) || (dst == 0 && f == 1.0f)) return;
   const ListChunk ch = v.chunks[blockIdx.x];
   const ListEntry &e = v.entries[ch.entry];
-  each_element(e, ch.index, v.chunk_units, [&](int64_t r, int64_t c) {
-    const float x = load_elem(e.data[0], r * e.pitch[0] + c, e.dtype[0]);
-    store_elem(e.data[dst], r * e.pitch[dst] + c, e.dtype[dst], x * f);
+  const Span s = span_of(e, ch.index, v.chunk_units);
+  with_type(e.dtype[0], [&](auto from) {
+    with_type(e.dtype[dst], [&](auto to) {
+      using A = decltype(from);
+      using B = decltype(to);
+      using SA = typename A::S;
+      using SB = typename B::S;
+      constexpr int V = sizeof(SA) == 2 && sizeof(SB) == 2 ? 8 : 4;   // 16 bytes on the wider side
+      const SA *x = static_cast<const SA *>(e.data[0]);
+      SB *y = static_cast<SB *>(e.data[dst]);
+      if (s.dense) {
+        const SA *p = x + s.first;
+        SB *q = y + s.first;
+        auto put = [&](int i, const RawOf<A, V> &r) {
+          float t[V];
+          decode<A, V>(r, t);
+#pragma unroll
+          for (int j = 0; j < V; ++j) t[j] *= f;
+          st_raw<B, V>(q + i, encode<B, V>(t));
+        };
+        each_dense<V, kUnroll>(
+            s.n,
+            [&](int i, int step) {
+              RawOf<A, V> r[kUnroll];
+#pragma unroll
+              for (int u = 0; u < kUnroll; ++u) r[u] = ld_raw<A, V>(p + i + u * step);
+#pragma unroll
+              for (int u = 0; u < kUnroll; ++u) put(i + u * step, r[u]);
+            },
+            [&](int i) { put(i, ld_raw<A, V>(p + i)); }, [&](int i) { st_one(q + i, B::st(A::ld(ld_one(p + i)) * f)); });
+      } else {
+        each_unit(e, s, [&](int64_t r, int64_t c, int n) {
+          const SA *p = x + r * e.pitch[0] + c;
+          SB *q = y + r * e.pitch[dst] + c;
+          if (n == kListUnit) {
+            float t[kListUnit];
+            decode<A, kListUnit>(ld_raw<A, kListUnit>(p), t);
+#pragma unroll
+            for (int j = 0; j < kListUnit; ++j) t[j] *= f;
+            st_raw<B, kListUnit>(q, encode<B, kListUnit>(t));
+          } else {
+            for (int j = 0; j < n; ++j) st_one(q + j, B::st(A::ld(ld_one(p + j)) * f));
+          }
+        });
+      }
+    });
   });
 }
 
-__global__ void __launch_bounds__(kThreads)
-list_adamw(ListView v, bool copy, AdamwScalars h, const float *grad_scale) {
+// One element's update: m and v in place, the parameter returned.
+struct AdamwRule {
+  float f, beta1, one_minus_beta1, beta2, one_minus_beta2, inv_sqrt_bias2, eps, decay, rate;
+  __device__ float operator()(float p, float g, float &m, float &v) const {
+    g *= f;
+    m = fmaf(beta1, m, one_minus_beta1 * g);
+    v = fmaf(beta2, v, one_minus_beta2 * (g * g));
+    return fmaf(-rate, m / fmaf(sqrtf(v), inv_sqrt_bias2, eps), decay * p);
+  }
+};
+
+template <bool COPY>
+__global__ void __launch_bounds__(kThreads) list_adamw(ListView v, AdamwScalars h, const float *grad_scale) {
   const float f = grad_scale ? *grad_scale : 1.0f;
   if (!isfinite(f)) return;
   const ListChunk ch = v.chunks[blockIdx.x];
   const ListEntry &e = v.entries[ch.entry];
+  const Span s = span_of(e, ch.index, v.chunk_units);
   const double eta = h.lr * e.lr_scale;
-  const float decay = static_cast<float>(1.0 - eta * (h.weight_decay * e.wd_scale));
-  const float rate = static_cast<float>(eta / h.bias1);
-  each_element(e, ch.index, v.chunk_units, [&](int64_t r, int64_t c) {
-    const float g = f * load_elem(e.data[0], r * e.pitch[0] + c, e.dtype[0]);
-    float *p = static_cast<float *>(e.data[1]) + r * e.pitch[1] + c;
-    float *m = static_cast<float *>(e.data[2]) + r * e.pitch[2] + c;
-    float *s = static_cast<float *>(e.data[3]) + r * e.pitch[3] + c;
-    const float m1 = fmaf(h.beta1, *m, h.one_minus_beta1 * g);
-    const float s1 = fmaf(h.beta2, *s, h.one_minus_beta2 * (g * g));
-    const float p1 = fmaf(-rate, m1 / fmaf(sqrtf(s1), h.inv_sqrt_bias2, h.eps), decay * *p);
-    *m = m1;
-    *s = s1;
-    *p = p1;
-    if (copy) store_elem(e.data[4], r * e.pitch[4] + c, e.dtype[4], p1);
+  const AdamwRule rule{f, h.beta1, h.one_minus_beta1, h.beta2, h.one_minus_beta2, h.inv_sqrt_bias2, h.eps,
+                       static_cast<float>(1.0 - eta * (h.weight_decay * e.wd_scale)),
+                       static_cast<float>(eta / h.bias1)};
+  float *P = static_cast<float *>(e.data[1]), *M = static_cast<float *>(e.data[2]),
+        *Q = static_cast<float *>(e.data[3]);
+  auto body = [&](auto grad, auto copy) {
+    using G = decltype(grad);
+    using C = decltype(copy);
+    const typename G::S *g = static_cast<const typename G::S *>(e.data[0]);
+    typename C::S *w = static_cast<typename C::S *>(e.data[4]);
+    auto update = [&](auto width, const auto &rp, const auto &rg, const auto &rm, const auto &rq, int64_t ip,
+                      int64_t im, int64_t iq, int64_t iw) {
+      constexpr int V = decltype(width)::value;
+      float p[V], x[V], m[V], q[V];
+      decode<EF32, V>(rp, p);
+      decode<G, V>(rg, x);
+      decode<EF32, V>(rm, m);
+      decode<EF32, V>(rq, q);
+#pragma unroll
+      for (int j = 0; j < V; ++j) p[j] = rule(p[j], x[j], m[j], q[j]);
+      st_raw<EF32, V>(P + ip, encode<EF32, V>(p));
+      st_raw<EF32, V>(M + im, encode<EF32, V>(m));
+      st_raw<EF32, V>(Q + iq, encode<EF32, V>(q));
+      if constexpr (COPY) st_raw<C, V>(w + iw, encode<C, V>(p));
+    };
+    auto one = [&](int64_t ig, int64_t ip, int64_t im, int64_t iq, int64_t iw) {
+      float m = ld_one(M + im), q = ld_one(Q + iq);
+      const float p = rule(ld_one(P + ip), G::ld(ld_one(g + ig)), m, q);
+      st_one(P + ip, p);
+      st_one(M + im, m);
+      st_one(Q + iq, q);
+      if constexpr (COPY) st_one(w + iw, C::st(p));
+    };
+    if (s.dense) {
+      constexpr int V = 4, U = 2;
+      auto whole = [&](int i) {
+        const int64_t at = s.first + i;
+        update(std::integral_constant<int, V>{}, ld_raw<EF32, V>(P + at), ld_raw<G, V>(g + at),
+               ld_raw<EF32, V>(M + at), ld_raw<EF32, V>(Q + at), at, at, at, at);
+      };
+      each_dense<V, U>(
+          s.n,
+          [&](int i, int step) {
+            RawOf<EF32, V> rp[U], rm[U], rq[U];
+            RawOf<G, V> rg[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              const int64_t at = s.first + i + u * step;
+              rp[u] = ld_raw<EF32, V>(P + at);
+              rg[u] = ld_raw<G, V>(g + at);
+              rm[u] = ld_raw<EF32, V>(M + at);
+              rq[u] = ld_raw<EF32, V>(Q + at);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              const int64_t at = s.first + i + u * step;
+              update(std::integral_constant<int, V>{}, rp[u], rg[u], rm[u], rq[u], at, at, at, at);
+            }
+          },
+          whole, [&](int i) { one(s.first + i, s.first + i, s.first + i, s.first + i, s.first + i); });
+    } else {
+      each_unit(e, s, [&](int64_t r, int64_t c, int n) {
+        const int64_t ig = r * e.pitch[0] + c, ip = r * e.pitch[1] + c, im = r * e.pitch[2] + c,
+                      iq = r * e.pitch[3] + c, iw = r * e.pitch[4] + c;
+        if (n == kListUnit) {
+          constexpr int V = kListUnit;
+          update(std::integral_constant<int, V>{}, ld_raw<EF32, V>(P + ip), ld_raw<G, V>(g + ig),
+                 ld_raw<EF32, V>(M + im), ld_raw<EF32, V>(Q + iq), ip, im, iq, iw);
+        } else {
+          for (int j = 0; j < n; ++j) one(ig + j, ip + j, im + j, iq + j, iw + j);
+        }
+      });
+    }
+  };
+  with_type(e.dtype[0], [&](auto grad) {
+    if constexpr (COPY) with_type(e.dtype[4], [&](auto copy) { body(grad, copy); });
+    else body(grad, EF32{});
   });
 }
 
@@ -183,7 +460,9 @@ hipError_t launch_list_scale(const ListView &v, int dst, const float *factor, hi
 hipError_t launch_list_adamw(const ListView &v, bool copy, const AdamwScalars &h, const float *grad_scale,
                              hipStream_t s) {
   if (v.n_chunks == 0) return hipSuccess;
-  list_adamw<<<dim3(static_cast<unsigned>(v.n_chunks)), kThreads, 0, s>>>(v, copy, h, grad_scale);
+  const dim3 grid(static_cast<unsigned>(v.n_chunks));
+  if (copy) list_adamw<true><<<grid, kThreads, 0, s>>>(v, h, grad_scale);
+  else list_adamw<false><<<grid, kThreads, 0, s>>>(v, h, grad_scale);
   return hipGetLastError();
 }
 
