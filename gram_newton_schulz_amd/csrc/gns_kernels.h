@@ -181,18 +181,26 @@ struct ListView {
   int64_t count;
   int64_t n_chunks;
   int64_t chunk_units;
+  int64_t keep_from;   // chunks from here on: what a pass leaves in the last-level cache
 };
 
-// partials[c] of every chunk: its sum of squares of array 0 (fp64), or with
-// `max` the bits of its largest magnitude (as a float's, NaN largest).
-hipError_t launch_list_partials(const ListView &v, bool max, uint64_t *partials, hipStream_t s);
-// result[0] = norm of all chunks times *inv_scale (1 when null), result[1] =
-// clip coefficient; tensor_norms[i] (when not null) of every entry.
-hipError_t launch_list_finish(const ListView &v, bool max, const uint64_t *partials, const float *inv_scale,
-                              double max_norm, double eps, float *result, float *tensor_norms, hipStream_t s);
-// array `dst` <- *factor * array 0, rounded once; nothing when *factor is not
-// finite, or when it is 1 and dst is 0.
-hipError_t launch_list_scale(const ListView &v, int dst, const float *factor, hipStream_t s);
+// What a norm writes: result[0] = norm of array 0 times *inv_scale (1 when
+// null), result[1] = its clip factor.
+struct NormArgs {
+  const float *inv_scale;
+  double max_norm, eps;
+  float *result;
+};
+// The norm (with `max` the largest magnitude), and every entry's own in
+// tensor_norms unless that is null.  partials: one per chunk, the sum of
+// squares (fp64) or the bits of the largest magnitude (as a float's, NaN
+// largest); *arrived is zero before and after.
+hipError_t launch_list_norm(const ListView &v, bool max, uint64_t *partials, uint32_t *arrived, const NormArgs &a,
+                            float *tensor_norms, hipStream_t s);
+// The norm, then array dst <- clip factor * array 0, rounded once; nothing
+// when the factor is not finite, or when it is 1 and dst is 0.
+hipError_t launch_list_clip(const ListView &v, int dst, bool max, uint64_t *partials, uint32_t *arrived,
+                            const NormArgs &a, float *tensor_norms, hipStream_t s);
 // AdamW over the entries' arrays {gradient, parameter, first moment, second
 // moment[, copy]}; nothing when grad_scale is given and not finite.
 struct AdamwScalars {

@@ -27,6 +27,8 @@ static_assert(kListArrays == GNS_LIST_MAX_ARRAYS, "header and library agree on t
 
 constexpr int64_t kMaxCount = int64_t(1) << 20;
 constexpr int64_t kMaxElements = int64_t(1) << 42;   // per list
+constexpr size_t kArrivedBytes = 256;   // of the workspace: the count of finished chunks
+constexpr double kLastLevelCache = 256.0 * (1 << 20);
 constexpr int64_t kMaxSpan = int64_t(1) << 58;       // elements between an entry's first and last: byte
                                                      // offsets fit an int64
 
@@ -153,6 +155,20 @@ unsigned find_overlaps(const gns_tensor *tensors, int arrays, int64_t count) {
   return bits;
 }
 
+// How many of the list's last chunks hold kLastLevelCache bytes of array 0.
+int64_t chunks_at_end(const gns_tensor *grads, int64_t count, const ListEntry *entries, int64_t chunk_units) {
+  double room = kLastLevelCache;
+  int64_t n = 0;
+  for (int64_t i = count; i-- > 0;) {
+    const double each = static_cast<double>(chunk_units) * kListUnit * gns::dtype_size(grads[i].dtype);
+    const int64_t fit = std::min<int64_t>(entries[i].chunks, static_cast<int64_t>(room / each));
+    n += fit;
+    if (fit < entries[i].chunks) break;
+    room -= std::min(room, static_cast<double>(grads[i].rows) * grads[i].cols * gns::dtype_size(grads[i].dtype));
+  }
+  return n;
+}
+
 ListView view_of(const gns_tensor_list *l, const void *table) {
   ListView v;
   v.entries = static_cast<const ListEntry *>(table);
@@ -160,12 +176,14 @@ ListView view_of(const gns_tensor_list *l, const void *table) {
   v.count = l->count;
   v.n_chunks = l->chunks;
   v.chunk_units = l->chunk_units;
+  v.keep_from = l->keep_from;
   return v;
 }
 
 bool valid_list(const gns_tensor_list *l) {
   return (l->arrays == 1 || l->arrays == 2 || l->arrays == 4 || l->arrays == 5) && l->count >= 0 &&
          l->count <= kMaxCount && l->chunks >= 0 && l->chunks <= kMaxChunks && l->chunk_units >= 1 &&
+         l->keep_from >= 0 && l->keep_from <= l->chunks &&
          l->table_bytes == sizeof(ListEntry) * l->count + sizeof(ListChunk) * l->chunks;
 }
 
@@ -187,27 +205,17 @@ gns_status norm_and_clip(const gns_tensor_list *list, const void *table, gns_nor
   const int dst = list->arrays == 2 ? 1 : 0;
   if (clip && (overlap(list, dst, dst) || (dst && overlap(list, 0, dst)))) return GNS_E_ALIAS;
   const ListView v = view_of(list, table);
-  uint64_t *partials = static_cast<uint64_t *>(workspace);
-  const bool max = kind == GNS_NORM_MAX;
+  uint32_t *arrived = static_cast<uint32_t *>(workspace);
+  uint64_t *partials = reinterpret_cast<uint64_t *>(static_cast<unsigned char *>(workspace) + kArrivedBytes);
   const double n = static_cast<double>(list->elements);
-  {
-    LaunchScope ls(s, "grad_norm", "list_partials", 2.0 * n, list->bytes[0]);
-    const hipError_t e = gns::launch_list_partials(v, max, partials, s);
-    ls.done();
-    if (e != hipSuccess) return GNS_E_HIP;
-  }
-  {
-    LaunchScope ls(s, "grad_norm", "list_finish", static_cast<double>(list->chunks), 8.0 * list->chunks);
-    const hipError_t e = gns::launch_list_finish(v, max, partials, inv_scale, max_norm, eps, result, tensor_norms, s);
-    ls.done();
-    if (e != hipSuccess) return GNS_E_HIP;
-  }
-  if (clip) {
-    LaunchScope ls(s, "grad_clip", "list_scale", n, list->bytes[0] + list->bytes[dst]);
-    const hipError_t e = gns::launch_list_scale(v, dst, result + 1, s);
-    ls.done();
-    if (e != hipSuccess) return GNS_E_HIP;
-  }
+  const bool max = kind == GNS_NORM_MAX;
+  const gns::NormArgs args{inv_scale, max_norm, eps, result};
+  LaunchScope ls(s, clip ? "grad_clip" : "grad_norm", clip ? "list_partials+list_scale" : "list_partials",
+                 (clip ? 3.0 : 2.0) * n, list->bytes[0] * (clip ? 2.0 : 1.0) + (clip ? list->bytes[dst] : 0.0));
+  const hipError_t e = clip ? gns::launch_list_clip(v, dst, max, partials, arrived, args, tensor_norms, s)
+                            : gns::launch_list_norm(v, max, partials, arrived, args, tensor_norms, s);
+  ls.done();
+  if (e != hipSuccess) return GNS_E_HIP;
   return GNS_OK;
 }
 
@@ -267,12 +275,13 @@ gns_status gns_tensor_list_build(const gns_tensor *tensors, int arrays, int64_t 
     for (uint32_t c = 0; c < e.chunks; ++c) chunks[at + c] = ListChunk{static_cast<uint32_t>(i), c};
     at += e.chunks;
   }
+  l.keep_from = l.chunks - chunks_at_end(tensors, count, entries, tt.chunk_units);
   *list = l;
   return GNS_OK;
 }
 
 size_t gns_tensor_list_workspace_bytes(const gns_tensor_list *list) {
-  return list && valid_list(list) ? sizeof(uint64_t) * std::max<int64_t>(list->chunks, 1) : 0;
+  return list && valid_list(list) ? kArrivedBytes + sizeof(uint64_t) * list->chunks : 0;
 }
 
 gns_status gns_grad_norm(const gns_tensor_list *list, const void *table, gns_norm kind, double max_norm,

@@ -17,6 +17,19 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// Norms of up to this many chunks are one launch: the workgroup that ends last
+// adds the partials up.  Counting the workgroups costs an atomic and its
+// fences in each, which line up on one address: 24 tensors of 1024 elements
+// 12.8 -> 9.4 us per call, 512 chunks no different, 1024 chunks 4 us more and
+// 16384 chunks 800 us more than a second launch of one workgroup.
+constexpr int64_t kFinishChunks = 128;
+
+// Up to this many partials are added up by every workgroup of the scaling
+// itself, which saves the launch between: 3 x 513x777 13.9 -> 11.5 us per
+// call, 8 x 512x4096 bf16 (2048 chunks) 18.9 -> 17.5; with 16384 chunks it
+// costs 82 us.
+constexpr int64_t kScaleChunks = 4096;
+
 // V consecutive elements as they lie in memory.  The addresses are aligned to
 // the element only: gfx950 loads and stores 8 and 16 bytes from any address,
 // and a wave's accesses are consecutive, so a misaligned tensor costs one more
@@ -42,21 +55,23 @@ template <class E, int V> using RawOf = Raw<V * static_cast<int>(sizeof(typename
 template <class S> __device__ __forceinline__ S ld_one(const S *p) { return *(const GNS_GLOBAL S *)p; }
 template <class S> __device__ __forceinline__ void st_one(S *p, S v) { *(GNS_GLOBAL S *)p = v; }
 
-template <class E, int V>
+// NT: with the streaming hint, for data that this pass is the last to want.
+template <class E, int V, bool NT>
 __device__ __forceinline__ RawOf<E, V> ld_raw(const typename E::S *p) {
   using R = RawOf<E, V>;
   R r;
   const GNS_GLOBAL typename R::T *q = (const GNS_GLOBAL typename R::T *)p;
 #pragma unroll
-  for (unsigned i = 0; i < sizeof(R) / sizeof(typename R::T); ++i) r.v[i] = q[i];
+  for (unsigned i = 0; i < sizeof(R) / sizeof(typename R::T); ++i) r.v[i] = NT ? __builtin_nontemporal_load(q + i) : q[i];
   return r;
 }
-template <class E, int V>
+template <class E, int V, bool NT>
 __device__ __forceinline__ void st_raw(typename E::S *p, const RawOf<E, V> &r) {
   using R = RawOf<E, V>;
   GNS_GLOBAL typename R::T *q = (GNS_GLOBAL typename R::T *)p;
 #pragma unroll
-  for (unsigned i = 0; i < sizeof(R) / sizeof(typename R::T); ++i) q[i] = r.v[i];
+  for (unsigned i = 0; i < sizeof(R) / sizeof(typename R::T); ++i) if constexpr (NT) __builtin_nontemporal_store(r.v[i], q + i);
+    else q[i] = r.v[i];
 }
 template <class R> __device__ __forceinline__ uint32_t word(const R &r, int i) {
   constexpr int W = sizeof(typename R::T) / 4;
@@ -91,35 +106,54 @@ __device__ __forceinline__ void with_type(int dtype, F f) {
 }
 
 // A chunk of an entry.  Dense: `n` elements from element `first` of the only
-// row.  Otherwise units [u0, u0 + n_units), found row by row.
+// row.  Otherwise units [first, first + n), found row by row.
+//
+// Dense chunks are shifted so that array `a` is whole cache lines from element
+// `head` of the chunk on (head > 0 in an entry's first chunk only): tensors
+// packed behind one another start anywhere, and stores that end inside a line
+// leave partial lines behind (AdamW of 200 packed tensors, 8.9M elements:
+// 65.6 -> 63 us).  Arrays of another phase are accessed across lines.
+constexpr int kLine = 128;
 struct Span {
   int64_t first;
-  int n;
+  int n, head;
   bool dense;
 };
-__device__ __forceinline__ Span span_of(const ListEntry &e, uint32_t index, int64_t chunk_units) {
+__device__ __forceinline__ Span span_of(const ListEntry &e, uint32_t index, int64_t chunk_units, int a) {
   Span s;
   const int64_t u0 = static_cast<int64_t>(index) * chunk_units;
   s.dense = e.units == e.per_row;
-  const int64_t left = s.dense ? e.cols - u0 * kListUnit : e.units - u0;
-  const int64_t most = s.dense ? chunk_units * kListUnit : chunk_units;
-  s.first = s.dense ? u0 * kListUnit : u0;
-  s.n = static_cast<int>(left < most ? left : most);
+  s.head = 0;
+  if (s.dense) {
+    const uint32_t size = e.dtype[a] == DT_F32 ? 4 : 2;
+    const int shift = static_cast<int>((0u - static_cast<uint32_t>(reinterpret_cast<uintptr_t>(e.data[a]))) %
+                                       kLine / size);
+    const int64_t end = (u0 + chunk_units) * kListUnit + shift;
+    s.first = index ? u0 * kListUnit + shift : 0;
+    s.n = static_cast<int>((end < e.cols ? end : e.cols) - s.first);
+    if (s.n < 0) s.n = 0;
+    if (!index) s.head = shift < s.n ? shift : s.n;
+  } else {
+    s.first = u0;
+    const int64_t left = e.units - u0;
+    s.n = static_cast<int>(left < chunk_units ? left : chunk_units);
+  }
   return s;
 }
 
-// A dense chunk by this thread: whole(i) takes the V elements from i (called
-// for U pieces at a time by block(i, stride), which can issue all their loads
-// first), and one(i) each element of the last, partial piece.
+// A dense chunk by this thread: block(i, stride) takes U pieces of V elements
+// (it can issue all their loads first), whole(i) one piece, and one(i) one
+// element, at the two ends.
 template <int V, int U, class Block, class Whole, class One>
-__device__ __forceinline__ void each_dense(int n, Block block, Whole whole, One one) {
+__device__ __forceinline__ void each_dense(const Span &s, Block block, Whole whole, One one) {
   constexpr int step = kThreads * V;
-  const int end = n / V * V;
-  int i = threadIdx.x * V;
+  const int end = s.head + (s.n - s.head) / V * V;
+  int i = s.head + threadIdx.x * V;
   for (; i + (U - 1) * step < end; i += U * step) block(i, step);
   for (; i < end; i += step) whole(i);
-  if (i == end)
-    for (int j = end; j < n; ++j) one(j);
+  const int t = threadIdx.x;
+  if (t < s.head) one(t);
+  if (t < s.n - end) one(end + t);
 }
 
 // A chunk of units by this thread: f(row, column, elements of the unit).
@@ -171,6 +205,12 @@ __device__ __forceinline__ uint32_t block_max(uint32_t x) {
 // above infinity: an integer maximum keeps a NaN.
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
+// A partial is stored where the workgroup that adds them up sees it, on
+// whichever XCD it runs.
+__device__ __forceinline__ void put_partial(uint64_t *out, uint64_t bits) {
+  __hip_atomic_store(out, bits, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
 // What one thread has of a chunk's norm: a sum of squares, or the largest
 // magnitude.
 template <class E, bool MAX> struct NormPart;
@@ -191,7 +231,7 @@ template <class E> struct NormPart<E, false> {
   }
   __device__ void finish(uint64_t *out) {
     const double t = block_sum(acc + acc2);
-    if (threadIdx.x == 0) *out = __double_as_longlong(t);
+    if (threadIdx.x == 0) put_partial(out, __double_as_longlong(t));
   }
 };
 template <class E> struct NormPart<E, true> {
@@ -205,87 +245,175 @@ template <class E> struct NormPart<E, true> {
   __device__ void add_one(typename E::S v) { top = max(top, magnitude(E::ld(v))); }
   __device__ void finish(uint64_t *out) {
     const uint32_t t = block_max(top);
-    if (threadIdx.x == 0) *out = t;
+    if (threadIdx.x == 0) put_partial(out, t);
   }
 };
 
+// Total over `n` partials by the `threads` threads of which this is number
+// `t`, before the reduction over them.
 template <bool MAX>
-__global__ void __launch_bounds__(kThreads) list_partials(ListView v, uint64_t *partials) {
+__device__ __forceinline__ void add_partials(const uint64_t *p, int64_t n, int t, int threads, double &acc,
+                                             uint32_t &top) {
+  constexpr int kAtOnce = 8;   // loads in flight per thread
+  for (int64_t i = t; i < n; i += kAtOnce * threads) {
+    uint64_t x[kAtOnce];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int64_t at = i + u * threads;
+      // from where every XCD sees it, whichever wrote it
+      x[u] = at < n ? __hip_atomic_load(p + at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      if constexpr (MAX) top = max(top, static_cast<uint32_t>(x[u]));
+      else acc += __longlong_as_double(x[u]);
+    }
+  }
+}
+
+// Norm of all `n` partials (thread 0's), by the whole workgroup.
+template <bool MAX>
+__device__ __forceinline__ double norm_of(const uint64_t *partials, int64_t n) {
+  double acc = 0.0;
+  uint32_t top = 0;
+  add_partials<MAX>(partials, n, threadIdx.x, blockDim.x, acc, top);
+  if constexpr (MAX) return __uint_as_float(block_max(top));
+  else return sqrt(block_sum(acc));
+}
+
+// The result's {norm, clip factor} from the norm of the stored gradients.
+__device__ __forceinline__ float2 result_of(const NormArgs &a, double raw) {
+  const double s = a.inv_scale ? static_cast<double>(*a.inv_scale) : 1.0;
+  const double norm = raw * s;
+  const double ratio = a.max_norm / (norm + a.eps);
+  return make_float2(static_cast<float>(norm),
+                     isfinite(norm) ? static_cast<float>(s * (ratio < 1.0 ? ratio : 1.0)) : __builtin_nanf(""));
+}
+__device__ __forceinline__ void write_result(const NormArgs &a, double raw) {
+  const float2 r = result_of(a, raw);
+  a.result[0] = r.x;
+  a.result[1] = r.y;
+}
+
+// partials[c] of every chunk c.  With FINISH the workgroup that stores the
+// last of them adds them up, in the order of the chunks, and writes the
+// result; it leaves *arrived at zero, as it found it.
+template <bool MAX, bool FINISH>
+__global__ void __launch_bounds__(kThreads)
+list_partials(ListView v, uint64_t *partials, uint32_t *arrived, NormArgs args) {
   const ListChunk ch = v.chunks[blockIdx.x];
   const ListEntry &e = v.entries[ch.entry];
-  const Span s = span_of(e, ch.index, v.chunk_units);
+  const Span s = span_of(e, ch.index, v.chunk_units, 0);
   with_type(e.dtype[0], [&](auto type) {
     using E = decltype(type);
     using S = typename E::S;
     constexpr int V = 16 / sizeof(S);
     const S *base = static_cast<const S *>(e.data[0]);
     NormPart<E, MAX> part;
-    if (s.dense) {
+    // Loads with the streaming hint run at 7.0 TB/s against 6.0, but leave
+    // nothing in the last-level cache for the pass that takes the gradients
+    // next.  So the chunks that fill the cache are read without it: AdamW after
+    // the norm of 67M fp32 gradients 383 -> 343 us for both, clipping 268M
+    // fp32 gradients 528 -> 516, and a norm alone pays for it with 4 of
+    // 164 us (8 x 4096x16384 bf16).
+    auto dense = [&](auto once) {
+      constexpr bool ONCE = decltype(once)::value;
       const S *p = base + s.first;
       each_dense<V, kUnroll>(
-          s.n,
+          s,
           [&](int i, int step) {
             RawOf<E, V> r[kUnroll];
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) r[u] = ld_raw<E, V>(p + i + u * step);
+            for (int u = 0; u < kUnroll; ++u) r[u] = ld_raw<E, V, ONCE>(p + i + u * step);
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) part.template add<V>(r[u]);
           },
-          [&](int i) { part.template add<V>(ld_raw<E, V>(p + i)); }, [&](int i) { part.add_one(ld_one(p + i)); });
-    } else {
+          [&](int i) { part.template add<V>(ld_raw<E, V, ONCE>(p + i)); }, [&](int i) { part.add_one(ld_one(p + i)); });
+    };
+    if (s.dense && blockIdx.x < v.keep_from) dense(std::true_type{});
+    else if (s.dense) dense(std::false_type{});
+    else {
       const int64_t pitch = e.pitch[0];
       each_unit(e, s, [&](int64_t r, int64_t c, int n) {
         const S *p = base + r * pitch + c;
-        if (n == kListUnit) part.template add<kListUnit>(ld_raw<E, kListUnit>(p));
+        if (n == kListUnit) part.template add<kListUnit>(ld_raw<E, kListUnit, false>(p));
         else
           for (int j = 0; j < n; ++j) part.add_one(ld_one(p + j));
       });
     }
     part.finish(partials + blockIdx.x);
   });
-}
-
-// Norm of chunks [first, first + n) (thread 0's).
-template <bool MAX>
-__device__ __forceinline__ double norm_of(const uint64_t *partials, int64_t first, int64_t n) {
-  if constexpr (MAX) {
-    uint32_t top = 0;
-    for (int64_t i = threadIdx.x; i < n; i += blockDim.x) top = max(top, static_cast<uint32_t>(partials[first + i]));
-    return __uint_as_float(block_max(top));
-  } else {
-    double acc = 0.0;
-    for (int64_t i = threadIdx.x; i < n; i += blockDim.x) acc += __longlong_as_double(partials[first + i]);
-    return sqrt(block_sum(acc));
-  }
-}
-
-// Block 0: the norm of everything and the clip factor; block 1 + i: entry i's.
-template <bool MAX>
-__global__ void __launch_bounds__(kThreads)
-list_finish(ListView v, const uint64_t *partials, const float *inv_scale, double max_norm, double eps,
-            float *result, float *tensor_norms) {
-  const double s = inv_scale ? static_cast<double>(*inv_scale) : 1.0;
-  if (blockIdx.x == 0) {
-    const double norm = norm_of<MAX>(partials, 0, v.n_chunks) * s;
+  if constexpr (FINISH) {
+    __shared__ bool last;
+    if (threadIdx.x == 0)
+      last = __hip_atomic_fetch_add(arrived, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+    __syncthreads();
+    if (!last) return;
+    const double norm = norm_of<MAX>(partials, v.n_chunks);
     if (threadIdx.x == 0) {
-      const float n32 = static_cast<float>(norm);
-      const double ratio = max_norm / (norm + eps);
-      result[0] = n32;
-      result[1] = isfinite(norm) ? static_cast<float>(s * (ratio < 1.0 ? ratio : 1.0)) : __builtin_nanf("");
+      write_result(args, norm);
+      __hip_atomic_store(arrived, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-  } else {
-    const ListEntry &e = v.entries[blockIdx.x - 1];
-    const double norm = norm_of<MAX>(partials, e.first_chunk, e.chunks) * s;
-    if (threadIdx.x == 0) tensor_norms[blockIdx.x - 1] = static_cast<float>(norm);
   }
 }
 
-__global__ void __launch_bounds__(kThreads) list_scale(ListView v, int dst, const float *factor) {
-  const float f = *factor;
+// The second launch of a norm: block 0 writes the result; the others write
+// the entries' own norms, a block or (per_wave) a wave to each.
+template <bool MAX>
+__global__ void __launch_bounds__(1024)
+list_finish(ListView v, const uint64_t *partials, NormArgs args, float *tensor_norms, bool per_wave) {
+  if (blockIdx.x == 0) {
+    const double norm = norm_of<MAX>(partials, v.n_chunks);
+    if (threadIdx.x == 0) write_result(args, norm);
+    return;
+  }
+  const double s = args.inv_scale ? static_cast<double>(*args.inv_scale) : 1.0;
+  if (!per_wave) {
+    const ListEntry &e = v.entries[blockIdx.x - 1];
+    const double norm = norm_of<MAX>(partials + e.first_chunk, e.chunks) * s;
+    if (threadIdx.x == 0) tensor_norms[blockIdx.x - 1] = static_cast<float>(norm);
+    return;
+  }
+  const int64_t i = (blockIdx.x - 1) * static_cast<int64_t>(blockDim.x / 64) + threadIdx.x / 64;
+  if (i >= v.count) return;
+  const ListEntry &e = v.entries[i];
+  double acc = 0.0;
+  uint32_t top = 0;
+  add_partials<MAX>(partials + e.first_chunk, e.chunks, threadIdx.x & 63, 64, acc, top);
+  for (int off = 32; off > 0; off >>= 1) {
+    acc += __shfl_down(acc, off, 64);
+    top = max(top, static_cast<uint32_t>(__shfl_down(top, off, 64)));
+  }
+  if ((threadIdx.x & 63) == 0)
+    tensor_norms[i] = static_cast<float>((MAX ? static_cast<double>(__uint_as_float(top)) : sqrt(acc)) * s);
+}
+
+// Array dst <- factor * array 0.  The factor is the result's, or with
+// PARTIALS every workgroup's own sum of the partials (all in the same order,
+// so all the same), of which the first writes the result.
+template <bool PARTIALS, bool MAX>
+__global__ void __launch_bounds__(kThreads)
+list_scale(ListView v, int dst, const uint64_t *partials, NormArgs args) {
+  float f;
+  if constexpr (PARTIALS) {
+    __shared__ float2 found;
+    const double norm = norm_of<MAX>(partials, v.n_chunks);
+    if (threadIdx.x == 0) {
+      found = result_of(args, norm);
+      if (blockIdx.x == 0) {
+        args.result[0] = found.x;
+        args.result[1] = found.y;
+      }
+    }
+    __syncthreads();
+    f = found.y;
+  } else {
+    f = args.result[1];
+  }
   if (!isfinite(f) || (dst == 0 && f == 1.0f)) return;
   const ListChunk ch = v.chunks[blockIdx.x];
   const ListEntry &e = v.entries[ch.entry];
-  const Span s = span_of(e, ch.index, v.chunk_units);
+  const Span s = span_of(e, ch.index, v.chunk_units, dst);
   with_type(e.dtype[0], [&](auto from) {
     with_type(e.dtype[dst], [&](auto to) {
       using A = decltype(from);
@@ -303,28 +431,28 @@ __global__ void __launch_bounds__(kThreads) list_scale(ListView v, int dst, cons
           decode<A, V>(r, t);
 #pragma unroll
           for (int j = 0; j < V; ++j) t[j] *= f;
-          st_raw<B, V>(q + i, encode<B, V>(t));
+          st_raw<B, V, true>(q + i, encode<B, V>(t));
         };
         each_dense<V, kUnroll>(
-            s.n,
+            s,
             [&](int i, int step) {
               RawOf<A, V> r[kUnroll];
 #pragma unroll
-              for (int u = 0; u < kUnroll; ++u) r[u] = ld_raw<A, V>(p + i + u * step);
+              for (int u = 0; u < kUnroll; ++u) r[u] = ld_raw<A, V, true>(p + i + u * step);
 #pragma unroll
               for (int u = 0; u < kUnroll; ++u) put(i + u * step, r[u]);
             },
-            [&](int i) { put(i, ld_raw<A, V>(p + i)); }, [&](int i) { st_one(q + i, B::st(A::ld(ld_one(p + i)) * f)); });
+            [&](int i) { put(i, ld_raw<A, V, true>(p + i)); }, [&](int i) { st_one(q + i, B::st(A::ld(ld_one(p + i)) * f)); });
       } else {
         each_unit(e, s, [&](int64_t r, int64_t c, int n) {
           const SA *p = x + r * e.pitch[0] + c;
           SB *q = y + r * e.pitch[dst] + c;
           if (n == kListUnit) {
             float t[kListUnit];
-            decode<A, kListUnit>(ld_raw<A, kListUnit>(p), t);
+            decode<A, kListUnit>(ld_raw<A, kListUnit, true>(p), t);
 #pragma unroll
             for (int j = 0; j < kListUnit; ++j) t[j] *= f;
-            st_raw<B, kListUnit>(q, encode<B, kListUnit>(t));
+            st_raw<B, kListUnit, true>(q, encode<B, kListUnit>(t));
           } else {
             for (int j = 0; j < n; ++j) st_one(q + j, B::st(A::ld(ld_one(p + j)) * f));
           }
@@ -351,7 +479,7 @@ __global__ void __launch_bounds__(kThreads) list_adamw(ListView v, AdamwScalars 
   if (!isfinite(f)) return;
   const ListChunk ch = v.chunks[blockIdx.x];
   const ListEntry &e = v.entries[ch.entry];
-  const Span s = span_of(e, ch.index, v.chunk_units);
+  const Span s = span_of(e, ch.index, v.chunk_units, 1);
   const double eta = h.lr * e.lr_scale;
   const AdamwRule rule{f, h.beta1, h.one_minus_beta1, h.beta2, h.one_minus_beta2, h.inv_sqrt_bias2, h.eps,
                        static_cast<float>(1.0 - eta * (h.weight_decay * e.wd_scale)),
@@ -373,10 +501,10 @@ __global__ void __launch_bounds__(kThreads) list_adamw(ListView v, AdamwScalars 
       decode<EF32, V>(rq, q);
 #pragma unroll
       for (int j = 0; j < V; ++j) p[j] = rule(p[j], x[j], m[j], q[j]);
-      st_raw<EF32, V>(P + ip, encode<EF32, V>(p));
-      st_raw<EF32, V>(M + im, encode<EF32, V>(m));
-      st_raw<EF32, V>(Q + iq, encode<EF32, V>(q));
-      if constexpr (COPY) st_raw<C, V>(w + iw, encode<C, V>(p));
+      st_raw<EF32, V, true>(P + ip, encode<EF32, V>(p));
+      st_raw<EF32, V, true>(M + im, encode<EF32, V>(m));
+      st_raw<EF32, V, true>(Q + iq, encode<EF32, V>(q));
+      if constexpr (COPY) st_raw<C, V, true>(w + iw, encode<C, V>(p));
     };
     auto one = [&](int64_t ig, int64_t ip, int64_t im, int64_t iq, int64_t iw) {
       float m = ld_one(M + im), q = ld_one(Q + iq);
@@ -387,24 +515,24 @@ __global__ void __launch_bounds__(kThreads) list_adamw(ListView v, AdamwScalars 
       if constexpr (COPY) st_one(w + iw, C::st(p));
     };
     if (s.dense) {
-      constexpr int V = 4, U = 2;
+      constexpr int V = 4, U = kUnroll;
       auto whole = [&](int i) {
         const int64_t at = s.first + i;
-        update(std::integral_constant<int, V>{}, ld_raw<EF32, V>(P + at), ld_raw<G, V>(g + at),
-               ld_raw<EF32, V>(M + at), ld_raw<EF32, V>(Q + at), at, at, at, at);
+        update(std::integral_constant<int, V>{}, ld_raw<EF32, V, true>(P + at), ld_raw<G, V, true>(g + at),
+               ld_raw<EF32, V, true>(M + at), ld_raw<EF32, V, true>(Q + at), at, at, at, at);
       };
       each_dense<V, U>(
-          s.n,
+          s,
           [&](int i, int step) {
             RawOf<EF32, V> rp[U], rm[U], rq[U];
             RawOf<G, V> rg[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
               const int64_t at = s.first + i + u * step;
-              rp[u] = ld_raw<EF32, V>(P + at);
-              rg[u] = ld_raw<G, V>(g + at);
-              rm[u] = ld_raw<EF32, V>(M + at);
-              rq[u] = ld_raw<EF32, V>(Q + at);
+              rp[u] = ld_raw<EF32, V, true>(P + at);
+              rg[u] = ld_raw<G, V, true>(g + at);
+              rm[u] = ld_raw<EF32, V, true>(M + at);
+              rq[u] = ld_raw<EF32, V, true>(Q + at);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -419,8 +547,8 @@ __global__ void __launch_bounds__(kThreads) list_adamw(ListView v, AdamwScalars 
                       iq = r * e.pitch[3] + c, iw = r * e.pitch[4] + c;
         if (n == kListUnit) {
           constexpr int V = kListUnit;
-          update(std::integral_constant<int, V>{}, ld_raw<EF32, V>(P + ip), ld_raw<G, V>(g + ig),
-                 ld_raw<EF32, V>(M + im), ld_raw<EF32, V>(Q + iq), ip, im, iq, iw);
+          update(std::integral_constant<int, V>{}, ld_raw<EF32, V, true>(P + ip), ld_raw<G, V, true>(g + ig),
+                 ld_raw<EF32, V, true>(M + im), ld_raw<EF32, V, true>(Q + iq), ip, im, iq, iw);
         } else {
           for (int j = 0; j < n; ++j) one(ig + j, ip + j, im + j, iq + j, iw + j);
         }
@@ -433,27 +561,47 @@ __global__ void __launch_bounds__(kThreads) list_adamw(ListView v, AdamwScalars 
   });
 }
 
-}  // namespace
-
-hipError_t launch_list_partials(const ListView &v, bool max, uint64_t *partials, hipStream_t s) {
+hipError_t launch_partials(const ListView &v, bool max, uint64_t *partials, hipStream_t s) {
   if (v.n_chunks == 0) return hipSuccess;
   const dim3 grid(static_cast<unsigned>(v.n_chunks));
-  if (max) list_partials<true><<<grid, kThreads, 0, s>>>(v, partials);
-  else list_partials<false><<<grid, kThreads, 0, s>>>(v, partials);
+  if (max) list_partials<true, false><<<grid, kThreads, 0, s>>>(v, partials, nullptr, NormArgs{});
+  else list_partials<false, false><<<grid, kThreads, 0, s>>>(v, partials, nullptr, NormArgs{});
   return hipGetLastError();
 }
 
-hipError_t launch_list_finish(const ListView &v, bool max, const uint64_t *partials, const float *inv_scale,
-                              double max_norm, double eps, float *result, float *tensor_norms, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>(tensor_norms ? 1 + v.count : 1));
-  if (max) list_finish<true><<<grid, kThreads, 0, s>>>(v, partials, inv_scale, max_norm, eps, result, tensor_norms);
-  else list_finish<false><<<grid, kThreads, 0, s>>>(v, partials, inv_scale, max_norm, eps, result, tensor_norms);
+}  // namespace
+
+hipError_t launch_list_norm(const ListView &v, bool max, uint64_t *partials, uint32_t *arrived, const NormArgs &a,
+                            float *tensor_norms, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>(v.n_chunks));
+  const bool one = v.n_chunks > 0 && v.n_chunks <= kFinishChunks && !tensor_norms;
+  if (one && max) list_partials<true, true><<<grid, kThreads, 0, s>>>(v, partials, arrived, a);
+  else if (one) list_partials<false, true><<<grid, kThreads, 0, s>>>(v, partials, arrived, a);
+  if (one) return hipGetLastError();
+  hipError_t e = launch_partials(v, max, partials, s);
+  if (e != hipSuccess) return e;
+  const unsigned threads = v.n_chunks > 256 ? 1024 : 256;
+  const bool per_wave = v.count > 256;
+  const int64_t each = per_wave ? threads / 64 : 1;
+  const dim3 blocks(static_cast<unsigned>(tensor_norms ? 1 + (v.count + each - 1) / each : 1));
+  if (max) list_finish<true><<<blocks, threads, 0, s>>>(v, partials, a, tensor_norms, per_wave);
+  else list_finish<false><<<blocks, threads, 0, s>>>(v, partials, a, tensor_norms, per_wave);
   return hipGetLastError();
 }
 
-hipError_t launch_list_scale(const ListView &v, int dst, const float *factor, hipStream_t s) {
-  if (v.n_chunks == 0) return hipSuccess;
-  list_scale<<<dim3(static_cast<unsigned>(v.n_chunks)), kThreads, 0, s>>>(v, dst, factor);
+hipError_t launch_list_clip(const ListView &v, int dst, bool max, uint64_t *partials, uint32_t *arrived,
+                            const NormArgs &a, float *tensor_norms, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>(v.n_chunks));
+  if (v.n_chunks == 0 || v.n_chunks > kScaleChunks || tensor_norms) {
+    hipError_t e = launch_list_norm(v, max, partials, arrived, a, tensor_norms, s);
+    if (e != hipSuccess || v.n_chunks == 0) return e;
+    list_scale<false, false><<<grid, kThreads, 0, s>>>(v, dst, nullptr, a);
+    return hipGetLastError();
+  }
+  hipError_t e = launch_partials(v, max, partials, s);
+  if (e != hipSuccess) return e;
+  if (max) list_scale<true, true><<<grid, kThreads, 0, s>>>(v, dst, partials, a);
+  else list_scale<true, false><<<grid, kThreads, 0, s>>>(v, dst, partials, a);
   return hipGetLastError();
 }
 

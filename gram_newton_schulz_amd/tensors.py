@@ -23,6 +23,12 @@ NORM_L2, NORM_MAX = 0, 1
 _NORMS = {2: NORM_L2, math.inf: NORM_MAX}
 
 
+# the current stream's handle without the Stream object around it, which costs
+# 1.8 us of a call that takes 6
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 class Tensor(ctypes.Structure):
     """gns_tensor."""
     _fields_ = [("data", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
@@ -32,7 +38,8 @@ class Tensor(ctypes.Structure):
 class ListInfo(ctypes.Structure):
     """gns_tensor_list."""
     _fields_ = [("arrays", ctypes.c_int), ("count", ctypes.c_int64), ("elements", ctypes.c_int64),
-                ("chunks", ctypes.c_int64), ("chunk_units", ctypes.c_int64), ("table_bytes", ctypes.c_size_t),
+                ("chunks", ctypes.c_int64), ("chunk_units", ctypes.c_int64), ("keep_from", ctypes.c_int64),
+                ("table_bytes", ctypes.c_size_t),
                 ("dtypes", ctypes.c_uint * 5), ("bytes", ctypes.c_double * 5), ("overlaps", ctypes.c_uint)]
 
 
@@ -106,17 +113,30 @@ class TensorList:
         self.count = count
         self.workspace_bytes = int(L.gns_tensor_list_workspace_bytes(ctypes.byref(self.info)))
         self._info = ctypes.byref(self.info)
+        self._workspaces = {}
         if self.device is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
         # the copy runs on the current stream; calls on other streams wait for it
-        self._home = torch.cuda.current_stream(self.device)
+        home = torch.cuda.current_stream(self.device)
+        self._home = home.cuda_stream
         self.table = image.to(self.device, non_blocking=True)
         self._ready = torch.cuda.Event()
-        self._ready.record(self._home)
+        self._ready.record(home)
         self._table = self.table.data_ptr()
 
     def __len__(self) -> int:
         return self.count
+
+    def _workspace(self, raw: int) -> torch.Tensor:
+        """The workspace of calls on one stream (those of different streams may
+        overlap in time).  A capture takes one of its own, which its graph
+        then keeps."""
+        ws = self._workspaces.get(raw)
+        if ws is None:
+            ws = torch.zeros(self.workspace_bytes, dtype=torch.uint8, device=self.device)
+            if not torch.cuda.is_current_stream_capturing():
+                self._workspaces[raw] = ws
+        return ws
 
     def _external(self, raw: int):
         return torch.cuda.ExternalStream(raw, device=self.device)
@@ -124,14 +144,15 @@ class TensorList:
     def _on(self, stream) -> int:
         """The raw stream a call runs on, ordered after the table's copy."""
         if stream is None:
-            stream = torch.cuda.current_stream(self.device)
-        elif isinstance(stream, int):
-            stream = self._external(stream)
-        if stream != self._home:
+            raw = _current_raw_stream(self.device.index)
+        else:
+            raw = stream if isinstance(stream, int) else stream.cuda_stream
+        if raw != self._home:
+            other = self._external(raw)
             if not torch.cuda.is_current_stream_capturing():
-                stream.wait_event(self._ready)
-            self.table.record_stream(stream)
-        return stream.cuda_stream
+                other.wait_event(self._ready)
+            self.table.record_stream(other)
+        return raw
 
 
 def tensor_list(grads: Sequence[torch.Tensor], out: Optional[Sequence[torch.Tensor]] = None) -> TensorList:
@@ -190,13 +211,11 @@ def _norm_call(fn, grads, max_norm, ord, eps, inv_scale, per_tensor, workspace, 
     if ord not in _NORMS:
         raise GnsError(11, f"ord must be 2 or inf, got {ord}")
     s = lst._on(stream)
-    ws = workspace
     # allocated for the stream that the call runs on
     with contextlib.nullcontext() if stream is None else torch.cuda.stream(lst._external(s)):
         result = torch.empty(2, dtype=torch.float32, device=lst.device)
         norms = torch.empty(lst.count, dtype=torch.float32, device=lst.device) if per_tensor else None
-        if ws is None:
-            ws = torch.empty(lst.workspace_bytes, dtype=torch.uint8, device=lst.device)
+        ws = lst._workspace(s) if workspace is None else workspace
     _check(fn(lst._info, lst._table, _NORMS[ord], float(max_norm), float(eps),
               _scalar("inv_scale", inv_scale, lst.device), result.data_ptr(), _ptr(norms),
               ws.data_ptr(), ws.numel(), s))
@@ -211,7 +230,10 @@ def grad_norm(grads: Union[TensorList, Sequence[torch.Tensor]], *, ord: float = 
     them to ``max_norm`` (gns_grad_norm).  Nothing synchronises: pass the
     result's ``clip`` to :func:`adamw_step` and ``dion3_step`` as
     ``grad_scale``, which then clip while they read the gradients.  When a
-    gradient is not finite, ``clip`` is NaN and those steps change nothing."""
+    gradient is not finite, ``clip`` is NaN and those steps change nothing.
+    The list keeps a workspace for every stream it is used on; ``workspace``
+    (uint8, ``workspace_bytes`` of the list, its first 256 bytes zero before
+    the first use) takes its place."""
     return _norm_call(lib().gns_grad_norm, grads, max_norm, ord, eps, inv_scale, per_tensor, workspace, stream)
 
 

@@ -403,6 +403,8 @@ typedef struct {
   int64_t elements;      /* over all entries of one array                      */
   int64_t chunks;        /* pieces of work: about one workgroup each           */
   int64_t chunk_units;   /* 8-element units per chunk                          */
+  int64_t keep_from;     /* chunks from here on are the last 256 MiB of
+                            gradients: what the last-level cache can hold      */
   size_t table_bytes;
   unsigned dtypes[GNS_LIST_MAX_ARRAYS];  /* per array: bit d set when an entry
                                             has dtype d                        */
@@ -459,7 +461,9 @@ typedef enum {
  *   tensor_norms (device) [count] floats, written: every tensor's own norm
  *                (times s), or NULL.
  *   workspace    (device) >= gns_tensor_list_workspace_bytes(list) bytes,
- *                256-byte aligned; clobbered.
+ *                256-byte aligned.  Its first 256 bytes are zero before the
+ *                first call that uses it, and every call leaves them zero;
+ *                the rest is clobbered.
  * Squares and sums are fp64 in a fixed order, so no gradient overflows or
  * underflows on the way and the result is the same in every run.
  * GNS_E_NULL, GNS_E_PARAM (max_norm or eps negative or NaN, eps infinite, an

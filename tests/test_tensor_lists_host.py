@@ -147,7 +147,7 @@ def norm(info, clip=False, kind=0, max_norm=1.0, eps=1e-6, table=BASE, result=BA
 
 def test_norm_and_clip_refusals():
     _, info, _ = build([[(BASE, 2, 3, 3, F32)]])
-    assert gns.lib().gns_tensor_list_workspace_bytes(ctypes.byref(info)) == 8
+    assert gns.lib().gns_tensor_list_workspace_bytes(ctypes.byref(info)) == 256 + 8
     assert gns.lib().gns_tensor_list_workspace_bytes(None) == 0
     for clip in (False, True):
         assert norm(None, clip) == E["NULL"]
