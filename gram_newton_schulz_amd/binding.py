@@ -44,7 +44,7 @@ EXPORTS = [
     "gns_call_plan", "gns_check_finite", "gns_select_count", "gns_safety_scale",
     "gns_gram_batched_noalloc",
     "gns_tensor_list_bytes", "gns_tensor_list_build", "gns_tensor_list_workspace_bytes",
-    "gns_grad_norm", "gns_grad_clip", "gns_adamw_step",
+    "gns_grad_norm", "gns_grad_clip", "gns_adamw_step", "gns_dion3_step_clipped",
 ]
 
 
@@ -110,6 +110,8 @@ def lib() -> ctypes.CDLL:
                                  ctypes.POINTER(ctypes.c_double), ctypes.c_int,
                                  ctypes.POINTER(ctypes.c_int), ctypes.c_int,
                                  dbl, dbl, dbl, dbl, dbl, ctypes.c_int, vp, ctypes.c_uint, vp, sz, vp]
+    L.gns_dion3_step_clipped.restype = ctypes.c_int
+    L.gns_dion3_step_clipped.argtypes = L.gns_dion3_step.argtypes[:2] + [vp] + L.gns_dion3_step.argtypes[2:]
     L.gns_tuned_tile.restype = ctypes.c_int
     L.gns_tuned_tile.argtypes = [ctypes.c_int, ctypes.c_int, ctypes.c_int, i64, i64, i64,
                                  ctypes.POINTER(ctypes.c_int)]
@@ -230,6 +232,16 @@ def _device_tensor(name: str, t: torch.Tensor, device) -> None:
         raise GnsError(1, f"{name} must be a GPU tensor, got device {t.device}")
     if device is not None and t.device != device:
         raise GnsError(1, f"{name} is on {t.device}, X on {device}")
+
+
+def _scalar_ptr(name: str, t: Optional[torch.Tensor], device) -> Optional[int]:
+    """Address of one float32 on the GPU (None for None)."""
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or t.numel() != 1:
+        raise GnsError(3, f"{name} must be one float32 on the GPU")
+    _device_tensor(name, t, device)
+    return t.data_ptr()
 
 
 def _prepare(X: torch.Tensor, row_idx: Optional[torch.Tensor], out: Optional[torch.Tensor]):
@@ -475,10 +487,14 @@ def dion3_step(W: torch.Tensor, G: torch.Tensor, M: torch.Tensor, v: Optional[to
                normuon: bool = True, compute_dtype=torch.bfloat16, naive_algebra: bool = False,
                square_fallback: bool = True, tile=None, split_batch: bool = True,
                debug_checks: bool = False, row_idx: Optional[torch.Tensor] = None,
+               grad_scale: Optional[torch.Tensor] = None,
                workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """One Dion3 update (Algorithm 4) of every matrix in W ([batch, n, m] or
     [n, m], fp32) via gns_dion3_step: W, M (fp32) and v (fp32 [batch, n], or
     None without NorMuon) are updated in place; G is fp32, bf16 or fp16.
+    ``grad_scale`` (one float32 on the GPU, as the ``clip`` of grad_norm)
+    multiplies G; when it is not finite W, M and v keep what they hold
+    (gns_dion3_step_clipped).
     Returns the selected rows S (int64 [batch, k], ascending)."""
     squeeze = W.dim() == 2
     Wb, Gb, Mb = (t.unsqueeze(0) if squeeze else t for t in (W, G, M))
@@ -509,8 +525,8 @@ def dion3_step(W: torch.Tensor, G: torch.Tensor, M: torch.Tensor, v: Optional[to
     carr, T = _coeff_array(coeffs)
     rs = list(restarts)
     rarr = (ctypes.c_int * max(len(rs), 1))(*rs)
-    _check(lib().gns_dion3_step(
-        _ptr(Wb), _ptr(Gb), _ptr(Mb), _ptr(vb), B, n, m, _dtype_code(Gb.dtype), cdt, k, carr, T,
+    _check(lib().gns_dion3_step_clipped(
+        _ptr(Wb), _ptr(Gb), _scalar_ptr("grad_scale", grad_scale, Wb.device), _ptr(Mb), _ptr(vb), B, n, m, _dtype_code(Gb.dtype), cdt, k, carr, T,
         rarr, len(rs), float(lr), float(weight_decay), float(mu), float(beta2), float(eps),
         1 if normuon else 0, _ptr(row_idx),
         (GNS_OPT_NAIVE_ALGEBRA if naive_algebra else 0)

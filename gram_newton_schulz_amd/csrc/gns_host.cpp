@@ -1342,6 +1342,17 @@ gns_status gns_dion3_step(float *W, const void *G, float *M, float *v, int64_t b
                           double lr, double weight_decay, double mu, double beta2, double eps,
                           int normuon, int64_t *row_idx, unsigned opts, void *workspace,
                           size_t workspace_bytes, void *stream) {
+  return gns_dion3_step_clipped(W, G, nullptr, M, v, batch, n, m, grad_dtype, cdt, k, coeffs, T, restart_after,
+                                n_restart, lr, weight_decay, mu, beta2, eps, normuon, row_idx, opts, workspace,
+                                workspace_bytes, stream);
+}
+
+gns_status gns_dion3_step_clipped(float *W, const void *G, const float *grad_scale, float *M, float *v,
+                                  int64_t batch, int64_t n, int64_t m, gns_dtype grad_dtype, gns_dtype cdt,
+                                  int64_t k, const double *coeffs, int T, const int *restart_after, int n_restart,
+                                  double lr, double weight_decay, double mu, double beta2, double eps, int normuon,
+                                  int64_t *row_idx, unsigned opts, void *workspace, size_t workspace_bytes,
+                                  void *stream) {
   if (!valid_dtype(grad_dtype) || !valid_compute(cdt)) return GNS_E_DTYPE;
   if (batch < 0 || n < 1 || m < 1 || k < 1 || k > n || batch > 65535 || n > (int64_t(1) << 30))
     return GNS_E_SHAPE;
@@ -1369,11 +1380,12 @@ gns_status gns_dion3_step(float *W, const void *G, float *M, float *v, int64_t b
   struct Range { const void *p; size_t bytes; };
   const Range user[] = {{W, elems * 4}, {M, elems * 4}, {G, elems * gns::dtype_size(grad_dtype)},
                         {row_idx, sizeof(int64_t) * batch * k},
-                        {normuon ? v : nullptr, sizeof(float) * batch * n}};
+                        {normuon ? v : nullptr, sizeof(float) * batch * n}, {grad_scale, sizeof(float)}};
+  constexpr int kUser = sizeof(user) / sizeof(user[0]);
   for (const Range &r : user)
     if (r.p && ranges_overlap(workspace, d.bytes, r.p, r.bytes)) return GNS_E_ALIAS;
-  for (int i = 0; i < 5; ++i)
-    for (int j = i + 1; j < 5; ++j)
+  for (int i = 0; i < kUser; ++i)
+    for (int j = i + 1; j < kUser; ++j)
       if (user[i].p && user[j].p && ranges_overlap(user[i].p, user[i].bytes, user[j].p, user[j].bytes))
         return GNS_E_ALIAS;
 
@@ -1396,7 +1408,7 @@ gns_status gns_dion3_step(float *W, const void *G, float *M, float *v, int64_t b
   // selected rows)
   {
     LaunchScope ls(s, "momentum_l1", "momentum_l1", 4.0 * bn * m, bn * m * (8.0 + gsz));
-    hipError_t e = gns::launch_momentum_l1(grad_dtype, M, G, batch, n, m, keys, msq, s);
+    hipError_t e = gns::launch_momentum_l1(grad_dtype, M, G, grad_scale, batch, n, m, keys, msq, s);
     ls.done();
     if (e != hipSuccess) return GNS_E_HIP;
   }
@@ -1436,7 +1448,7 @@ gns_status gns_dion3_step(float *W, const void *G, float *M, float *v, int64_t b
   {
     LaunchScope ls(s, "normuon", "row_sumsq+normuon_factors", normuon ? 2.0 * bk * m : 0.0,
                    normuon ? bk * m * 4.0 + bk * 16.0 : bk * 8.0);
-    hipError_t e = gns::launch_normuon(O, batch, k, m, v, row_idx, n, beta2, eps, normuon, rowsq, factor, s);
+    hipError_t e = gns::launch_normuon(O, batch, k, m, v, row_idx, n, beta2, eps, normuon, rowsq, factor, grad_scale, s);
     ls.done();
     if (e != hipSuccess) return GNS_E_HIP;
   }
@@ -1445,7 +1457,7 @@ gns_status gns_dion3_step(float *W, const void *G, float *M, float *v, int64_t b
     const double rows_w = decay != 1.0f ? bn : bk;
     LaunchScope ls(s, "dion3_update", "dion3_update", 3.0 * bk * m, rows_w * m * 8.0 + bk * m * 12.0);
     hipError_t e = gns::launch_dion3_update(W, M, O, row_idx, factor, batch, n, m, k, decay, lr,
-                                            static_cast<float>(mu), s);
+                                            static_cast<float>(mu), grad_scale, s);
     ls.done();
     if (e != hipSuccess) return GNS_E_HIP;
   }

@@ -124,10 +124,12 @@ hipError_t launch_check_rows(const int64_t *row_idx, int64_t batch, int64_t k, i
                              int32_t *result, hipStream_t s);
 
 // Dion3 update (Algorithm 4 around the orthogonalisation).
+// grad_scale, where not null: one device float that multiplies the gradient;
+// when it is not finite M, v and W keep what they hold.
 // M <- M + G (fp32) and keys[b][i] = sum_j |M_b[i][j]| (fp64); with sumsq
 // also sumsq[b][i] = sum_j M_b[i][j]^2 (fp64).
-hipError_t launch_momentum_l1(int grad_dtype, float *M, const void *G, int64_t batch, int64_t n,
-                              int64_t m, double *keys, double *sumsq, hipStream_t s);
+hipError_t launch_momentum_l1(int grad_dtype, float *M, const void *G, const float *grad_scale, int64_t batch,
+                              int64_t n, int64_t m, double *keys, double *sumsq, hipStream_t s);
 // partials[b][p] (p < parts) = sum over the rows r of part p (ceil(k / parts)
 // consecutive entries of row_idx[b], in order) of rowsq[b][row_idx[b][r]]:
 // the norm partials of a row subset whose per-row sums of squares are known.
@@ -140,11 +142,11 @@ hipError_t launch_select_topk(const double *keys, int64_t batch, int64_t n, int6
 // with the Frobenius rescale, or all ones without NorMuon.
 hipError_t launch_normuon(const float *O, int64_t batch, int64_t k, int64_t m, float *v,
                           const int64_t *S, int64_t n, double beta2, double eps, int normuon,
-                          double *rowsq, double *factor, hipStream_t s);
+                          double *rowsq, double *factor, const float *grad_scale, hipStream_t s);
 // W <- decay W everywhere, W[S_i] -= lr factor_i O_i, M[S_i] *= mu (S ascending).
 hipError_t launch_dion3_update(float *W, float *M, const float *O, const int64_t *S,
                                const double *factor, int64_t batch, int64_t n, int64_t m, int64_t k,
-                               float decay, double lr, float mu, hipStream_t s);
+                               float decay, double lr, float mu, const float *grad_scale, hipStream_t s);
 
 // --------------------------------------------------------------------------
 // lists of tensors (gns_tensors.hip): norm, clip, AdamW

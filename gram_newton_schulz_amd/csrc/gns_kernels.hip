@@ -1784,11 +1784,23 @@ select_topk(const double *keys, int64_t n, int64_t k, int64_t *out) {
 // element, stored), and every row of the sum gets its l1 key sum_j |M_ij|
 // and, when sumsq is given, its sum of squares sum_j M_ij^2 (both fp64;
 // lane-strided 16-byte pieces, then the wave tree: a fixed order for a given
-// shape).  One wave per row.
-template <class TG>
+// shape).  One wave per row.  SCALED: M <- M + c G with c = *grad_scale (one
+// fused multiply-add per element), or M as it is when c is not finite.
+template <class TG, bool SCALED>
 __global__ void __launch_bounds__(256)
-momentum_l1(float *M, const void *G, int64_t n, int64_t m, bool vec, double *keys, double *sumsq) {
+momentum_l1(float *M, const void *G, const float *grad_scale, int64_t n, int64_t m, bool vec, double *keys,
+            double *sumsq) {
   using SG = typename TG::S;
+  float scale = 1.0f;
+  bool skip = false;
+  if constexpr (SCALED) {
+    scale = *grad_scale;
+    skip = !isfinite(scale);
+  }
+  auto sum = [&](float mv, float g) {
+    if constexpr (SCALED) return skip ? mv : fmaf(scale, g, mv);
+    else return mv + g;
+  };
   const int b = blockIdx.y;
   const int lane = threadIdx.x & 63;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
@@ -1813,10 +1825,10 @@ momentum_l1(float *M, const void *G, int64_t n, int64_t m, bool vec, double *key
       }
     };
     auto finish = [&](int64_t v, float4 mv, const float *g) {
-      mv.x += g[0];
-      mv.y += g[1];
-      mv.z += g[2];
-      mv.w += g[3];
+      mv.x = sum(mv.x, g[0]);
+      mv.y = sum(mv.y, g[1]);
+      mv.z = sum(mv.z, g[2]);
+      mv.w = sum(mv.w, g[3]);
       st_once(reinterpret_cast<float4 *>(mr) + v, mv);
       acc += fabs(static_cast<double>(mv.x));
       acc += fabs(static_cast<double>(mv.y));
@@ -1847,7 +1859,7 @@ momentum_l1(float *M, const void *G, int64_t n, int64_t m, bool vec, double *key
     }
   } else {
     for (int64_t c = lane; c < m; c += 64) {
-      const float s = mr[c] + TG::ld(gr[c]);
+      const float s = sum(mr[c], TG::ld(gr[c]));
       mr[c] = s;
       acc += fabs(static_cast<double>(s));
       sq += static_cast<double>(s) * s;
@@ -1930,10 +1942,12 @@ row_sumsq(const float *O, int64_t k, int64_t m, bool vec, double *rowsq) {
 // and O_hat = diag(s) O is brought back to the Frobenius norm of O, so the
 // factor of row i is g s_i with g = ||O||_F / ||O_hat||_F (g = 0 when O_hat
 // is zero).  Without NorMuon every factor is 1.  fp64 throughout, with
-// fixed-order reductions.
+// fixed-order reductions.  With a grad_scale that is not finite v stays as it
+// is (and the factors are not used).
 __global__ void __launch_bounds__(256)
 normuon_factors(const double *rowsq, float *v, const int64_t *S, int64_t n, int64_t k, int64_t m,
-                double beta2, double eps, int normuon, double *factor) {
+                double beta2, double eps, int normuon, double *factor, const float *grad_scale) {
+  if (grad_scale && !isfinite(*grad_scale)) return;
   const int b = blockIdx.x;
   const double *rs = rowsq + static_cast<int64_t>(b) * k;
   const int64_t *Sb = S + static_cast<int64_t>(b) * k;
@@ -1980,10 +1994,12 @@ normuon_factors(const double *rowsq, float *v, const int64_t *S, int64_t n, int6
 //   W[S_i] <- W[S_i] - lr f_i O_i     on the selected rows,
 //   M[S_i] <- mu M[S_i]               (error feedback, selected rows only).
 // The slot i of a row in the ascending index list S comes from a binary
-// search.  fp32 arithmetic on the caller's fp32 buffers.
+// search.  fp32 arithmetic on the caller's fp32 buffers.  Nothing is written
+// with a grad_scale that is not finite.
 __global__ void __launch_bounds__(256)
 dion3_update(float *W, float *M, const float *O, const int64_t *S, const double *factor, int64_t n,
-             int64_t m, int64_t k, float decay, double lr, float mu, bool vec) {
+             int64_t m, int64_t k, float decay, double lr, float mu, bool vec, const float *grad_scale) {
+  if (grad_scale && !isfinite(*grad_scale)) return;
   const int b = blockIdx.y;
   const int64_t row = blockIdx.x;
   const int64_t *Sb = S + static_cast<int64_t>(b) * k;
@@ -2235,14 +2251,26 @@ hipError_t launch_check_rows(const int64_t *row_idx, int64_t batch, int64_t k, i
   return hipGetLastError();
 }
 
-hipError_t launch_momentum_l1(int grad_dtype, float *M, const void *G, int64_t batch, int64_t n,
-                              int64_t m, double *keys, double *sumsq, hipStream_t s) {
+namespace {
+template <bool SCALED>
+void momentum_for(int grad_dtype, dim3 grid, hipStream_t s, float *M, const void *G, const float *grad_scale,
+                  int64_t n, int64_t m, bool vec, double *keys, double *sumsq) {
+  if (grad_dtype == DT_BF16)
+    momentum_l1<EBF16, SCALED><<<grid, 256, 0, s>>>(M, G, grad_scale, n, m, vec, keys, sumsq);
+  else if (grad_dtype == DT_F16)
+    momentum_l1<EF16, SCALED><<<grid, 256, 0, s>>>(M, G, grad_scale, n, m, vec, keys, sumsq);
+  else
+    momentum_l1<EF32, SCALED><<<grid, 256, 0, s>>>(M, G, grad_scale, n, m, vec, keys, sumsq);
+}
+}  // namespace
+
+hipError_t launch_momentum_l1(int grad_dtype, float *M, const void *G, const float *grad_scale, int64_t batch,
+                              int64_t n, int64_t m, double *keys, double *sumsq, hipStream_t s) {
   dim3 grid(static_cast<unsigned>((n + 3) / 4), static_cast<unsigned>(batch));
   const bool vec = (m % 4) == 0 && (reinterpret_cast<uintptr_t>(M) & 15) == 0 &&
                    (reinterpret_cast<uintptr_t>(G) & (grad_dtype == DT_F32 ? 15 : 7)) == 0;
-  if (grad_dtype == DT_BF16) momentum_l1<EBF16><<<grid, 256, 0, s>>>(M, G, n, m, vec, keys, sumsq);
-  else if (grad_dtype == DT_F16) momentum_l1<EF16><<<grid, 256, 0, s>>>(M, G, n, m, vec, keys, sumsq);
-  else momentum_l1<EF32><<<grid, 256, 0, s>>>(M, G, n, m, vec, keys, sumsq);
+  if (grad_scale) momentum_for<true>(grad_dtype, grid, s, M, G, grad_scale, n, m, vec, keys, sumsq);
+  else momentum_for<false>(grad_dtype, grid, s, M, G, nullptr, n, m, vec, keys, sumsq);
   return hipGetLastError();
 }
 
@@ -2262,7 +2290,7 @@ hipError_t launch_select_topk(const double *keys, int64_t batch, int64_t n, int6
 
 hipError_t launch_normuon(const float *O, int64_t batch, int64_t k, int64_t m, float *v,
                           const int64_t *S, int64_t n, double beta2, double eps, int normuon,
-                          double *rowsq, double *factor, hipStream_t s) {
+                          double *rowsq, double *factor, const float *grad_scale, hipStream_t s) {
   if (normuon) {
     dim3 grid(static_cast<unsigned>((k + 3) / 4), static_cast<unsigned>(batch));
     const bool vec = (m % 4) == 0 && (reinterpret_cast<uintptr_t>(O) & 15) == 0;
@@ -2271,17 +2299,17 @@ hipError_t launch_normuon(const float *O, int64_t batch, int64_t k, int64_t m, f
     if (e != hipSuccess) return e;
   }
   normuon_factors<<<static_cast<unsigned>(batch), 256, 0, s>>>(rowsq, v, S, n, k, m, beta2, eps, normuon,
-                                                               factor);
+                                                               factor, grad_scale);
   return hipGetLastError();
 }
 
 hipError_t launch_dion3_update(float *W, float *M, const float *O, const int64_t *S,
                                const double *factor, int64_t batch, int64_t n, int64_t m, int64_t k,
-                               float decay, double lr, float mu, hipStream_t s) {
+                               float decay, double lr, float mu, const float *grad_scale, hipStream_t s) {
   dim3 grid(static_cast<unsigned>(n), static_cast<unsigned>(batch));
   const bool vec = (m % 4) == 0 && (reinterpret_cast<uintptr_t>(W) & 15) == 0 &&
                    (reinterpret_cast<uintptr_t>(M) & 15) == 0 && (reinterpret_cast<uintptr_t>(O) & 15) == 0;
-  dion3_update<<<grid, 256, 0, s>>>(W, M, O, S, factor, n, m, k, decay, lr, mu, vec);
+  dion3_update<<<grid, 256, 0, s>>>(W, M, O, S, factor, n, m, k, decay, lr, mu, vec, grad_scale);
   return hipGetLastError();
 }
 

@@ -17,7 +17,7 @@ from typing import Optional, Sequence, Union
 import torch
 
 
-from .binding import GnsError, _check, _device_tensor, _dtype_code, _ptr, lib
+from .binding import GnsError, _check, _device_tensor, _dtype_code, _ptr, _scalar_ptr, lib
 
 NORM_L2, NORM_MAX = 0, 1
 _NORMS = {2: NORM_L2, math.inf: NORM_MAX}
@@ -197,15 +197,6 @@ class GradNorm:
         return self.result[1]
 
 
-def _scalar(name: str, t: Optional[torch.Tensor], device) -> Optional[int]:
-    if t is None:
-        return None
-    if t.dtype != torch.float32 or t.numel() != 1:
-        raise GnsError(3, f"{name} must be one float32 on the GPU")
-    _device_tensor(name, t, device)
-    return t.data_ptr()
-
-
 def _norm_call(fn, grads, max_norm, ord, eps, inv_scale, per_tensor, workspace, stream) -> GradNorm:
     lst = grads if isinstance(grads, TensorList) else tensor_list(grads)
     if ord not in _NORMS:
@@ -217,7 +208,7 @@ def _norm_call(fn, grads, max_norm, ord, eps, inv_scale, per_tensor, workspace, 
         norms = torch.empty(lst.count, dtype=torch.float32, device=lst.device) if per_tensor else None
         ws = lst._workspace(s) if workspace is None else workspace
     _check(fn(lst._info, lst._table, _NORMS[ord], float(max_norm), float(eps),
-              _scalar("inv_scale", inv_scale, lst.device), result.data_ptr(), _ptr(norms),
+              _scalar_ptr("inv_scale", inv_scale, lst.device), result.data_ptr(), _ptr(norms),
               ws.data_ptr(), ws.numel(), s))
     return GradNorm(result, norms)
 
@@ -256,4 +247,4 @@ def adamw_step(tensors: TensorList, step: int, *, lr: float, betas: Sequence[flo
     s = tensors._on(stream)
     _check(lib().gns_adamw_step(tensors._info, tensors._table, int(step), float(lr), float(betas[0]),
                                 float(betas[1]), float(eps), float(weight_decay),
-                                _scalar("grad_scale", grad_scale, tensors.device), s))
+                                _scalar_ptr("grad_scale", grad_scale, tensors.device), s))

@@ -368,6 +368,20 @@ gns_status gns_dion3_step(float *W, const void *G, float *M, float *v, int64_t b
                           size_t workspace_bytes, void *stream);
 
 /*
+ * gns_dion3_step on gradients times *grad_scale, a (device) float such as the
+ * clip factor of gns_grad_norm: step 1 is M <- M + (*grad_scale) G (one fused
+ * multiply-add per element), everything else as there.  When it is not finite
+ * the update is skipped: W, M and v keep what they hold, and row_idx gets the
+ * selection of M as it is.  NULL runs gns_dion3_step.
+ */
+gns_status gns_dion3_step_clipped(float *W, const void *G, const float *grad_scale, float *M, float *v,
+                                  int64_t batch, int64_t n, int64_t m, gns_dtype grad_dtype,
+                                  gns_dtype compute_dtype, int64_t k, const double *coeffs, int T,
+                                  const int *restart_after, int n_restart, double lr, double weight_decay,
+                                  double mu, double beta2, double eps, int normuon, int64_t *row_idx,
+                                  unsigned opts, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * Operators over lists of tensors: the parts of an optimiser step that go over
  * every tensor of a model, whatever its shape, beside the matrices that the
  * entry points above update.  A list names its tensors once; the calls on it
