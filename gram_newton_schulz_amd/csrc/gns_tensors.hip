@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "gns_elem.h"
@@ -22,13 +23,32 @@ constexpr int kThreads = 256;
 // fences in each, which line up on one address: 24 tensors of 1024 elements
 // 12.8 -> 9.4 us per call, 512 chunks no different, 1024 chunks 4 us more and
 // 16384 chunks 800 us more than a second launch of one workgroup.
-constexpr int64_t kFinishChunks = 128;
+constexpr int64_t kFinishChunks = 128, kFinishCount = 4096;
 
 // Up to this many partials are added up by every workgroup of the scaling
 // itself, which saves the launch between: 3 x 513x777 13.9 -> 11.5 us per
 // call, 8 x 512x4096 bf16 (2048 chunks) 18.9 -> 17.5; with 16384 chunks it
 // costs 82 us.
 constexpr int64_t kScaleChunks = 4096;
+
+// The passes that write cut the chunks into parts of so many units, a
+// workgroup each.  The workgroups run in order, so short ones keep all of them
+// in a narrow window of every array that moves through memory, where long
+// ones each go their own way: AdamW of 268M elements with the norm before it
+// takes 1454 us with parts of 16384 elements, 1410 with 8192, 1367 with 4096,
+// 1254 with 2048 and 1270 with 1024, of 8.9M packed elements 57.0 with 8192
+// and 53.4 with 1024 (one 16-byte piece of each array per thread).
+// Grids that walk the parts in a loop instead lose the window again
+// (clipping 64 x 2048x7168 bf16: 880 us one by one, 1010 to 1270 in loops).
+constexpr int64_t kAdamwUnits = 128;
+// Clipping moves fewer bytes per workgroup, so that starting them weighs more
+// (940M bf16 elements: 960 us with parts of 8192 units, 915 with 2048, 880 with
+// 512, 1010 with 256).  Lists that the last-level cache holds do not gain
+// (134 MB fp16 to fp32: 83 us whole, 86 with 512).  In place most steps end
+// with nothing to write once training is stable, and then starting the
+// workgroups is all that is left: 5 us for the same list with 8192 units, 47
+// with 512.
+constexpr int64_t kScaleUnits = 512, kScaleInPlaceUnits = 8192;
 
 // V consecutive elements as they lie in memory.  The addresses are aligned to
 // the element only: gfx950 loads and stores 8 and 16 bytes from any address,
@@ -130,13 +150,13 @@ __device__ __forceinline__ Span span_of(const ListEntry &e, uint32_t index, int6
                                        kLine / size);
     const int64_t end = (u0 + chunk_units) * kListUnit + shift;
     s.first = index ? u0 * kListUnit + shift : 0;
-    s.n = static_cast<int>((end < e.cols ? end : e.cols) - s.first);
-    if (s.n < 0) s.n = 0;
+    const int64_t n = (end < e.cols ? end : e.cols) - s.first;
+    s.n = n > 0 ? static_cast<int>(n) : 0;
     if (!index) s.head = shift < s.n ? shift : s.n;
   } else {
     s.first = u0;
     const int64_t left = e.units - u0;
-    s.n = static_cast<int>(left < chunk_units ? left : chunk_units);
+    s.n = left <= 0 ? 0 : static_cast<int>(left < chunk_units ? left : chunk_units);
   }
   return s;
 }
@@ -254,7 +274,7 @@ template <class E> struct NormPart<E, true> {
 template <bool MAX>
 __device__ __forceinline__ void add_partials(const uint64_t *p, int64_t n, int t, int threads, double &acc,
                                              uint32_t &top) {
-  constexpr int kAtOnce = 8;   // loads in flight per thread
+  constexpr int kAtOnce = 16;   // loads in flight per thread
   for (int64_t i = t; i < n; i += kAtOnce * threads) {
     uint64_t x[kAtOnce];
 #pragma unroll
@@ -271,6 +291,13 @@ __device__ __forceinline__ void add_partials(const uint64_t *p, int64_t n, int t
   }
 }
 
+// Norm (thread 0's) of one partial per thread.
+template <bool MAX>
+__device__ __forceinline__ double norm_of(uint64_t bits) {
+  if constexpr (MAX) return __uint_as_float(block_max(static_cast<uint32_t>(bits)));
+  else return sqrt(block_sum(__longlong_as_double(bits)));
+}
+
 // Norm of all `n` partials (thread 0's), by the whole workgroup.
 template <bool MAX>
 __device__ __forceinline__ double norm_of(const uint64_t *partials, int64_t n) {
@@ -282,8 +309,11 @@ __device__ __forceinline__ double norm_of(const uint64_t *partials, int64_t n) {
 }
 
 // The result's {norm, clip factor} from the norm of the stored gradients.
+__device__ __forceinline__ double unscale(const NormArgs &a) {
+  return a.inv_scale ? static_cast<double>(*a.inv_scale) : 1.0;
+}
 __device__ __forceinline__ float2 result_of(const NormArgs &a, double raw) {
-  const double s = a.inv_scale ? static_cast<double>(*a.inv_scale) : 1.0;
+  const double s = unscale(a);
   const double norm = raw * s;
   const double ratio = a.max_norm / (norm + a.eps);
   return make_float2(static_cast<float>(norm),
@@ -297,10 +327,10 @@ __device__ __forceinline__ void write_result(const NormArgs &a, double raw) {
 
 // partials[c] of every chunk c.  With FINISH the workgroup that stores the
 // last of them adds them up, in the order of the chunks, and writes the
-// result; it leaves *arrived at zero, as it found it.
+// result and the entries' norms; it leaves *arrived at zero, as it found it.
 template <bool MAX, bool FINISH>
 __global__ void __launch_bounds__(kThreads)
-list_partials(ListView v, uint64_t *partials, uint32_t *arrived, NormArgs args) {
+list_partials(ListView v, uint64_t *partials, uint32_t *arrived, NormArgs args, float *tensor_norms) {
   const ListChunk ch = v.chunks[blockIdx.x];
   const ListEntry &e = v.entries[ch.entry];
   const Span s = span_of(e, ch.index, v.chunk_units, 0);
@@ -349,10 +379,26 @@ list_partials(ListView v, uint64_t *partials, uint32_t *arrived, NormArgs args) 
       last = __hip_atomic_fetch_add(arrived, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
     __syncthreads();
     if (!last) return;
-    const double norm = norm_of<MAX>(partials, v.n_chunks);
-    if (threadIdx.x == 0) {
+    __shared__ uint64_t all[kFinishChunks];
+    const int t = threadIdx.x, n = static_cast<int>(v.n_chunks);
+    if (t < n) all[t] = __hip_atomic_load(partials + t, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    const double norm = norm_of<MAX>(t < n ? all[t] : 0);
+    if (t == 0) {
       write_result(args, norm);
       __hip_atomic_store(arrived, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    if (!tensor_norms) return;
+    const double s = unscale(args);
+    for (int64_t i = t; i < v.count; i += kThreads) {
+      const ListEntry &e = v.entries[i];
+      double acc = 0.0;
+      uint32_t top = 0;
+      for (uint32_t c = e.first_chunk; c < e.first_chunk + e.chunks; ++c) {
+        if constexpr (MAX) top = max(top, static_cast<uint32_t>(all[c]));
+        else acc += __longlong_as_double(all[c]);
+      }
+      tensor_norms[i] = static_cast<float>((MAX ? static_cast<double>(__uint_as_float(top)) : sqrt(acc)) * s);
     }
   }
 }
@@ -367,7 +413,7 @@ list_finish(ListView v, const uint64_t *partials, NormArgs args, float *tensor_n
     if (threadIdx.x == 0) write_result(args, norm);
     return;
   }
-  const double s = args.inv_scale ? static_cast<double>(*args.inv_scale) : 1.0;
+  const double s = unscale(args);
   if (!per_wave) {
     const ListEntry &e = v.entries[blockIdx.x - 1];
     const double norm = norm_of<MAX>(partials + e.first_chunk, e.chunks) * s;
@@ -388,12 +434,13 @@ list_finish(ListView v, const uint64_t *partials, NormArgs args, float *tensor_n
     tensor_norms[i] = static_cast<float>((MAX ? static_cast<double>(__uint_as_float(top)) : sqrt(acc)) * s);
 }
 
-// Array dst <- factor * array 0.  The factor is the result's, or with
+// Array dst <- factor * array 0, one workgroup for each of `parts` parts of a
+// chunk.  The factor is the result's, or with
 // PARTIALS every workgroup's own sum of the partials (all in the same order,
 // so all the same), of which the first writes the result.
 template <bool PARTIALS, bool MAX>
 __global__ void __launch_bounds__(kThreads)
-list_scale(ListView v, int dst, const uint64_t *partials, NormArgs args) {
+list_scale(ListView v, int dst, const uint64_t *partials, NormArgs args, unsigned parts) {
   float f;
   if constexpr (PARTIALS) {
     __shared__ float2 found;
@@ -411,9 +458,9 @@ list_scale(ListView v, int dst, const uint64_t *partials, NormArgs args) {
     f = args.result[1];
   }
   if (!isfinite(f) || (dst == 0 && f == 1.0f)) return;
-  const ListChunk ch = v.chunks[blockIdx.x];
+  const ListChunk ch = v.chunks[blockIdx.x / parts];
   const ListEntry &e = v.entries[ch.entry];
-  const Span s = span_of(e, ch.index, v.chunk_units, dst);
+  const Span s = span_of(e, ch.index * parts + blockIdx.x % parts, v.chunk_units / parts, dst);
   with_type(e.dtype[0], [&](auto from) {
     with_type(e.dtype[dst], [&](auto to) {
       using A = decltype(from);
@@ -474,12 +521,12 @@ struct AdamwRule {
 };
 
 template <bool COPY>
-__global__ void __launch_bounds__(kThreads) list_adamw(ListView v, AdamwScalars h, const float *grad_scale) {
+__global__ void __launch_bounds__(kThreads) list_adamw(ListView v, AdamwScalars h, const float *grad_scale, unsigned parts) {
   const float f = grad_scale ? *grad_scale : 1.0f;
   if (!isfinite(f)) return;
-  const ListChunk ch = v.chunks[blockIdx.x];
+  const ListChunk ch = v.chunks[blockIdx.x / parts];
   const ListEntry &e = v.entries[ch.entry];
-  const Span s = span_of(e, ch.index, v.chunk_units, 1);
+  const Span s = span_of(e, ch.index * parts + blockIdx.x % parts, v.chunk_units / parts, 1);
   const double eta = h.lr * e.lr_scale;
   const AdamwRule rule{f, h.beta1, h.one_minus_beta1, h.beta2, h.one_minus_beta2, h.inv_sqrt_bias2, h.eps,
                        static_cast<float>(1.0 - eta * (h.weight_decay * e.wd_scale)),
@@ -515,32 +562,14 @@ __global__ void __launch_bounds__(kThreads) list_adamw(ListView v, AdamwScalars 
       if constexpr (COPY) st_one(w + iw, C::st(p));
     };
     if (s.dense) {
-      constexpr int V = 4, U = kUnroll;
+      constexpr int V = 4;
       auto whole = [&](int i) {
         const int64_t at = s.first + i;
         update(std::integral_constant<int, V>{}, ld_raw<EF32, V, true>(P + at), ld_raw<G, V, true>(g + at),
                ld_raw<EF32, V, true>(M + at), ld_raw<EF32, V, true>(Q + at), at, at, at, at);
       };
-      each_dense<V, U>(
-          s,
-          [&](int i, int step) {
-            RawOf<EF32, V> rp[U], rm[U], rq[U];
-            RawOf<G, V> rg[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-              const int64_t at = s.first + i + u * step;
-              rp[u] = ld_raw<EF32, V, true>(P + at);
-              rg[u] = ld_raw<G, V, true>(g + at);
-              rm[u] = ld_raw<EF32, V, true>(M + at);
-              rq[u] = ld_raw<EF32, V, true>(Q + at);
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-              const int64_t at = s.first + i + u * step;
-              update(std::integral_constant<int, V>{}, rp[u], rg[u], rm[u], rq[u], at, at, at, at);
-            }
-          },
-          whole, [&](int i) { one(s.first + i, s.first + i, s.first + i, s.first + i, s.first + i); });
+      each_dense<V, 1>(s, [&](int i, int) { whole(i); }, whole,
+                       [&](int i) { one(s.first + i, s.first + i, s.first + i, s.first + i, s.first + i); });
     } else {
       each_unit(e, s, [&](int64_t r, int64_t c, int n) {
         const int64_t ig = r * e.pitch[0] + c, ip = r * e.pitch[1] + c, im = r * e.pitch[2] + c,
@@ -561,11 +590,19 @@ __global__ void __launch_bounds__(kThreads) list_adamw(ListView v, AdamwScalars 
   });
 }
 
+// Into how many parts of `units` units a pass cuts every chunk (a power of
+// two, as the chunk is); no more than a grid holds.
+unsigned parts_of(const ListView &v, int64_t units) {
+  int64_t parts = std::max<int64_t>(1, v.chunk_units / units);
+  while (parts > 1 && v.n_chunks * parts > (int64_t(1) << 23)) parts /= 2;
+  return static_cast<unsigned>(parts);
+}
+
 hipError_t launch_partials(const ListView &v, bool max, uint64_t *partials, hipStream_t s) {
   if (v.n_chunks == 0) return hipSuccess;
   const dim3 grid(static_cast<unsigned>(v.n_chunks));
-  if (max) list_partials<true, false><<<grid, kThreads, 0, s>>>(v, partials, nullptr, NormArgs{});
-  else list_partials<false, false><<<grid, kThreads, 0, s>>>(v, partials, nullptr, NormArgs{});
+  if (max) list_partials<true, false><<<grid, kThreads, 0, s>>>(v, partials, nullptr, NormArgs{}, nullptr);
+  else list_partials<false, false><<<grid, kThreads, 0, s>>>(v, partials, nullptr, NormArgs{}, nullptr);
   return hipGetLastError();
 }
 
@@ -574,9 +611,9 @@ hipError_t launch_partials(const ListView &v, bool max, uint64_t *partials, hipS
 hipError_t launch_list_norm(const ListView &v, bool max, uint64_t *partials, uint32_t *arrived, const NormArgs &a,
                             float *tensor_norms, hipStream_t s) {
   const dim3 grid(static_cast<unsigned>(v.n_chunks));
-  const bool one = v.n_chunks > 0 && v.n_chunks <= kFinishChunks && !tensor_norms;
-  if (one && max) list_partials<true, true><<<grid, kThreads, 0, s>>>(v, partials, arrived, a);
-  else if (one) list_partials<false, true><<<grid, kThreads, 0, s>>>(v, partials, arrived, a);
+  const bool one = v.n_chunks > 0 && v.n_chunks <= kFinishChunks && (!tensor_norms || v.count <= kFinishCount);
+  if (one && max) list_partials<true, true><<<grid, kThreads, 0, s>>>(v, partials, arrived, a, tensor_norms);
+  else if (one) list_partials<false, true><<<grid, kThreads, 0, s>>>(v, partials, arrived, a, tensor_norms);
   if (one) return hipGetLastError();
   hipError_t e = launch_partials(v, max, partials, s);
   if (e != hipSuccess) return e;
@@ -595,22 +632,24 @@ hipError_t launch_list_clip(const ListView &v, int dst, bool max, uint64_t *part
   if (v.n_chunks == 0 || v.n_chunks > kScaleChunks || tensor_norms) {
     hipError_t e = launch_list_norm(v, max, partials, arrived, a, tensor_norms, s);
     if (e != hipSuccess || v.n_chunks == 0) return e;
-    list_scale<false, false><<<grid, kThreads, 0, s>>>(v, dst, nullptr, a);
+    const unsigned parts = v.keep_from == 0 ? 1 : parts_of(v, dst ? kScaleUnits : kScaleInPlaceUnits);
+    list_scale<false, false><<<grid.x * parts, kThreads, 0, s>>>(v, dst, nullptr, a, parts);
     return hipGetLastError();
   }
   hipError_t e = launch_partials(v, max, partials, s);
   if (e != hipSuccess) return e;
-  if (max) list_scale<true, true><<<grid, kThreads, 0, s>>>(v, dst, partials, a);
-  else list_scale<true, false><<<grid, kThreads, 0, s>>>(v, dst, partials, a);
+  if (max) list_scale<true, true><<<grid, kThreads, 0, s>>>(v, dst, partials, a, 1);
+  else list_scale<true, false><<<grid, kThreads, 0, s>>>(v, dst, partials, a, 1);
   return hipGetLastError();
 }
 
 hipError_t launch_list_adamw(const ListView &v, bool copy, const AdamwScalars &h, const float *grad_scale,
                              hipStream_t s) {
   if (v.n_chunks == 0) return hipSuccess;
-  const dim3 grid(static_cast<unsigned>(v.n_chunks));
-  if (copy) list_adamw<true><<<grid, kThreads, 0, s>>>(v, h, grad_scale);
-  else list_adamw<false><<<grid, kThreads, 0, s>>>(v, h, grad_scale);
+  const unsigned parts = parts_of(v, kAdamwUnits);
+  const dim3 grid(static_cast<unsigned>(v.n_chunks) * parts);
+  if (copy) list_adamw<true><<<grid, kThreads, 0, s>>>(v, h, grad_scale, parts);
+  else list_adamw<false><<<grid, kThreads, 0, s>>>(v, h, grad_scale, parts);
   return hipGetLastError();
 }
 
