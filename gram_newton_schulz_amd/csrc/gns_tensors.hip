@@ -55,6 +55,10 @@ constexpr int64_t kScaleUnits = 512, kScaleInPlaceUnits = 8192;
 // and a wave's accesses are consecutive, so a misaligned tensor costs one more
 // cache line per wave and instruction, not another path.
 template <int BYTES> struct Raw;
+template <> struct Raw<4> {
+  typedef uint32_t T __attribute__((ext_vector_type(1), aligned(2)));
+  T v[1];
+};
 template <> struct Raw<8> {
   typedef uint32_t T __attribute__((ext_vector_type(2), aligned(2)));
   T v[1];
@@ -115,6 +119,45 @@ __device__ __forceinline__ RawOf<E, V> encode(const float (&x)[V]) {
     else r.v[i / W][i % W] = E::st2(x[2 * i], x[2 * i + 1]);
   }
   return r;
+}
+
+// A unit of n <= kListUnit elements.  A short one is its pieces of four, two
+// and one, in x[0..3], x[4..5] and x[6] (the rest of x is zero).
+template <class E, int V, bool NT>
+__device__ __forceinline__ void ld_piece(const typename E::S *p, float *x) {
+  float t[V];
+  decode<E, V>(ld_raw<E, V, NT>(p), t);
+#pragma unroll
+  for (int j = 0; j < V; ++j) x[j] = t[j];
+}
+template <class E, int V, bool NT>
+__device__ __forceinline__ void st_piece(typename E::S *p, const float *x) {
+  float t[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) t[j] = x[j];
+  st_raw<E, V, NT>(p, encode<E, V>(t));
+}
+template <class E, bool NT>
+__device__ __forceinline__ void ld_unit(const typename E::S *p, int n, float (&x)[kListUnit]) {
+  if (n == kListUnit) {
+    ld_piece<E, kListUnit, NT>(p, x);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kListUnit; ++j) x[j] = 0.0f;
+    if (n & 4) ld_piece<E, 4, NT>(p, x);
+    if (n & 2) ld_piece<E, 2, NT>(p + (n & 4), x + 4);
+    if (n & 1) x[6] = E::ld(ld_one(p + (n & 6)));
+  }
+}
+template <class E, bool NT>
+__device__ __forceinline__ void st_unit(typename E::S *p, int n, const float (&x)[kListUnit]) {
+  if (n == kListUnit) {
+    st_piece<E, kListUnit, NT>(p, x);
+  } else {
+    if (n & 4) st_piece<E, 4, NT>(p, x);
+    if (n & 2) st_piece<E, 2, NT>(p + (n & 4), x + 4);
+    if (n & 1) st_one(p + (n & 6), E::st(x[6]));
+  }
 }
 
 // Calls f with a value of the element type that a table names.
@@ -239,6 +282,9 @@ template <class E> struct NormPart<E, false> {
   template <int V> __device__ void add(const RawOf<E, V> &r) {
     float x[V];
     decode<E, V>(r, x);
+    add_values<V>(x);
+  }
+  template <int V> __device__ void add_values(const float (&x)[V]) {
 #pragma unroll
     for (int i = 0; i < V; i += 2) {
       acc = fma(static_cast<double>(x[i]), static_cast<double>(x[i]), acc);
@@ -259,6 +305,9 @@ template <class E> struct NormPart<E, true> {
   template <int V> __device__ void add(const RawOf<E, V> &r) {
     float x[V];
     decode<E, V>(r, x);
+    add_values<V>(x);
+  }
+  template <int V> __device__ void add_values(const float (&x)[V]) {
 #pragma unroll
     for (int i = 0; i < V; ++i) top = max(top, magnitude(x[i]));
   }
@@ -365,10 +414,9 @@ list_partials(ListView v, uint64_t *partials, uint32_t *arrived, NormArgs args, 
     else {
       const int64_t pitch = e.pitch[0];
       each_unit(e, s, [&](int64_t r, int64_t c, int n) {
-        const S *p = base + r * pitch + c;
-        if (n == kListUnit) part.template add<kListUnit>(ld_raw<E, kListUnit, false>(p));
-        else
-          for (int j = 0; j < n; ++j) part.add_one(ld_one(p + j));
+        float x[kListUnit];
+        ld_unit<E, false>(base + r * pitch + c, n, x);
+        part.template add_values<kListUnit>(x);
       });
     }
     part.finish(partials + blockIdx.x);
@@ -494,14 +542,22 @@ list_scale(ListView v, int dst, const uint64_t *partials, NormArgs args, unsigne
         each_unit(e, s, [&](int64_t r, int64_t c, int n) {
           const SA *p = x + r * e.pitch[0] + c;
           SB *q = y + r * e.pitch[dst] + c;
-          if (n == kListUnit) {
-            float t[kListUnit];
-            decode<A, kListUnit>(ld_raw<A, kListUnit, true>(p), t);
+          // each width on its own, from load to store: a wave then waits for the
+          // ends of rows while the stores of the whole units are on their way
+          auto piece = [&](auto width, int at) {
+            constexpr int W = decltype(width)::value;
+            float t[W];
+            decode<A, W>(ld_raw<A, W, true>(p + at), t);
 #pragma unroll
-            for (int j = 0; j < kListUnit; ++j) t[j] *= f;
-            st_raw<B, kListUnit, true>(q, encode<B, kListUnit>(t));
+            for (int j = 0; j < W; ++j) t[j] *= f;
+            st_raw<B, W, true>(q + at, encode<B, W>(t));
+          };
+          if (n == kListUnit) {
+            piece(std::integral_constant<int, kListUnit>{}, 0);
           } else {
-            for (int j = 0; j < n; ++j) st_one(q + j, B::st(A::ld(ld_one(p + j)) * f));
+            if (n & 4) piece(std::integral_constant<int, 4>{}, 0);
+            if (n & 2) piece(std::integral_constant<int, 2>{}, n & 4);
+            if (n & 1) st_one(q + (n & 6), B::st(A::ld(ld_one(p + (n & 6))) * f));
           }
         });
       }
@@ -538,49 +594,49 @@ __global__ void __launch_bounds__(kThreads) list_adamw(ListView v, AdamwScalars 
     using C = decltype(copy);
     const typename G::S *g = static_cast<const typename G::S *>(e.data[0]);
     typename C::S *w = static_cast<typename C::S *>(e.data[4]);
-    auto update = [&](auto width, const auto &rp, const auto &rg, const auto &rm, const auto &rq, int64_t ip,
-                      int64_t im, int64_t iq, int64_t iw) {
-      constexpr int V = decltype(width)::value;
-      float p[V], x[V], m[V], q[V];
-      decode<EF32, V>(rp, p);
-      decode<G, V>(rg, x);
-      decode<EF32, V>(rm, m);
-      decode<EF32, V>(rq, q);
-#pragma unroll
-      for (int j = 0; j < V; ++j) p[j] = rule(p[j], x[j], m[j], q[j]);
-      st_raw<EF32, V, true>(P + ip, encode<EF32, V>(p));
-      st_raw<EF32, V, true>(M + im, encode<EF32, V>(m));
-      st_raw<EF32, V, true>(Q + iq, encode<EF32, V>(q));
-      if constexpr (COPY) st_raw<C, V, true>(w + iw, encode<C, V>(p));
-    };
-    auto one = [&](int64_t ig, int64_t ip, int64_t im, int64_t iq, int64_t iw) {
-      float m = ld_one(M + im), q = ld_one(Q + iq);
-      const float p = rule(ld_one(P + ip), G::ld(ld_one(g + ig)), m, q);
-      st_one(P + ip, p);
-      st_one(M + im, m);
-      st_one(Q + iq, q);
-      if constexpr (COPY) st_one(w + iw, C::st(p));
-    };
     if (s.dense) {
       constexpr int V = 4;
       auto whole = [&](int i) {
         const int64_t at = s.first + i;
-        update(std::integral_constant<int, V>{}, ld_raw<EF32, V, true>(P + at), ld_raw<G, V, true>(g + at),
-               ld_raw<EF32, V, true>(M + at), ld_raw<EF32, V, true>(Q + at), at, at, at, at);
+        const auto rp = ld_raw<EF32, V, true>(P + at), rm = ld_raw<EF32, V, true>(M + at),
+                   rq = ld_raw<EF32, V, true>(Q + at);
+        const auto rg = ld_raw<G, V, true>(g + at);
+        float p[V], x[V], m[V], q[V];
+        decode<EF32, V>(rp, p);
+        decode<G, V>(rg, x);
+        decode<EF32, V>(rm, m);
+        decode<EF32, V>(rq, q);
+#pragma unroll
+        for (int j = 0; j < V; ++j) p[j] = rule(p[j], x[j], m[j], q[j]);
+        st_raw<EF32, V, true>(P + at, encode<EF32, V>(p));
+        st_raw<EF32, V, true>(M + at, encode<EF32, V>(m));
+        st_raw<EF32, V, true>(Q + at, encode<EF32, V>(q));
+        if constexpr (COPY) st_raw<C, V, true>(w + at, encode<C, V>(p));
       };
-      each_dense<V, 1>(s, [&](int i, int) { whole(i); }, whole,
-                       [&](int i) { one(s.first + i, s.first + i, s.first + i, s.first + i, s.first + i); });
+      each_dense<V, 1>(s, [&](int i, int) { whole(i); }, whole, [&](int i) {
+        const int64_t at = s.first + i;
+        float m = ld_one(M + at), q = ld_one(Q + at);
+        const float p = rule(ld_one(P + at), G::ld(ld_one(g + at)), m, q);
+        st_one(P + at, p);
+        st_one(M + at, m);
+        st_one(Q + at, q);
+        if constexpr (COPY) st_one(w + at, C::st(p));
+      });
     } else {
       each_unit(e, s, [&](int64_t r, int64_t c, int n) {
         const int64_t ig = r * e.pitch[0] + c, ip = r * e.pitch[1] + c, im = r * e.pitch[2] + c,
                       iq = r * e.pitch[3] + c, iw = r * e.pitch[4] + c;
-        if (n == kListUnit) {
-          constexpr int V = kListUnit;
-          update(std::integral_constant<int, V>{}, ld_raw<EF32, V, true>(P + ip), ld_raw<G, V, true>(g + ig),
-                 ld_raw<EF32, V, true>(M + im), ld_raw<EF32, V, true>(Q + iq), ip, im, iq, iw);
-        } else {
-          for (int j = 0; j < n; ++j) one(ig + j, ip + j, im + j, iq + j, iw + j);
-        }
+        float p[kListUnit], x[kListUnit], m[kListUnit], q[kListUnit];
+        ld_unit<EF32, false>(P + ip, n, p);
+        ld_unit<G, false>(g + ig, n, x);
+        ld_unit<EF32, false>(M + im, n, m);
+        ld_unit<EF32, false>(Q + iq, n, q);
+#pragma unroll
+        for (int j = 0; j < kListUnit; ++j) p[j] = rule(p[j], x[j], m[j], q[j]);
+        st_unit<EF32, false>(P + ip, n, p);
+        st_unit<EF32, false>(M + im, n, m);
+        st_unit<EF32, false>(Q + iq, n, q);
+        if constexpr (COPY) st_unit<C, false>(w + iw, n, p);
       });
     }
   };

@@ -14,10 +14,11 @@ import ctypes
 import math
 from typing import Optional, Sequence, Union
 
+import numpy as np
 import torch
 
 
-from .binding import GnsError, _check, _device_tensor, _dtype_code, _ptr, _scalar_ptr, lib
+from .binding import GnsError, _DT, _check, _device_tensor, _dtype_code, _ptr, _scalar_ptr, lib
 
 NORM_L2, NORM_MAX = 0, 1
 _NORMS = {2: NORM_L2, math.inf: NORM_MAX}
@@ -33,6 +34,12 @@ class Tensor(ctypes.Structure):
     """gns_tensor."""
     _fields_ = [("data", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
                 ("pitch", ctypes.c_int64), ("dtype", ctypes.c_int)]
+
+
+# the same, for filling many at once
+_ENTRY = np.dtype([("data", np.uint64), ("rows", np.int64), ("cols", np.int64), ("pitch", np.int64),
+                   ("dtype", np.int32), ("_pad", np.int32)])
+assert _ENTRY.itemsize == ctypes.sizeof(Tensor)
 
 
 class ListInfo(ctypes.Structure):
@@ -84,32 +91,48 @@ class TensorList:
             if scales is not None and len(scales) != count:
                 raise GnsError(2, f"{len(scales)} {name}, {count} {names[0]}")
         self.arrays, self.tensors, self.device = len(arrays), arrays, None
-        entries = (Tensor * max(1, self.arrays * count))()
-        for i, group in enumerate(zip(*arrays)):
-            for name, t in zip(names, group):
-                if not isinstance(t, torch.Tensor) or t.layout != torch.strided:
-                    raise GnsError(1, f"{name}[{i}] is not a dense tensor: {type(t).__name__}")
-                if t.shape != group[0].shape:
-                    raise GnsError(2, f"{name}[{i}] has shape {tuple(t.shape)}, "
-                                      f"{names[0]}[{i}] has {tuple(group[0].shape)}")
-                _device_tensor(f"{name}[{i}]", t, self.device)
-                self.device = t.device
-            if group[0].numel() == 0:
-                form = 0, 0, [0] * self.arrays
-            else:
-                form = _rows(group)
+        # column by column: a list is built again whenever a program replaces
+        # its gradients, and may have thousands of them
+        entries = np.zeros((self.arrays, max(1, count)), dtype=_ENTRY)
+        shapes = None
+        dense = [True] * count
+        for k, (name, a) in enumerate(zip(names, arrays)):
+            if not all(isinstance(t, torch.Tensor) and t.layout is torch.strided for t in a):
+                i = next(i for i in range(count)
+                         if not isinstance(a[i], torch.Tensor) or a[i].layout is not torch.strided)
+                raise GnsError(1, f"{name}[{i}] is not a dense tensor: {type(a[i]).__name__}")
+            mine = [t.shape for t in a]
+            shapes = shapes or mine
+            if mine != shapes:
+                i = next(i for i in range(count) if mine[i] != shapes[i])
+                raise GnsError(2, f"{name}[{i}] has shape {tuple(mine[i])}, "
+                                  f"{names[0]}[{i}] has {tuple(shapes[i])}")
+            if count == 0:
+                continue
+            if {t.get_device() for t in a} != {arrays[0][0].get_device()} or not arrays[0][0].is_cuda:
+                for i, t in enumerate(a):
+                    _device_tensor(f"{name}[{i}]", t, arrays[0][0].device if k or i else None)
+            entries["data"][k] = [t.data_ptr() for t in a]
+            entries["dtype"][k] = [_DT[t.dtype] if t.dtype in _DT else _dtype_code(t.dtype) for t in a]
+            dense = [d and t.is_contiguous() for d, t in zip(dense, a)]
+        if count:
+            self.device = arrays[0][0].device
+            entries["rows"] = 1
+            entries["cols"] = entries["pitch"] = [t.numel() for t in arrays[0]]
+        for i in (i for i, d in enumerate(dense) if not d):
+            group = [a[i] for a in arrays]
+            form = _rows(group) if group[0].numel() else (1, 0, [0] * self.arrays)
             if form is None:
                 raise GnsError(2, f"{names[0]}[{i}]: strides {[t.stride() for t in group]} are not rows of "
                                   "consecutive elements that are the same for every array")
-            for a, t in enumerate(group):
-                entries[a * count + i] = Tensor(t.data_ptr(), form[0], form[1], form[2][a], _dtype_code(t.dtype))
+            entries["rows"][:, i], entries["cols"][:, i], entries["pitch"][:, i] = form
         L = lib()
-        nbytes = int(L.gns_tensor_list_bytes(entries, self.arrays, count))
+        nbytes = int(L.gns_tensor_list_bytes(entries.ctypes.data, self.arrays, count))
         self.info = ListInfo()
         image = torch.empty(max(nbytes, 16), dtype=torch.uint8, pin_memory=self.device is not None)
         as_floats = [None if s is None else (ctypes.c_float * max(1, count))(*s) for s in (lr_scales, wd_scales)]
-        _check(L.gns_tensor_list_build(entries, self.arrays, count, *as_floats, image.data_ptr(), image.numel(),
-                                       ctypes.byref(self.info)))
+        _check(L.gns_tensor_list_build(entries.ctypes.data, self.arrays, count, *as_floats, image.data_ptr(),
+                                       image.numel(), ctypes.byref(self.info)))
         self.count = count
         self.workspace_bytes = int(L.gns_tensor_list_workspace_bytes(ctypes.byref(self.info)))
         self._info = ctypes.byref(self.info)
