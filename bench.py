@@ -71,7 +71,7 @@ def short_kernel(name):
     for k in ("norm_partial", "row_partials", "scale_transpose", "scale_rows_f32", "transpose_sumsq",
               "norm_finish", "row_l1",
               "select_topk", "check_rows", "momentum_l1", "row_sumsq", "normuon_factors",
-              "dion3_update"):
+              "dion3_update", "list_partials", "list_finish", "list_scale", "list_adamw"):
         if k in name:
             return k
     return name.split("(")[0][:60]
@@ -272,7 +272,8 @@ def summarize_pmc(fetch_dir, write_dir, calib_mib, workload):
 
 HBM_KERNELS = ("norm_partial", "row_partials", "scale_transpose", "scale_rows_f32", "transpose_sumsq", "norm_finish",
                "momentum_l1",
-               "row_sumsq", "normuon_factors", "dion3_update", "select_topk")
+               "row_sumsq", "normuon_factors", "dion3_update", "select_topk",
+               "list_partials", "list_finish", "list_scale", "list_adamw")
 
 
 def mfma_from_profile(kernel, workload):
@@ -519,6 +520,57 @@ def bench_dion3_step(gns, synth, torch, w, coeffs, restarts, stream, steps=10):
             "hbm_kernels": kernels}
 
 
+def bench_lists(gns, torch, steps):
+    """The operators over lists of tensors: ms per call and the GB/s of the
+    bytes each cannot do without (every gradient read once, every output and
+    state read and written once).  Calls go round three copies of the tensors,
+    so that none finds its own data in the last-level cache."""
+    gen = torch.Generator(device="cuda").manual_seed(7)
+
+    def tensors(count, n, m, dtype, spread=0.01):
+        return [torch.empty(n, m, device="cuda").normal_(0.0, spread, generator=gen).to(dtype) for _ in range(count)]
+
+    def norm():
+        lst = gns.tensor_list(tensors(8, 4096, 16384, torch.bfloat16))
+        return lambda: gns.grad_norm(lst, max_norm=1.0), 2.0 * lst.info.elements
+
+    def clip():
+        g = tensors(16, 1024, 4096, torch.float16)
+        lst = gns.tensor_list(g, out=[torch.empty_like(t, dtype=torch.float32) for t in g])
+        return lambda: gns.clip_grad_norm_(lst, 1.0), 6.0 * lst.info.elements
+
+    def adamw():
+        lst = gns.adamw_list(tensors(2, 32768, 4096, torch.float32), tensors(2, 32768, 4096, torch.bfloat16),
+                             tensors(2, 32768, 4096, torch.float32, 1e-3),
+                             [t.square_() for t in tensors(2, 32768, 4096, torch.float32, 1e-3)],
+                             copies=tensors(2, 32768, 4096, torch.bfloat16))
+
+        def step():
+            got = gns.grad_norm(lst, max_norm=1.0)
+            gns.adamw_step(lst, 10, lr=1e-3, weight_decay=0.1, grad_scale=got.clip)
+        return step, 28.0 * lst.info.elements
+
+    out = {}
+    for name, make in (("grad_norm 8 x 4096x16384 bf16", norm), ("clip 16 x 1024x4096 fp16 to fp32", clip),
+                       ("grad_norm + adamw 2 x 32768x4096, bf16 gradients and copies", adamw)):
+        log(f"timing {name}")
+        calls = [make() for _ in range(3)]
+        for f, _ in calls:
+            f()
+        torch.cuda.synchronize()
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        e0.record()
+        for i in range(steps):
+            calls[i % 3][0]()
+        e1.record()
+        torch.cuda.synchronize()
+        ms = e0.elapsed_time(e1) / steps
+        out[name] = {"ms": round(ms, 4), "gbs": round(calls[0][1] / (ms / 1e3) / 1e9, 1)}
+        del calls
+        torch.cuda.empty_cache()
+    return out
+
+
 def desc_of(cfg):
     return {
         2: "16 x 1024x4096 bf16, log-uniform spectrum [1e-4,1]",
@@ -543,6 +595,8 @@ def main():
     ap.add_argument("--no-cpu", action="store_true", help="skip the CPU oracle baseline")
     ap.add_argument("--no-dion3", action="store_true",
                     help="skip the timing of the whole Dion3 update (f = 1/4) on the workload's shape")
+    ap.add_argument("--only-lists", action="store_true",
+                    help="time only the operators over lists of tensors (gradient norm, clipping, AdamW)")
     ap.add_argument("--only-dion3", action="store_true",
                     help="time only the whole Dion3 update on the workload's shape (for profiles)")
     ap.add_argument("--calib-copy-mib", type=int, default=0,
@@ -610,6 +664,9 @@ def main():
     T, restarts = 5, (2,)
     cdt = {"bf16": torch.bfloat16, "f16": torch.float16, "bf16x3": "bf16x3"}[args.compute]
 
+    if args.only_lists:
+        print(json.dumps({"lists": bench_lists(gns, torch, args.steps)}), flush=True)
+        return
     if args.only_dion3:
         print(json.dumps({"dion3_step": bench_dion3_step(gns, synth, torch, w, coeffs, restarts,
                                                          torch.cuda.current_stream(), steps=args.steps)}),

@@ -76,7 +76,9 @@ def _rows(group: Sequence[torch.Tensor]):
 
 class TensorList:
     """Arrays of tensors of the same shapes, ready for the calls on them (see
-    :func:`tensor_list` and :func:`adamw_list`).  Keeps the tensors alive."""
+    :func:`tensor_list` and :func:`adamw_list`).  Keeps the tensors alive.
+    Build it before a graph capture that uses it, and keep it as long as the
+    graph is replayed."""
 
     def __init__(self, arrays: Sequence[Sequence[torch.Tensor]], names: Sequence[str],
                  lr_scales: Optional[Sequence[float]] = None, wd_scales: Optional[Sequence[float]] = None):
@@ -152,13 +154,13 @@ class TensorList:
 
     def _workspace(self, raw: int) -> torch.Tensor:
         """The workspace of calls on one stream (those of different streams may
-        overlap in time).  A capture takes one of its own, which its graph
-        then keeps."""
+        overlap in time).  A captured call has one of its own: its graph may be
+        replayed beside other calls."""
+        if torch.cuda.is_current_stream_capturing():
+            return torch.zeros(self.workspace_bytes, dtype=torch.uint8, device=self.device)
         ws = self._workspaces.get(raw)
         if ws is None:
-            ws = torch.zeros(self.workspace_bytes, dtype=torch.uint8, device=self.device)
-            if not torch.cuda.is_current_stream_capturing():
-                self._workspaces[raw] = ws
+            ws = self._workspaces[raw] = torch.zeros(self.workspace_bytes, dtype=torch.uint8, device=self.device)
         return ws
 
     def _external(self, raw: int):

@@ -187,6 +187,106 @@ def test_clip_views_into_views():
     assert torch.equal(d.cpu(), dst)
 
 
+def test_clip_dense_into_slices_and_back():
+    """Dense gradients into column slices, and slices into dense outputs."""
+    gns = need_gpu()
+    rng = np.random.default_rng(75)
+    for src, dst in ((torch.bfloat16, torch.float32), (torch.float32, torch.float16)):
+        g = rand(rng, (97, 45), 0.5, src)
+        wide = torch.full((97, 60), 3.0, dtype=dst, device="cuda")
+        say("dense into slices", src, dst)
+        got = gns.clip_grad_norm_(gns.tensor_list([g.cuda()], out=[wide[:, 7:52]]), 0.5)
+        want = (g.float() * got.clip.cpu()).to(dst)
+        assert torch.equal(wide[:, 7:52].cpu(), want)
+        assert bool((wide[:, :7] == 3.0).all()) and bool((wide[:, 52:] == 3.0).all())
+        dense = torch.zeros(97, 45, dtype=dst, device="cuda")
+        big = torch.zeros(97, 60, dtype=src, device="cuda")
+        big[:, 7:52] = g.cuda()
+        gns.clip_grad_norm_(gns.tensor_list([big[:, 7:52]], out=[dense]), 0.5)
+        assert torch.equal(dense.cpu(), want)
+
+
+@pytest.mark.parametrize("offset", [0, 1, 3, 31, 64])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_chunk_edges(offset, dtype):
+    """Lengths around whole chunks, from starts of every alignment: each
+    element is read and scaled exactly once, and nothing around it is."""
+    gns = need_gpu()
+    rng = np.random.default_rng(76)
+    lengths = [8192 * k + d for k in (1, 2, 3) for d in (-65, -1, 0, 1, 63, 64)]
+    flat = rand(rng, sum(lengths) + 200 * len(lengths), 0.5, dtype)
+    dev, cpu = flat.cuda(), flat.clone()
+
+    def views(base):
+        out, at = [], 0
+        for n in lengths:
+            out.append(base[at + offset:at + offset + n])
+            at += n + 200
+        return out
+
+    say("chunk edges", offset, dtype)
+    got = gns.grad_norm(views(dev), max_norm=10.0, per_tensor=True)
+    check_norm(got, views(cpu), 2, 10.0, each=got.tensor_norms)
+    got = gns.clip_grad_norm_(views(dev), 10.0)
+    for t in views(cpu):
+        t.copy_((t.float() * got.clip.cpu()).to(dtype))
+    assert torch.equal(dev.cpu(), cpu)
+    for n in (8192 * 3 + 1, 5, 8192):
+        p, m, v = (torch.zeros(n + 300, device="cuda") for _ in range(3))
+        g = rand(rng, n, 0.5, dtype).cuda()
+        view = [[t[offset:offset + n]] for t in (p, m, v)]
+        gns.adamw_step(gns.adamw_list(view[0], [g], view[1], view[2]), 1, lr=0.5, weight_decay=0.0)
+        # the first step from zero moves every parameter by -lr g / (|g| + eps)
+        want = -0.5 * g.double() / (g.double().abs() + 1e-8)
+        assert torch.allclose(p[offset:offset + n].double(), want, rtol=0, atol=1e-4)
+        assert not p[:offset].any() and not p[offset + n:].any()
+        assert not m[:offset].any() and not v[offset + n:].any()
+
+
+@pytest.mark.parametrize("chunks", [127, 128, 129, 4096, 4097])
+@pytest.mark.parametrize("ord", [2, math.inf])
+def test_number_of_chunks(chunks, ord):
+    """Around the numbers of chunks at which the sum of the partials moves from
+    one launch to another: `chunks` tensors of one chunk each."""
+    gns = need_gpu()
+    rng = np.random.default_rng(77)
+    values = rand(rng, (chunks, 5), 0.5, torch.float32)
+    dev = values.cuda()
+    say("number of chunks", chunks, ord)
+    lst = gns.tensor_list(list(dev))
+    assert lst.info.chunks == chunks
+    for per_tensor in (False, True):
+        got = gns.grad_norm(lst, ord=ord, max_norm=1.0, per_tensor=per_tensor)
+        check_norm(got, list(values), ord, 1.0, each=got.tensor_norms)
+    got = gns.clip_grad_norm_(lst, 1.0, ord=ord)
+    check_norm(got, list(values), ord, 1.0)
+    assert torch.equal(dev.cpu(), values * got.clip.cpu())
+
+
+def test_list_beyond_the_cache():
+    """More gradients than the last-level cache holds (loads of both kinds,
+    chunks in parts), of odd sizes; against torch in fp64 and to the bit."""
+    gns = need_gpu()
+    gen = torch.Generator(device="cuda").manual_seed(78)
+    for dtype, out_dtype in ((torch.bfloat16, torch.float32), (torch.bfloat16, None), (torch.float32, torch.bfloat16)):
+        sizes = (70000001, 90000, 81234567) if dtype == torch.bfloat16 else (70000001, 90000, 3)
+        g = [torch.empty(n, device="cuda").normal_(0, 0.01, generator=gen).to(dtype) for n in sizes]
+        out = None if out_dtype is None else [torch.zeros(n, dtype=out_dtype, device="cuda") for n in sizes]
+        lst = gns.tensor_list(g, out=out)
+        assert lst.info.keep_from > 0
+        norms = [float(t.double().square().sum().sqrt()) for t in g]
+        norm = math.sqrt(sum(n * n for n in norms))
+        say("beyond the cache", dtype, out_dtype)
+        got = gns.grad_norm(lst, max_norm=1.0, per_tensor=True)
+        assert abs(float(got.norm) - norm) <= 1.01 * U * norm
+        for a, b in zip(got.tensor_norms.tolist(), norms):
+            assert abs(a - b) <= 1.01 * U * b
+        want = [(t.float() * got.clip).to(out_dtype or dtype) for t in g]
+        gns.clip_grad_norm_(lst, 1.0)
+        for a, b in zip(out or g, want):
+            assert torch.equal(a, b)
+
+
 def test_clip_below_the_bound_changes_nothing():
     gns = need_gpu()
     rng = np.random.default_rng(54)
