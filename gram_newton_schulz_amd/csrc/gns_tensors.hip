@@ -18,12 +18,17 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Norms of up to this many chunks are one launch: the workgroup that ends last
-// adds the partials up.  Counting the workgroups costs an atomic and its
-// fences in each, which line up on one address: 24 tensors of 1024 elements
-// 12.8 -> 9.4 us per call, 512 chunks no different, 1024 chunks 4 us more and
-// 16384 chunks 800 us more than a second launch of one workgroup.
-constexpr int64_t kFinishChunks = 128, kFinishCount = 4096;
+// Norms of up to this many chunks are one launch (list_norm_once), where the
+// workgroup that ends last adds the partials up: a call is bound by its
+// launches there, and one instead of two takes a list of 24 x 1024 fp32 from
+// 12.8 to 8.1 us, of 4M elements (512 chunks) from 10.8 to 8.1 (bf16) and 8.8
+// (fp32).  Each workgroup pays an atomic and its fences, which line up on one
+// address, so there are few, of four chunks each: with 1024 chunks there is
+// nothing to gain, 2048 cost 4 us, and with a workgroup for each of 16384
+// chunks it was 800 us.
+constexpr int64_t kOnceChunks = 512, kOnceEntries = 4096, kOnceGrid = kOnceChunks / 4;
+// Entries of more chunks have their norm added up by a wave instead of a thread.
+constexpr uint32_t kLargeEntry = 16;
 
 // Up to this many partials are added up by every workgroup of the scaling
 // itself, which saves the launch between: 3 x 513x777 13.9 -> 11.5 us per
@@ -204,6 +209,9 @@ __device__ __forceinline__ Span span_of(const ListEntry &e, uint32_t index, int6
   return s;
 }
 
+// Which of the kThreads threads that share a chunk this is.
+__device__ __forceinline__ int thread_of_chunk() { return threadIdx.x % kThreads; }
+
 // A dense chunk by this thread: block(i, stride) takes U pieces of V elements
 // (it can issue all their loads first), whole(i) one piece, and one(i) one
 // element, at the two ends.
@@ -211,10 +219,10 @@ template <int V, int U, class Block, class Whole, class One>
 __device__ __forceinline__ void each_dense(const Span &s, Block block, Whole whole, One one) {
   constexpr int step = kThreads * V;
   const int end = s.head + (s.n - s.head) / V * V;
-  int i = s.head + threadIdx.x * V;
+  int i = s.head + thread_of_chunk() * V;
   for (; i + (U - 1) * step < end; i += U * step) block(i, step);
   for (; i < end; i += step) whole(i);
-  const int t = threadIdx.x;
+  const int t = thread_of_chunk();
   if (t < s.head) one(t);
   if (t < s.n - end) one(end + t);
 }
@@ -225,7 +233,7 @@ __device__ __forceinline__ void each_unit(const ListEntry &e, const Span &s, F f
   const int64_t row0 = s.first / e.per_row;
   const int64_t at0 = s.first - row0 * e.per_row;
   const bool narrow = e.per_row < (int64_t(1) << 30);   // 32-bit division
-  for (int u = threadIdx.x; u < s.n; u += kThreads) {
+  for (int u = thread_of_chunk(); u < s.n; u += kThreads) {
     int64_t r, q;
     if (narrow) {
       const uint32_t at = static_cast<uint32_t>(at0) + u;
@@ -243,36 +251,28 @@ __device__ __forceinline__ void each_unit(const ListEntry &e, const Span &s, F f
   }
 }
 
-// Sum (or maximum) over a workgroup of up to 16 waves, in a fixed order; the
-// result is thread 0's.
-__device__ __forceinline__ double block_sum(double x) {
-  __shared__ double part[16];
-  for (int off = 32; off > 0; off >>= 1) x += __shfl_down(x, off, 64);
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = x;
-  __syncthreads();
-  if (threadIdx.x == 0)
-    for (unsigned w = 1; w < (blockDim.x + 63) / 64; ++w) x += part[w];
-  return x;
+// Partials are 64 bits: a sum of squares (fp64), or with MAX the bits of the
+// largest magnitude as a float.  Zero bits are zero for both.
+template <bool MAX> __device__ __forceinline__ uint64_t join(uint64_t a, uint64_t b) {
+  if constexpr (MAX) return max(static_cast<uint32_t>(a), static_cast<uint32_t>(b));
+  else return __double_as_longlong(__longlong_as_double(a) + __longlong_as_double(b));
 }
-__device__ __forceinline__ uint32_t block_max(uint32_t x) {
-  __shared__ uint32_t part[16];
-  for (int off = 32; off > 0; off >>= 1) x = max(x, static_cast<uint32_t>(__shfl_down(x, off, 64)));
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = x;
-  __syncthreads();
-  if (threadIdx.x == 0)
-    for (unsigned w = 1; w < (blockDim.x + 63) / 64; ++w) x = max(x, part[w]);
-  return x;
+template <bool MAX> __device__ __forceinline__ double norm_of_total(uint64_t bits) {
+  if constexpr (MAX) return __uint_as_float(static_cast<uint32_t>(bits));
+  else return sqrt(__longlong_as_double(bits));
+}
+
+// Sum (or maximum) over a wave, in a fixed order; the first lane's.
+template <bool MAX>
+__device__ __forceinline__ uint64_t wave_total(uint64_t bits) {
+  for (int off = 32; off > 0; off >>= 1)
+    bits = join<MAX>(bits, __shfl_down(static_cast<unsigned long long>(bits), off, 64));
+  return bits;
 }
 
 // The magnitudes of floats order as their bits without the sign do, with NaN
 // above infinity: an integer maximum keeps a NaN.
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
-
-// A partial is stored where the workgroup that adds them up sees it, on
-// whichever XCD it runs.
-__device__ __forceinline__ void put_partial(uint64_t *out, uint64_t bits) {
-  __hip_atomic_store(out, bits, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
 
 // What one thread has of a chunk's norm: a sum of squares, or the largest
 // magnitude.
@@ -295,10 +295,7 @@ template <class E> struct NormPart<E, false> {
     const double x = E::ld(v);
     acc = fma(x, x, acc);
   }
-  __device__ void finish(uint64_t *out) {
-    const double t = block_sum(acc + acc2);
-    if (threadIdx.x == 0) put_partial(out, __double_as_longlong(t));
-  }
+  __device__ uint64_t bits() const { return __double_as_longlong(acc + acc2); }
 };
 template <class E> struct NormPart<E, true> {
   uint32_t top = 0;
@@ -312,49 +309,34 @@ template <class E> struct NormPart<E, true> {
     for (int i = 0; i < V; ++i) top = max(top, magnitude(x[i]));
   }
   __device__ void add_one(typename E::S v) { top = max(top, magnitude(E::ld(v))); }
-  __device__ void finish(uint64_t *out) {
-    const uint32_t t = block_max(top);
-    if (threadIdx.x == 0) put_partial(out, t);
-  }
+  __device__ uint64_t bits() const { return top; }
 };
 
-// Total over `n` partials by the `threads` threads of which this is number
-// `t`, before the reduction over them.
+// Total of `n` partials, this thread's share as number `t` of `threads`.
 template <bool MAX>
-__device__ __forceinline__ void add_partials(const uint64_t *p, int64_t n, int t, int threads, double &acc,
-                                             uint32_t &top) {
+__device__ __forceinline__ uint64_t partials_of(const uint64_t *p, int64_t n, int t, int threads) {
   constexpr int kAtOnce = 16;   // loads in flight per thread
+  uint64_t total = 0;
   for (int64_t i = t; i < n; i += kAtOnce * threads) {
     uint64_t x[kAtOnce];
 #pragma unroll
-    for (int u = 0; u < kAtOnce; ++u) {
-      const int64_t at = i + u * threads;
-      // from where every XCD sees it, whichever wrote it
-      x[u] = at < n ? __hip_atomic_load(p + at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
-    }
+    for (int u = 0; u < kAtOnce; ++u) x[u] = i + u * threads < n ? p[i + u * threads] : 0;
 #pragma unroll
-    for (int u = 0; u < kAtOnce; ++u) {
-      if constexpr (MAX) top = max(top, static_cast<uint32_t>(x[u]));
-      else acc += __longlong_as_double(x[u]);
-    }
+    for (int u = 0; u < kAtOnce; ++u) total = join<MAX>(total, x[u]);
   }
+  return total;
 }
 
-// Norm (thread 0's) of one partial per thread.
-template <bool MAX>
-__device__ __forceinline__ double norm_of(uint64_t bits) {
-  if constexpr (MAX) return __uint_as_float(block_max(static_cast<uint32_t>(bits)));
-  else return sqrt(block_sum(__longlong_as_double(bits)));
-}
-
-// Norm of all `n` partials (thread 0's), by the whole workgroup.
+// Norm of `n` partials (thread 0's), by the whole workgroup of up to 16 waves.
 template <bool MAX>
 __device__ __forceinline__ double norm_of(const uint64_t *partials, int64_t n) {
-  double acc = 0.0;
-  uint32_t top = 0;
-  add_partials<MAX>(partials, n, threadIdx.x, blockDim.x, acc, top);
-  if constexpr (MAX) return __uint_as_float(block_max(top));
-  else return sqrt(block_sum(acc));
+  __shared__ uint64_t part[16];
+  uint64_t total = wave_total<MAX>(partials_of<MAX>(partials, n, threadIdx.x, blockDim.x));
+  if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = total;
+  __syncthreads();
+  if (threadIdx.x == 0)
+    for (unsigned w = 1; w < blockDim.x / 64; ++w) total = join<MAX>(total, part[w]);
+  return norm_of_total<MAX>(total);
 }
 
 // The result's {norm, clip factor} from the norm of the stored gradients.
@@ -374,15 +356,13 @@ __device__ __forceinline__ void write_result(const NormArgs &a, double raw) {
   a.result[1] = r.y;
 }
 
-// partials[c] of every chunk c.  With FINISH the workgroup that stores the
-// last of them adds them up, in the order of the chunks, and writes the
-// result and the entries' norms; it leaves *arrived at zero, as it found it.
-template <bool MAX, bool FINISH>
-__global__ void __launch_bounds__(kThreads)
-list_partials(ListView v, uint64_t *partials, uint32_t *arrived, NormArgs args, float *tensor_norms) {
-  const ListChunk ch = v.chunks[blockIdx.x];
+// This thread's share of chunk c's norm.
+template <bool MAX>
+__device__ __forceinline__ uint64_t chunk_part(const ListView &v, int64_t c) {
+  const ListChunk ch = v.chunks[c];
   const ListEntry &e = v.entries[ch.entry];
   const Span s = span_of(e, ch.index, v.chunk_units, 0);
+  uint64_t bits = 0;
   with_type(e.dtype[0], [&](auto type) {
     using E = decltype(type);
     using S = typename E::S;
@@ -409,7 +389,7 @@ list_partials(ListView v, uint64_t *partials, uint32_t *arrived, NormArgs args, 
           },
           [&](int i) { part.template add<V>(ld_raw<E, V, ONCE>(p + i)); }, [&](int i) { part.add_one(ld_one(p + i)); });
     };
-    if (s.dense && blockIdx.x < v.keep_from) dense(std::true_type{});
+    if (s.dense && c < v.keep_from) dense(std::true_type{});
     else if (s.dense) dense(std::false_type{});
     else {
       const int64_t pitch = e.pitch[0];
@@ -419,35 +399,93 @@ list_partials(ListView v, uint64_t *partials, uint32_t *arrived, NormArgs args, 
         part.template add_values<kListUnit>(x);
       });
     }
-    part.finish(partials + blockIdx.x);
+    bits = part.bits();
   });
-  if constexpr (FINISH) {
-    __shared__ bool last;
-    if (threadIdx.x == 0)
-      last = __hip_atomic_fetch_add(arrived, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+  return bits;
+}
+
+// partials[c] of chunk c, one workgroup per chunk.
+template <bool MAX>
+__global__ void __launch_bounds__(kThreads) list_partials(ListView v, uint64_t *partials) {
+  __shared__ uint64_t part[kThreads / 64];
+  const uint64_t bits = wave_total<MAX>(chunk_part<MAX>(v, blockIdx.x));
+  if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = bits;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    uint64_t total = part[0];
+    for (int w = 1; w < kThreads / 64; ++w) total = join<MAX>(total, part[w]);
+    partials[blockIdx.x] = total;
+  }
+}
+
+// A norm in one launch, for lists of few chunks: kGroups chunks to a
+// workgroup at a time, and the workgroup that ends last adds the partials up
+// (in the order of the chunks) and writes the result and the entries' norms.
+// It leaves *arrived at zero, as it found it.
+constexpr int kGroups = 4;
+template <bool MAX>
+__global__ void __launch_bounds__(kGroups * kThreads)
+list_norm_once(ListView v, uint64_t *partials, uint32_t *arrived, NormArgs args, float *tensor_norms) {
+  constexpr int kWaves = kGroups * kThreads / 64;
+  __shared__ uint64_t part[kWaves];
+  const int t = threadIdx.x, wave = t / 64, n = static_cast<int>(v.n_chunks);
+  for (int c0 = blockIdx.x * kGroups; c0 < n; c0 += gridDim.x * kGroups) {
+    const int c = c0 + t / kThreads;
+    const uint64_t bits = wave_total<MAX>(c < n ? chunk_part<MAX>(v, c) : 0);
+    if (t % 64 == 0) part[wave] = bits;
     __syncthreads();
-    if (!last) return;
-    __shared__ uint64_t all[kFinishChunks];
-    const int t = threadIdx.x, n = static_cast<int>(v.n_chunks);
-    if (t < n) all[t] = __hip_atomic_load(partials + t, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __syncthreads();
-    const double norm = norm_of<MAX>(t < n ? all[t] : 0);
+    // one thread stores all of them, so that its release below covers them
     if (t == 0) {
-      write_result(args, norm);
-      __hip_atomic_store(arrived, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-    if (!tensor_norms) return;
-    const double s = unscale(args);
-    for (int64_t i = t; i < v.count; i += kThreads) {
-      const ListEntry &e = v.entries[i];
-      double acc = 0.0;
-      uint32_t top = 0;
-      for (uint32_t c = e.first_chunk; c < e.first_chunk + e.chunks; ++c) {
-        if constexpr (MAX) top = max(top, static_cast<uint32_t>(all[c]));
-        else acc += __longlong_as_double(all[c]);
+      for (int g = 0; g < kGroups && c0 + g < n; ++g) {
+        uint64_t total = part[g * (kWaves / kGroups)];
+        for (int w = 1; w < kWaves / kGroups; ++w) total = join<MAX>(total, part[g * (kWaves / kGroups) + w]);
+        __hip_atomic_store(partials + c0 + g, total, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       }
-      tensor_norms[i] = static_cast<float>((MAX ? static_cast<double>(__uint_as_float(top)) : sqrt(acc)) * s);
     }
+    __syncthreads();
+  }
+  __shared__ bool last;
+  if (t == 0)
+    last = __hip_atomic_fetch_add(arrived, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+  __syncthreads();
+  if (!last) return;
+  __shared__ uint64_t all[kOnceChunks];
+  __shared__ uint32_t large[kOnceChunks / kLargeEntry], n_large;
+  uint64_t mine = 0;
+  for (int c = t; c < n; c += kGroups * kThreads) {
+    all[c] = __hip_atomic_load(partials + c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    mine = join<MAX>(mine, all[c]);
+  }
+  if (t == 0) n_large = 0;
+  mine = wave_total<MAX>(mine);
+  if (t % 64 == 0) part[wave] = mine;
+  __syncthreads();
+  if (t == 0) {
+    uint64_t total = part[0];
+    for (int w = 1; w < kWaves; ++w) total = join<MAX>(total, part[w]);
+    write_result(args, norm_of_total<MAX>(total));
+    __hip_atomic_store(arrived, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  if (!tensor_norms) return;
+  // entries of few chunks by a thread, the others by a wave
+  const double s = unscale(args);
+  for (int64_t i = t; i < v.count; i += kGroups * kThreads) {
+    const uint32_t first = v.entries[i].first_chunk, count = v.entries[i].chunks;
+    if (count > kLargeEntry) {
+      large[atomicAdd(&n_large, 1u)] = static_cast<uint32_t>(i);
+      continue;
+    }
+    uint64_t total = 0;
+    for (uint32_t c = first; c < first + count; ++c) total = join<MAX>(total, all[c]);
+    tensor_norms[i] = static_cast<float>(norm_of_total<MAX>(total) * s);
+  }
+  __syncthreads();
+  for (uint32_t k = wave; k < n_large; k += kWaves) {
+    const ListEntry &e = v.entries[large[k]];
+    uint64_t total = 0;
+    for (uint32_t c = t % 64; c < e.chunks; c += 64) total = join<MAX>(total, all[e.first_chunk + c]);
+    total = wave_total<MAX>(total);
+    if (t % 64 == 0) tensor_norms[large[k]] = static_cast<float>(norm_of_total<MAX>(total) * s);
   }
 }
 
@@ -471,15 +509,9 @@ list_finish(ListView v, const uint64_t *partials, NormArgs args, float *tensor_n
   const int64_t i = (blockIdx.x - 1) * static_cast<int64_t>(blockDim.x / 64) + threadIdx.x / 64;
   if (i >= v.count) return;
   const ListEntry &e = v.entries[i];
-  double acc = 0.0;
-  uint32_t top = 0;
-  add_partials<MAX>(partials + e.first_chunk, e.chunks, threadIdx.x & 63, 64, acc, top);
-  for (int off = 32; off > 0; off >>= 1) {
-    acc += __shfl_down(acc, off, 64);
-    top = max(top, static_cast<uint32_t>(__shfl_down(top, off, 64)));
-  }
-  if ((threadIdx.x & 63) == 0)
-    tensor_norms[i] = static_cast<float>((MAX ? static_cast<double>(__uint_as_float(top)) : sqrt(acc)) * s);
+  const uint64_t total =
+      wave_total<MAX>(partials_of<MAX>(partials + e.first_chunk, e.chunks, threadIdx.x % 64, 64));
+  if (threadIdx.x % 64 == 0) tensor_norms[i] = static_cast<float>(norm_of_total<MAX>(total) * s);
 }
 
 // Array dst <- factor * array 0, one workgroup for each of `parts` parts of a
@@ -657,8 +689,8 @@ unsigned parts_of(const ListView &v, int64_t units) {
 hipError_t launch_partials(const ListView &v, bool max, uint64_t *partials, hipStream_t s) {
   if (v.n_chunks == 0) return hipSuccess;
   const dim3 grid(static_cast<unsigned>(v.n_chunks));
-  if (max) list_partials<true, false><<<grid, kThreads, 0, s>>>(v, partials, nullptr, NormArgs{}, nullptr);
-  else list_partials<false, false><<<grid, kThreads, 0, s>>>(v, partials, nullptr, NormArgs{}, nullptr);
+  if (max) list_partials<true><<<grid, kThreads, 0, s>>>(v, partials);
+  else list_partials<false><<<grid, kThreads, 0, s>>>(v, partials);
   return hipGetLastError();
 }
 
@@ -666,11 +698,12 @@ hipError_t launch_partials(const ListView &v, bool max, uint64_t *partials, hipS
 
 hipError_t launch_list_norm(const ListView &v, bool max, uint64_t *partials, uint32_t *arrived, const NormArgs &a,
                             float *tensor_norms, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>(v.n_chunks));
-  const bool one = v.n_chunks > 0 && v.n_chunks <= kFinishChunks && (!tensor_norms || v.count <= kFinishCount);
-  if (one && max) list_partials<true, true><<<grid, kThreads, 0, s>>>(v, partials, arrived, a, tensor_norms);
-  else if (one) list_partials<false, true><<<grid, kThreads, 0, s>>>(v, partials, arrived, a, tensor_norms);
-  if (one) return hipGetLastError();
+  if (v.n_chunks > 0 && v.n_chunks <= kOnceChunks && (!tensor_norms || v.count <= kOnceEntries)) {
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>((v.n_chunks + kGroups - 1) / kGroups, kOnceGrid)));
+    if (max) list_norm_once<true><<<grid, kGroups * kThreads, 0, s>>>(v, partials, arrived, a, tensor_norms);
+    else list_norm_once<false><<<grid, kGroups * kThreads, 0, s>>>(v, partials, arrived, a, tensor_norms);
+    return hipGetLastError();
+  }
   hipError_t e = launch_partials(v, max, partials, s);
   if (e != hipSuccess) return e;
   const unsigned threads = v.n_chunks > 256 ? 1024 : 256;

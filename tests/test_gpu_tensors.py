@@ -243,7 +243,7 @@ def test_chunk_edges(offset, dtype):
         assert not m[:offset].any() and not v[offset + n:].any()
 
 
-@pytest.mark.parametrize("chunks", [127, 128, 129, 4096, 4097])
+@pytest.mark.parametrize("chunks", [3, 4, 5, 511, 512, 513, 4096, 4097])
 @pytest.mark.parametrize("ord", [2, math.inf])
 def test_number_of_chunks(chunks, ord):
     """Around the numbers of chunks at which the sum of the partials moves from
@@ -261,6 +261,22 @@ def test_number_of_chunks(chunks, ord):
     got = gns.clip_grad_norm_(lst, 1.0, ord=ord)
     check_norm(got, list(values), ord, 1.0)
     assert torch.equal(dev.cpu(), values * got.clip.cpu())
+
+
+def test_small_list_of_large_and_small_entries():
+    """One launch, entries of one, of a few and of many chunks."""
+    gns = need_gpu()
+    rng = np.random.default_rng(79)
+    sizes = [3, 8192 * 40 + 17, 0, 8192 * 3, 1, 8192 * 17, 8192 * 200 + 5, 8192 * 16 + 1, 9000]
+    grads = [rand(rng, n, 0.1 * (i + 1), DTYPES[i % 3]) for i, n in enumerate(sizes)]
+    dev = [g.cuda() for g in grads]
+    for ord in (2, math.inf):
+        say("large and small entries", ord)
+        lst = gns.tensor_list(dev)
+        assert 128 < lst.info.chunks <= 512
+        for _ in range(3):
+            got = gns.grad_norm(lst, ord=ord, max_norm=1.0, per_tensor=True)
+            check_norm(got, grads, ord, 1.0, each=got.tensor_norms)
 
 
 def test_list_beyond_the_cache():
