@@ -91,7 +91,10 @@ __device__ __forceinline__ RawOf<E, V> ld_raw(const typename E::S *p) {
   R r;
   const GNS_GLOBAL typename R::T *q = (const GNS_GLOBAL typename R::T *)p;
 #pragma unroll
-  for (unsigned i = 0; i < sizeof(R) / sizeof(typename R::T); ++i) r.v[i] = NT ? __builtin_nontemporal_load(q + i) : q[i];
+  for (unsigned i = 0; i < sizeof(R) / sizeof(typename R::T); ++i) {
+    if constexpr (NT) r.v[i] = __builtin_nontemporal_load(q + i);
+    else r.v[i] = q[i];
+  }
   return r;
 }
 template <class E, int V, bool NT>
@@ -99,8 +102,10 @@ __device__ __forceinline__ void st_raw(typename E::S *p, const RawOf<E, V> &r) {
   using R = RawOf<E, V>;
   GNS_GLOBAL typename R::T *q = (GNS_GLOBAL typename R::T *)p;
 #pragma unroll
-  for (unsigned i = 0; i < sizeof(R) / sizeof(typename R::T); ++i) if constexpr (NT) __builtin_nontemporal_store(r.v[i], q + i);
+  for (unsigned i = 0; i < sizeof(R) / sizeof(typename R::T); ++i) {
+    if constexpr (NT) __builtin_nontemporal_store(r.v[i], q + i);
     else q[i] = r.v[i];
+  }
 }
 template <class R> __device__ __forceinline__ uint32_t word(const R &r, int i) {
   constexpr int W = sizeof(typename R::T) / 4;
@@ -176,12 +181,17 @@ __device__ __forceinline__ void with_type(int dtype, F f) {
 // A chunk of an entry.  Dense: `n` elements from element `first` of the only
 // row.  Otherwise units [first, first + n), found row by row.
 //
-// Dense chunks are shifted so that array `a` is whole cache lines from element
-// `head` of the chunk on (head > 0 in an entry's first chunk only): tensors
-// packed behind one another start anywhere, and stores that end inside a line
-// leave partial lines behind (AdamW of 200 packed tensors, 8.9M elements:
-// 65.6 -> 63 us).  Arrays of another phase are accessed across lines.
-constexpr int kLine = 128;
+// Dense chunks are shifted so that array `a` starts on a multiple of kStart
+// bytes from element `head` of the chunk on (head > 0 in an entry's first chunk
+// only): tensors packed behind one another start anywhere, and stores that end
+// inside a cache line leave partial lines behind.  Two lines of 128 bytes,
+// so that a 16-bit array at the same offset in its own buffer starts on one.
+// Without the shift, with 128 bytes, with 256: AdamW of 200 packed fp32
+// tensors (8.9M elements) 57.2, 53.4, 53.2 us; of 60 with bf16 gradients and
+// copies (27M) 150, 131, 129; clipping their gradients into fp32 42.3, 39.7,
+// 35.4.  Arrays of another phase are accessed across lines.
+constexpr int kStart = 256;
+static_assert(kStart / 2 <= kThreads, "a thread for every element of a head");
 struct Span {
   int64_t first;
   int n, head;
@@ -195,7 +205,7 @@ __device__ __forceinline__ Span span_of(const ListEntry &e, uint32_t index, int6
   if (s.dense) {
     const uint32_t size = e.dtype[a] == DT_F32 ? 4 : 2;
     const int shift = static_cast<int>((0u - static_cast<uint32_t>(reinterpret_cast<uintptr_t>(e.data[a]))) %
-                                       kLine / size);
+                                       kStart / size);
     const int64_t end = (u0 + chunk_units) * kListUnit + shift;
     s.first = index ? u0 * kListUnit + shift : 0;
     const int64_t n = (end < e.cols ? end : e.cols) - s.first;
@@ -345,7 +355,7 @@ __device__ __forceinline__ double unscale(const NormArgs &a) {
 }
 __device__ __forceinline__ float2 result_of(const NormArgs &a, double raw) {
   const double s = unscale(a);
-  const double norm = raw * s;
+  const double norm = raw * fabs(s);
   const double ratio = a.max_norm / (norm + a.eps);
   return make_float2(static_cast<float>(norm),
                      isfinite(norm) ? static_cast<float>(s * (ratio < 1.0 ? ratio : 1.0)) : __builtin_nanf(""));
@@ -456,7 +466,8 @@ __device__ __forceinline__ void scale_chunk(const ListView &v, int dst, float f,
 #pragma unroll
               for (int u = 0; u < kUnroll; ++u) put(i + u * step, r[u]);
             },
-            [&](int i) { put(i, ld_raw<A, V, true>(p + i)); }, [&](int i) { st_one(q + i, B::st(A::ld(ld_one(p + i)) * f)); });
+            [&](int i) { put(i, ld_raw<A, V, true>(p + i)); },
+            [&](int i) { st_one(q + i, B::st(A::ld(ld_one(p + i)) * f)); });
       } else {
         each_unit(e, s, [&](int64_t r, int64_t c, int n) {
           const SA *p = x + r * e.pitch[0] + c;
@@ -541,7 +552,7 @@ list_norm_once(ListView v, uint64_t *partials, uint32_t *arrived, NormArgs args,
   }
   if (!tensor_norms) return;
   // entries of few chunks by a thread, the others by a wave
-  const double s = unscale(args);
+  const double s = fabs(unscale(args));
   for (int64_t i = t; i < v.count; i += kGroups * kThreads) {
     const uint32_t first = v.entries[i].first_chunk, count = v.entries[i].chunks;
     if (count > kLargeEntry) {
@@ -572,7 +583,7 @@ list_finish(ListView v, const uint64_t *partials, NormArgs args, float *tensor_n
     if (threadIdx.x == 0) write_result(args, norm);
     return;
   }
-  const double s = unscale(args);
+  const double s = fabs(unscale(args));
   if (!per_wave) {
     const ListEntry &e = v.entries[blockIdx.x - 1];
     const double norm = norm_of<MAX>(partials + e.first_chunk, e.chunks) * s;
@@ -625,7 +636,8 @@ struct AdamwRule {
 };
 
 template <bool COPY>
-__global__ void __launch_bounds__(kThreads) list_adamw(ListView v, AdamwScalars h, const float *grad_scale, unsigned parts) {
+__global__ void __launch_bounds__(kThreads)
+list_adamw(ListView v, AdamwScalars h, const float *grad_scale, unsigned parts) {
   const float f = grad_scale ? *grad_scale : 1.0f;
   if (!isfinite(f)) return;
   const ListChunk ch = v.chunks[blockIdx.x / parts];
