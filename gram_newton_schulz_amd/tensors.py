@@ -247,6 +247,9 @@ def grad_norm(grads: Union[TensorList, Sequence[torch.Tensor]], *, ord: float = 
     result's ``clip`` to :func:`adamw_step` and ``dion3_step`` as
     ``grad_scale``, which then clip while they read the gradients.  When a
     gradient is not finite, ``clip`` is NaN and those steps change nothing.
+    With gradients sharded over ranks, gather the ranks' norms (taken with
+    ``inv_scale``) and call this on them as one tensor: its norm and ``clip``
+    are those of all gradients (times ``inv_scale`` once more for ``clip``).
     The list keeps a workspace for every stream it is used on; ``workspace``
     (uint8, ``workspace_bytes`` of the list, its first 256 bytes zero before
     the first use) takes its place."""

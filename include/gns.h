@@ -432,17 +432,19 @@ typedef struct {
  * A list is used through its table in device memory.  gns_tensor_list_bytes
  * gives the table's size (0 for arguments that gns_tensor_list_build refuses);
  * gns_tensor_list_build writes the table into host memory (`table`,
- * `table_bytes` of it, 16-byte aligned) and fills *list.  The caller copies it to device memory
- * (16-byte aligned) and passes that address with every call; the table holds the tensors' addresses,
- * so it is valid while they stay where they are.  It is only read: any
- * number of calls, on any streams, may share one.
+ * `table_bytes` of it, 16-byte aligned) and fills *list.  The caller copies it
+ * to device memory (16-byte aligned) and passes that address with every call.
+ * The table holds the tensors' addresses, so it is valid while they stay where
+ * they are.  It is only read: any number of calls, on any streams, may share
+ * one.
  *   tensors      (host) [arrays][count].
  *   lr_scale, wd_scale (host) [count] factors on the learning rate and on the
  *                weight decay of every entry (AdamW), or NULL for all ones.
  * GNS_E_SHAPE (arrays not 1, 2, 4 or 5, count outside 0..2^20, a negative or
  * overflowing size or pitch, entries of different shape), GNS_E_DTYPE,
  * GNS_E_NULL, GNS_E_PARAM (a misaligned address, or a scale that is not
- * finite), GNS_E_WORKSPACE (table_bytes too small).
+ * finite), GNS_E_WORKSPACE (table_bytes too small, or table misaligned),
+ * GNS_E_HIP (out of host memory).
  */
 size_t gns_tensor_list_bytes(const gns_tensor *tensors, int arrays, int64_t count);
 gns_status gns_tensor_list_build(const gns_tensor *tensors, int arrays, int64_t count, const float *lr_scale,
@@ -463,11 +465,12 @@ typedef enum {
  *   norm = || s g ||            s = *inv_scale (1 when NULL)
  *   clip = s min(1, max_norm / (norm + eps))
  * so that clip * g has the norm min(norm, max_norm) up to eps.  An empty list
- * has norm 0.
+ * has norm 0.  Gradients that are sharded over ranks: the norm (and clip
+ * factor) of the vector of the ranks' norms is that of all of them.
  *   table        (device) the list's table.
  *   max_norm     >= 0; INFINITY gives clip = s.
  *   eps          >= 0.
- *   inv_scale    (device) one float or NULL: the inverse of the loss scale.
+ *   inv_scale    (device) one float > 0 or NULL: the inverse of the loss scale.
  *   result       (device) two floats, written: {norm, clip}.  Where a gradient
  *                is Inf or NaN the norm is (the same as in a sum over them),
  *                and clip is NaN, which the calls that take it as a factor

@@ -476,6 +476,23 @@ def test_offsets_beyond_32_bits():
     assert int(torch.count_nonzero(base[5 + 701:5 + pitch])) == 0
 
 
+def test_norm_of_shards():
+    """Gradients in shards: the norm of the shards' norms is that of all of
+    them (each rounded once, so two roundings), and a shard's NaN reaches it."""
+    gns = need_gpu()
+    rng = np.random.default_rng(80)
+    shards = [[rand(rng, n, 0.3, torch.bfloat16) for n in sizes] for sizes in ((5000, 3), (70001,), (12, 9, 40000))]
+    for ord in (2, math.inf):
+        say("norm of shards", ord)
+        parts = torch.stack([gns.grad_norm([g.cuda() for g in shard], ord=ord).norm for shard in shards])
+        got = gns.grad_norm([parts], ord=ord, max_norm=1.0)
+        norm, clip, _ = oracle.grad_norm([f64(g) for shard in shards for g in shard], ord, 1.0)
+        assert abs(float(got.norm) - norm) <= 2.02 * U * norm
+        assert abs(float(got.clip) - clip) <= 2.02 * U * clip
+        parts[1] = math.nan
+        assert math.isnan(float(gns.grad_norm([parts], ord=ord, max_norm=1.0).clip))
+
+
 def test_repeats_are_identical():
     gns = need_gpu()
     rng = np.random.default_rng(66)
