@@ -279,6 +279,41 @@ def test_small_list_of_large_and_small_entries():
             check_norm(got, grads, ord, 1.0, each=got.tensor_norms)
 
 
+@pytest.mark.parametrize("count", [3, 600, 5000])
+@pytest.mark.parametrize("clip", [False, True])
+def test_writes_stay_inside(count, clip):
+    """Result, tensor norms and workspace of exactly their sizes inside larger
+    buffers, whose other bytes keep what they hold; the first 256 bytes of the
+    workspace are zero again after every call."""
+    gns = need_gpu()
+    L = gns.lib()
+    rng = np.random.default_rng(81)
+    values = rand(rng, (count, 40), 0.5, torch.float32)
+    dev = values.cuda()
+    lst = gns.tensor_list(list(dev))
+    need = lst.workspace_bytes
+    arena = torch.full((1024 + need + 1024,), 77, dtype=torch.uint8, device="cuda")
+    lo = -arena.data_ptr() % 256 + 256
+    arena[lo:lo + 256] = 0
+    floats = torch.full((count + 40,), 7.0, device="cuda")
+    result, norms = floats[8:10], floats[20:20 + count]
+    torch.cuda.synchronize()
+    say("writes stay inside", count, clip)
+    for _ in range(3):
+        dev.copy_(values)
+        st = (L.gns_grad_clip if clip else L.gns_grad_norm)(
+            lst._info, lst._table, 0, 1.0, 1e-6, None, result.data_ptr(), norms.data_ptr(),
+            arena.data_ptr() + lo, need, torch.cuda.current_stream().cuda_stream)
+        assert st == 0
+        norm, factor, each = oracle.grad_norm([f64(v) for v in values], 2, 1.0)
+        assert abs(float(result[0]) - norm) <= 1.01 * U * norm and abs(float(result[1]) - factor) <= 1.01 * U * factor
+        assert np.all(np.abs(f64(norms) - np.array(each)) <= 1.01 * U * np.array(each))
+        assert not arena[lo:lo + 256].any()
+    assert bool((arena[:lo] == 77).all()) and bool((arena[lo + need:] == 77).all())
+    assert bool((floats[:8] == 7.0).all()) and bool((floats[10:20] == 7.0).all())
+    assert bool((floats[20 + count:] == 7.0).all())
+
+
 def test_list_beyond_the_cache():
     """More gradients than the last-level cache holds (loads of both kinds,
     chunks in parts), of odd sizes; against torch in fp64 and to the bit."""
