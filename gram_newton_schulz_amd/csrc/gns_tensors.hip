@@ -40,9 +40,10 @@ constexpr int64_t kScaleChunks = 4096;
 // workgroup each.  The workgroups run in order, so short ones keep all of them
 // in a narrow window of every array that moves through memory, where long
 // ones each go their own way: AdamW of 268M elements with the norm before it
-// takes 1454 us with parts of 16384 elements, 1410 with 8192, 1367 with 4096,
-// 1254 with 2048 and 1270 with 1024, of 8.9M packed elements 57.0 with 8192
-// and 53.4 with 1024 (one 16-byte piece of each array per thread).
+// takes 1448 us with parts of 16384 elements, 1415 with 8192, 1391 with 4096,
+// 1372 with 2048, 1270 with 1024 (one 16-byte piece of each array per thread)
+// and 1288 with 512; of 8.9M packed elements 58.4 with 4096, 55.3, 53.3 and 55.0.
+// Its streaming hints belong to that: plain loads or stores take it to 1450.
 // Grids that walk the parts in a loop instead lose the window again
 // (clipping 64 x 2048x7168 bf16: 880 us one by one, 1010 to 1270 in loops).
 constexpr int64_t kAdamwUnits = 128;
