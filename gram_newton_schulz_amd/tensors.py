@@ -17,12 +17,10 @@ from typing import Optional, Sequence, Union
 import numpy as np
 import torch
 
-
 from .binding import GnsError, _DT, _check, _device_tensor, _dtype_code, _ptr, _scalar_ptr, lib
 
 NORM_L2, NORM_MAX = 0, 1
 _NORMS = {2: NORM_L2, math.inf: NORM_MAX}
-
 
 # the current stream's handle without the Stream object around it, which costs
 # 1.8 us of a call that takes 6
@@ -163,7 +161,10 @@ class TensorList:
             ws = self._workspaces[raw] = torch.zeros(self.workspace_bytes, dtype=torch.uint8, device=self.device)
         return ws
 
-    def _external(self, raw: int):
+    def _stream(self, raw: int):
+        """A stream object for a raw stream."""
+        if raw == 0:
+            return torch.cuda.default_stream(self.device)
         return torch.cuda.ExternalStream(raw, device=self.device)
 
     def _on(self, stream) -> int:
@@ -173,10 +174,11 @@ class TensorList:
         else:
             raw = stream if isinstance(stream, int) else stream.cuda_stream
         if raw != self._home:
-            other = self._external(raw)
-            if not torch.cuda.is_current_stream_capturing():
-                other.wait_event(self._ready)
-            self.table.record_stream(other)
+            with torch.cuda.stream(self._stream(raw)):
+                # (a capture begins after everything before it has ended)
+                if not torch.cuda.is_current_stream_capturing():
+                    self._ready.wait()
+                self.table.record_stream(torch.cuda.current_stream(self.device))
         return raw
 
 
@@ -228,7 +230,7 @@ def _norm_call(fn, grads, max_norm, ord, eps, inv_scale, per_tensor, workspace, 
         raise GnsError(11, f"ord must be 2 or inf, got {ord}")
     s = lst._on(stream)
     # allocated for the stream that the call runs on
-    with contextlib.nullcontext() if stream is None else torch.cuda.stream(lst._external(s)):
+    with contextlib.nullcontext() if stream is None else torch.cuda.stream(lst._stream(s)):
         result = torch.empty(2, dtype=torch.float32, device=lst.device)
         norms = torch.empty(lst.count, dtype=torch.float32, device=lst.device) if per_tensor else None
         ws = lst._workspace(s) if workspace is None else workspace

@@ -567,6 +567,49 @@ def test_other_streams():
     assert abs(float(one_shot.norm) - n64) <= 1.01 * U * n64
 
 
+def test_list_of_a_side_stream():
+    """A list built on a side stream, right behind the work that fills its
+    tensors, and used on the default stream once that is ordered."""
+    gns = need_gpu()
+    rng = np.random.default_rng(82)
+    g = rand(rng, 300001, 0.1, torch.float32)
+    src = g.cuda()
+    dev = torch.zeros(300001, device="cuda")
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    say("list of a side stream")
+    with torch.cuda.stream(side):
+        dev.copy_(src)
+        lst = gns.tensor_list([dev])
+        on_side = gns.grad_norm(lst).norm.clone()
+    torch.cuda.current_stream().wait_stream(side)
+    for stream in (None, 0, torch.cuda.default_stream()):
+        got = gns.grad_norm(lst, max_norm=1.0, stream=stream)
+        check_norm(got, [g], 2, 1.0)
+        assert float(got.norm) == float(on_side)
+
+
+def test_capture_by_stream_argument():
+    """A call captured through its stream argument, from a list whose home is
+    another stream."""
+    gns = need_gpu()
+    g = torch.full((5000,), 0.25, device="cuda")
+    lst = gns.tensor_list([g])
+    gns.grad_norm(lst)
+    torch.cuda.synchronize()
+    graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    say("capture by stream argument")
+    with torch.cuda.graph(graph, stream=stream):
+        got = gns.grad_norm(lst, max_norm=1.0, stream=stream)
+    for value in (0.25, 2.0, 0.5):
+        g.fill_(value)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        check_norm(got, [torch.full((5000,), value)], 2, 1.0)
+        check_norm(gns.grad_norm(lst, max_norm=1.0), [torch.full((5000,), value)], 2, 1.0)
+
+
 def test_graph_replay():
     """Norm, clip factor and AdamW captured into one graph; every replay equals
     the eager step bit for bit, with eager work between the replays."""
