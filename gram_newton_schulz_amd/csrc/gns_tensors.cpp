@@ -31,7 +31,7 @@ constexpr size_t kArrivedBytes = 256;   // of the workspace: the count of finish
 constexpr int64_t kMaxSpan = int64_t(1) << 58;       // elements between an entry's first and last: byte
                                                      // offsets fit an int64
 // What a norm leaves in the last-level cache for the pass after it (see
-// list_partials): all of its 256 MiB.  With 128, 192, 256 and 400 MB, and with
+// chunk_part): all of its 256 MiB.  With 128, 192, 256 and 400 MB, and with
 // everything read so, norm and AdamW of 67M fp32 gradients take 363, 353, 345,
 // 343 and 343 us, and a norm of 1.07 GB alone 161, 162, 164, 166 and 180.
 constexpr double kLastLevelCache = 256.0 * (1 << 20);
