@@ -397,7 +397,9 @@ gns_status gns_dion3_step_clipped(float *W, const void *G, const float *grad_sca
  *   5  the same and {copy}                            (a 16-bit copy of the
  *                                                     parameter, or fp32)
  * Gradients, outputs and copies may be GNS_F32, GNS_BF16 or GNS_F16, mixed
- * freely; parameters and moments are GNS_F32.
+ * freely; parameters and moments are GNS_F32.  Memory of the list that a call
+ * writes must not be the call's result, tensor_norms, workspace, inv_scale or
+ * grad_scale too (the overlaps within the list are checked, these are not).
  */
 typedef struct {
   void *data;     /* (device) element (0, 0); may be NULL when empty; aligned to
