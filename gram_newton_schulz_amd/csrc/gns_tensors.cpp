@@ -207,7 +207,8 @@ gns_status norm_and_clip(const gns_tensor_list *list, const void *table, gns_nor
       (reinterpret_cast<uintptr_t>(workspace) & 255))
     return GNS_E_WORKSPACE;
   const int dst = list->arrays == 2 ? 1 : 0;
-  if (clip && (overlap(list, dst, dst) || (dst && overlap(list, 0, dst)))) return GNS_E_ALIAS;
+  for (int a = 0; clip && a < list->arrays; ++a)
+    if (overlap(list, a, dst)) return GNS_E_ALIAS;
   const ListView v = view_of(list, table);
   uint32_t *arrived = static_cast<uint32_t *>(workspace);
   uint64_t *partials = reinterpret_cast<uint64_t *>(static_cast<unsigned char *>(workspace) + kArrivedBytes);

@@ -498,7 +498,8 @@ gns_status gns_grad_norm(const gns_tensor_list *list, const void *table, gns_nor
  * output.  In place, clip = 1 writes nothing.  With a norm that is not finite
  * nothing is written either (the gradients, or the output, keep what they
  * had).
- * GNS_E_ALIAS when written memory overlaps other memory of the list.
+ * GNS_E_ALIAS when written memory overlaps other memory of the list (in any of
+ * its arrays).
  */
 gns_status gns_grad_clip(const gns_tensor_list *list, const void *table, gns_norm kind, double max_norm,
                          double eps, const float *inv_scale, float *result, float *tensor_norms,
