@@ -12,6 +12,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import math
+import threading
 from typing import Optional, Sequence, Union
 
 import numpy as np
@@ -137,6 +138,7 @@ class TensorList:
         self.workspace_bytes = int(L.gns_tensor_list_workspace_bytes(ctypes.byref(self.info)))
         self._info = ctypes.byref(self.info)
         self._workspaces = {}
+        self._lock = threading.RLock()
         if self.device is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
         # the copy runs on the current stream; calls on other streams wait for it
@@ -153,7 +155,9 @@ class TensorList:
     def _workspace(self, raw: int) -> torch.Tensor:
         """The workspace of calls on one stream (those of different streams may
         overlap in time).  A captured call has one of its own: its graph may be
-        replayed beside other calls."""
+        replayed beside other calls.  Taken and used under the list's lock: a
+        call's launches hand partials over in it, and the library's call lets
+        other threads run."""
         if torch.cuda.is_current_stream_capturing():
             return torch.zeros(self.workspace_bytes, dtype=torch.uint8, device=self.device)
         ws = self._workspaces.get(raw)
@@ -229,14 +233,15 @@ def _norm_call(fn, grads, max_norm, ord, eps, inv_scale, per_tensor, workspace, 
     if ord not in _NORMS:
         raise GnsError(11, f"ord must be 2 or inf, got {ord}")
     s = lst._on(stream)
-    # allocated for the stream that the call runs on
-    with contextlib.nullcontext() if stream is None else torch.cuda.stream(lst._stream(s)):
-        result = torch.empty(2, dtype=torch.float32, device=lst.device)
-        norms = torch.empty(lst.count, dtype=torch.float32, device=lst.device) if per_tensor else None
-        ws = lst._workspace(s) if workspace is None else workspace
-    _check(fn(lst._info, lst._table, _NORMS[ord], float(max_norm), float(eps),
-              _scalar_ptr("inv_scale", inv_scale, lst.device), result.data_ptr(), _ptr(norms),
-              ws.data_ptr(), ws.numel(), s))
+    with lst._lock:
+        # allocated for the stream that the call runs on
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(lst._stream(s)):
+            result = torch.empty(2, dtype=torch.float32, device=lst.device)
+            norms = torch.empty(lst.count, dtype=torch.float32, device=lst.device) if per_tensor else None
+            ws = lst._workspace(s) if workspace is None else workspace
+        _check(fn(lst._info, lst._table, _NORMS[ord], float(max_norm), float(eps),
+                  _scalar_ptr("inv_scale", inv_scale, lst.device), result.data_ptr(), _ptr(norms),
+                  ws.data_ptr(), ws.numel(), s))
     return GradNorm(result, norms)
 
 
@@ -252,9 +257,9 @@ def grad_norm(grads: Union[TensorList, Sequence[torch.Tensor]], *, ord: float = 
     With gradients sharded over ranks, gather the ranks' norms (taken with
     ``inv_scale``) and call this on them as one tensor: its norm and ``clip``
     are those of all gradients (times ``inv_scale`` once more for ``clip``).
-    The list keeps a workspace for every stream it is used on; ``workspace``
-    (uint8, ``workspace_bytes`` of the list, its first 256 bytes zero before
-    the first use) takes its place."""
+    The list keeps a workspace for every stream it is used on, and threads may
+    share the list; ``workspace`` (uint8, ``workspace_bytes`` of the list, its
+    first 256 bytes zero before the first use) takes its place."""
     return _norm_call(lib().gns_grad_norm, grads, max_norm, ord, eps, inv_scale, per_tensor, workspace, stream)
 
 

@@ -50,8 +50,9 @@
  * - Results are deterministic for a fixed shape, dtype and option set (no
  *   atomics, fixed reduction order).
  * - batch == 0 is a no-op that returns GNS_OK (pointers may then be NULL).
- * - Calls that share one workspace must be ordered on one stream; calls with
- *   separate workspaces are independent and thread-safe.
+ * - Calls that share one workspace must be ordered on one stream and made one
+ *   after another (a call is several launches, and those of two threads must
+ *   not mix); calls with separate workspaces are independent and thread-safe.
  */
 #ifndef GNS_H_
 #define GNS_H_
