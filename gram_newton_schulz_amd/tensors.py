@@ -3,9 +3,10 @@ tensor of a model in a few launches (the C ABI's gns_tensor_list,
 gns_grad_norm, gns_grad_clip and gns_adamw_step).
 
 A :class:`TensorList` names its tensors once and is then passed to the calls,
-which take no per-tensor arguments.  It holds their addresses, so it serves
-while the tensors keep their memory: build it again after anything that
-replaces a ``.grad`` or a parameter.
+which take no per-tensor arguments and run on the tensors' device, whichever
+is current.  It holds their addresses, so it serves while the tensors keep
+their memory: build it again after anything that replaces a ``.grad`` or a
+parameter.
 """
 from __future__ import annotations
 
@@ -27,6 +28,7 @@ _NORMS = {2: NORM_L2, math.inf: NORM_MAX}
 # 1.8 us of a call that takes 6
 _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 class Tensor(ctypes.Structure):
@@ -172,11 +174,16 @@ class TensorList:
         return torch.cuda.ExternalStream(raw, device=self.device)
 
     def _on(self, stream) -> int:
-        """The raw stream a call runs on, ordered after the table's copy."""
+        """The raw stream a call runs on, ordered after the table's copy.  (A
+        raw handle is taken for one of the list's device.)"""
         if stream is None:
             raw = _current_raw_stream(self.device.index)
+        elif isinstance(stream, int):
+            raw = stream
         else:
-            raw = stream if isinstance(stream, int) else stream.cuda_stream
+            if stream.device.index != self.device.index:
+                raise GnsError(11, f"stream is on {stream.device}, the list on {self.device}")
+            raw = stream.cuda_stream
         if raw != self._home:
             with torch.cuda.stream(self._stream(raw)):
                 # (a capture begins after everything before it has ended)
@@ -232,6 +239,10 @@ def _norm_call(fn, grads, max_norm, ord, eps, inv_scale, per_tensor, workspace, 
     lst = grads if isinstance(grads, TensorList) else tensor_list(grads)
     if ord not in _NORMS:
         raise GnsError(11, f"ord must be 2 or inf, got {ord}")
+    # the library launches on the current device, where handle 0 is another stream
+    if _current_device() != lst.device.index:
+        with torch.cuda.device(lst.device):
+            return _norm_call(fn, lst, max_norm, ord, eps, inv_scale, per_tensor, workspace, stream)
     s = lst._on(stream)
     with lst._lock:
         # allocated for the stream that the call runs on
@@ -279,6 +290,10 @@ def adamw_step(tensors: TensorList, step: int, *, lr: float, betas: Sequence[flo
     ``step``-th (from 1), with decoupled weight decay (gns_adamw_step).
     ``grad_scale`` (a float32 on the GPU) multiplies the gradients; when it is
     not finite nothing changes."""
+    if _current_device() != tensors.device.index:
+        with torch.cuda.device(tensors.device):
+            return adamw_step(tensors, step, lr=lr, betas=betas, eps=eps, weight_decay=weight_decay,
+                              grad_scale=grad_scale, stream=stream)
     s = tensors._on(stream)
     _check(lib().gns_adamw_step(tensors._info, tensors._table, int(step), float(lr), float(betas[0]),
                                 float(betas[1]), float(eps), float(weight_decay),
