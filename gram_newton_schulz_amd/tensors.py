@@ -132,7 +132,7 @@ class TensorList:
         L = lib()
         nbytes = int(L.gns_tensor_list_bytes(entries.ctypes.data, self.arrays, count))
         self.info = ListInfo()
-        image = torch.empty(max(nbytes, 16), dtype=torch.uint8, pin_memory=self.device is not None)
+        image = torch.empty(max(nbytes, 16), dtype=torch.uint8, device="cpu", pin_memory=self.device is not None)
         as_floats = [None if s is None else (ctypes.c_float * max(1, count))(*s) for s in (lr_scales, wd_scales)]
         _check(L.gns_tensor_list_build(entries.ctypes.data, self.arrays, count, *as_floats, image.data_ptr(),
                                        image.numel(), ctypes.byref(self.info)))
