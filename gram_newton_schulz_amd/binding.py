@@ -220,7 +220,12 @@ def _tile_opts(tile) -> int:
 
 
 def _workspace(nbytes: int, device, workspace: Optional[torch.Tensor]) -> torch.Tensor:
+    """The caller's workspace, or a new one.  The library takes its address and
+    its size, so it has to be that many bytes of the GPU."""
     if workspace is not None:
+        _device_tensor("workspace", workspace, device)
+        if not workspace.is_contiguous():
+            raise GnsError(8, "workspace must be contiguous")
         return workspace
     return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
 

@@ -19,7 +19,7 @@ from typing import Optional, Sequence, Union
 import numpy as np
 import torch
 
-from .binding import GnsError, _DT, _check, _device_tensor, _dtype_code, _ptr, _scalar_ptr, lib
+from .binding import GnsError, _DT, _check, _device_tensor, _dtype_code, _ptr, _scalar_ptr, _workspace, lib
 
 NORM_L2, NORM_MAX = 0, 1
 _NORMS = {2: NORM_L2, math.inf: NORM_MAX}
@@ -249,7 +249,7 @@ def _norm_call(fn, grads, max_norm, ord, eps, inv_scale, per_tensor, workspace, 
         with contextlib.nullcontext() if stream is None else torch.cuda.stream(lst._stream(s)):
             result = torch.empty(2, dtype=torch.float32, device=lst.device)
             norms = torch.empty(lst.count, dtype=torch.float32, device=lst.device) if per_tensor else None
-            ws = lst._workspace(s) if workspace is None else workspace
+            ws = lst._workspace(s) if workspace is None else _workspace(0, lst.device, workspace)
         _check(fn(lst._info, lst._table, _NORMS[ord], float(max_norm), float(eps),
                   _scalar_ptr("inv_scale", inv_scale, lst.device), result.data_ptr(), _ptr(norms),
                   ws.data_ptr(), ws.numel(), s))

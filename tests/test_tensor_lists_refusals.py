@@ -1,10 +1,13 @@
 """Calls on lists of tensors that are refused before anything reaches the GPU
 (none needed here)."""
 import os
+import threading
 
 import pytest
+import torch
 
 gns = pytest.importorskip("gram_newton_schulz_amd")
+from gram_newton_schulz_amd import binding, tensors as T  # noqa: E402
 from test_tensor_lists_host import BASE, E, F32, build, norm  # noqa: E402
 
 pytestmark = pytest.mark.skipif(not os.path.exists(gns.LIB_PATH),
@@ -19,3 +22,27 @@ def test_clip_in_place_of_a_gradient_that_is_other_memory_of_the_list(arrays):
             lists = [[(BASE + 4096 * a, 1, 8, 8, F32)] for a in range(arrays)]
             lists[other] = [(BASE + shift, 1, 8, 8, F32)]
             assert norm(build(lists)[1], clip=True) == E["ALIAS"], (other, shift)
+
+
+@pytest.mark.parametrize("workspace,name", [
+    (torch.zeros(4096, dtype=torch.uint8), "GNS_E_NULL"),
+    (torch.zeros(4096, dtype=torch.uint8, device="meta"), "GNS_E_NULL"),
+    (torch.zeros(1, dtype=torch.uint8).expand(4096), "GNS_E_WORKSPACE"),
+    (torch.zeros(8192, dtype=torch.uint8)[::2], "GNS_E_WORKSPACE")], ids=["host", "meta", "expanded", "strided"])
+def test_workspace_that_is_not_the_memory_it_names(workspace, name, monkeypatch):
+    """The library takes a workspace's address and its number of bytes: a host
+    tensor, or one that has other memory than that, is refused before."""
+    if name == "GNS_E_WORKSPACE":                  # its device is not what is wrong with it
+        monkeypatch.setattr(binding, "_device_tensor", lambda *a: None)
+    lst = object.__new__(T.TensorList)
+    lst.__dict__.update(device=torch.device("cuda", 0), count=1, _info=None, _table=0, _home=0,
+                        _lock=threading.RLock())
+    monkeypatch.setattr(T, "_current_device", lambda: 0)
+    monkeypatch.setattr(T, "_current_raw_stream", lambda index: 0)
+    real = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, device=None, **kw: real(*a, **kw))
+    for call in (lambda: binding._workspace(16, torch.device("cuda", 0), workspace),
+                 lambda: T._norm_call(lambda *a: 0, lst, 1.0, 2, 1e-6, None, False, workspace, None)):
+        with pytest.raises(gns.GnsError) as e:
+            call()
+        assert e.value.name == name
