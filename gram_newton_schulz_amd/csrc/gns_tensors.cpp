@@ -311,7 +311,8 @@ gns_status gns_adamw_step(const gns_tensor_list *list, const void *table, int64_
   for (int a = 1; a <= 3; ++a)
     if (list->dtypes[a] & ~(1u << GNS_F32)) return GNS_E_DTYPE;
   if (step < 1 || !std::isfinite(lr) || !std::isfinite(weight_decay) || !(beta1 >= 0.0 && beta1 < 1.0) ||
-      !(beta2 >= 0.0 && beta2 < 1.0) || !std::isfinite(eps) || !(eps > 0.0))
+      !(beta2 >= 0.0 && beta2 < 1.0) || !std::isfinite(eps) ||
+      !(static_cast<float>(eps) > 0.0f))   // as the kernel has it: 0 / 0 where moments are zero
     return GNS_E_PARAM;
   if (list->count > 0 && !table) return GNS_E_NULL;
   for (int a = 1; a < list->arrays; ++a)

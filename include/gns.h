@@ -520,7 +520,7 @@ gns_status gns_grad_clip(const gns_tensor_list *list, const void *table, gns_nor
  * skipped: nothing is written.
  * GNS_E_SHAPE (a list of other arrays), GNS_E_DTYPE (parameters or moments
  * not fp32), GNS_E_PARAM (step < 1, a hyperparameter that is not finite, betas
- * outside [0, 1), eps <= 0), GNS_E_NULL, GNS_E_ALIAS.
+ * outside [0, 1), eps not above zero in fp32), GNS_E_NULL, GNS_E_ALIAS.
  */
 gns_status gns_adamw_step(const gns_tensor_list *list, const void *table, int64_t step, double lr,
                           double beta1, double beta2, double eps, double weight_decay,

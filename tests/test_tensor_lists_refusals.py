@@ -8,7 +8,7 @@ import torch
 
 gns = pytest.importorskip("gram_newton_schulz_amd")
 from gram_newton_schulz_amd import binding, tensors as T  # noqa: E402
-from test_tensor_lists_host import BASE, E, F32, build, norm  # noqa: E402
+from test_tensor_lists_host import BASE, E, F32, adamw, build, norm  # noqa: E402
 
 pytestmark = pytest.mark.skipif(not os.path.exists(gns.LIB_PATH),
                                 reason="libgns.so not built (run __graft_entry__.build())")
@@ -46,3 +46,13 @@ def test_workspace_that_is_not_the_memory_it_names(workspace, name, monkeypatch)
         with pytest.raises(gns.GnsError) as e:
             call()
         assert e.value.name == name
+
+
+def test_adamw_eps_is_checked_as_it_is_used():
+    """eps goes into the update in fp32, where anything up to 2^-150 is zero
+    and an element without a gradient would be 0 / 0."""
+    info = build([[(BASE + 4096 * a, 1, 8, 8, F32)] for a in range(4)])[1]
+    for eps in (2.0 ** -150, 1e-46, 1e-300, 0.0, -1e-8):
+        assert adamw(info, eps=eps) == E["PARAM"], eps
+    # the smallest that is one of fp32 passes this check (and stops at the table)
+    assert adamw(info, eps=2.0 ** -149, table=None) == E["NULL"]
