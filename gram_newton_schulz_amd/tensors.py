@@ -143,6 +143,8 @@ class TensorList:
         self._lock = threading.RLock()
         if self.device is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
+        self._index = self.device.index
+        self._others = torch.cuda.device_count() > 1    # asking which is current takes 0.2 us
         # the copy runs on the current stream; calls on other streams wait for it
         home = torch.cuda.current_stream(self.device)
         self._home = home.cuda_stream
@@ -177,11 +179,11 @@ class TensorList:
         """The raw stream a call runs on, ordered after the table's copy.  (A
         raw handle is taken for one of the list's device.)"""
         if stream is None:
-            raw = _current_raw_stream(self.device.index)
+            raw = _current_raw_stream(self._index)
         elif isinstance(stream, int):
             raw = stream
         else:
-            if stream.device.index != self.device.index:
+            if stream.device.index != self._index:
                 raise GnsError(11, f"stream is on {stream.device}, the list on {self.device}")
             raw = stream.cuda_stream
         if raw != self._home:
@@ -240,19 +242,25 @@ def _norm_call(fn, grads, max_norm, ord, eps, inv_scale, per_tensor, workspace, 
     if ord not in _NORMS:
         raise GnsError(11, f"ord must be 2 or inf, got {ord}")
     # the library launches on the current device, where handle 0 is another stream
-    if _current_device() != lst.device.index:
+    if lst._others and _current_device() != lst._index:
         with torch.cuda.device(lst.device):
             return _norm_call(fn, lst, max_norm, ord, eps, inv_scale, per_tensor, workspace, stream)
     s = lst._on(stream)
+    scale = None if inv_scale is None else _scalar_ptr("inv_scale", inv_scale, lst.device)
+
+    def buffers():
+        return (torch.empty(2, dtype=torch.float32, device=lst.device),
+                torch.empty(lst.count, dtype=torch.float32, device=lst.device) if per_tensor else None,
+                lst._workspace(s) if workspace is None else _workspace(0, lst.device, workspace))
+
     with lst._lock:
-        # allocated for the stream that the call runs on
-        with contextlib.nullcontext() if stream is None else torch.cuda.stream(lst._stream(s)):
-            result = torch.empty(2, dtype=torch.float32, device=lst.device)
-            norms = torch.empty(lst.count, dtype=torch.float32, device=lst.device) if per_tensor else None
-            ws = lst._workspace(s) if workspace is None else _workspace(0, lst.device, workspace)
-        _check(fn(lst._info, lst._table, _NORMS[ord], float(max_norm), float(eps),
-                  _scalar_ptr("inv_scale", inv_scale, lst.device), result.data_ptr(), _ptr(norms),
-                  ws.data_ptr(), ws.numel(), s))
+        if stream is None:
+            result, norms, ws = buffers()
+        else:                                  # allocated for the stream that the call runs on
+            with torch.cuda.stream(lst._stream(s)):
+                result, norms, ws = buffers()
+        _check(fn(lst._info, lst._table, _NORMS[ord], float(max_norm), float(eps), scale, result.data_ptr(),
+                  _ptr(norms), ws.data_ptr(), ws.numel(), s))
     return GradNorm(result, norms)
 
 
@@ -290,7 +298,7 @@ def adamw_step(tensors: TensorList, step: int, *, lr: float, betas: Sequence[flo
     ``step``-th (from 1), with decoupled weight decay (gns_adamw_step).
     ``grad_scale`` (a float32 on the GPU) multiplies the gradients; when it is
     not finite nothing changes."""
-    if _current_device() != tensors.device.index:
+    if tensors._others and _current_device() != tensors._index:
         with torch.cuda.device(tensors.device):
             return adamw_step(tensors, step, lr=lr, betas=betas, eps=eps, weight_decay=weight_decay,
                               grad_scale=grad_scale, stream=stream)

@@ -48,8 +48,8 @@ def machine(monkeypatch):
 
 def on(device):
     lst = object.__new__(T.TensorList)
-    lst.__dict__.update(device=device, count=1, workspace_bytes=1024, _info=None, _table=0, _home=0,
-                        _workspaces={}, _lock=threading.RLock())
+    lst.__dict__.update(device=device, _index=device.index, _others=True, count=1,
+                        workspace_bytes=1024, _info=None, _table=0, _home=0, _workspaces={}, _lock=threading.RLock())
     return lst
 
 

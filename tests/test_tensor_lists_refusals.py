@@ -35,7 +35,7 @@ def test_workspace_that_is_not_the_memory_it_names(workspace, name, monkeypatch)
     if name == "GNS_E_WORKSPACE":                  # its device is not what is wrong with it
         monkeypatch.setattr(binding, "_device_tensor", lambda *a: None)
     lst = object.__new__(T.TensorList)
-    lst.__dict__.update(device=torch.device("cuda", 0), count=1, _info=None, _table=0, _home=0,
+    lst.__dict__.update(device=torch.device("cuda", 0), _index=0, _others=True, count=1, _info=None, _table=0, _home=0,
                         _lock=threading.RLock())
     monkeypatch.setattr(T, "_current_device", lambda: 0)
     monkeypatch.setattr(T, "_current_raw_stream", lambda index: 0)

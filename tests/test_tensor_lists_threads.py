@@ -14,8 +14,8 @@ from gram_newton_schulz_amd import tensors as T  # noqa: E402
 def one_list(monkeypatch):
     """A list on the CPU, whose calls see stream 0, no capture."""
     lst = object.__new__(T.TensorList)
-    lst.__dict__.update(device=torch.device("cpu"), count=1, workspace_bytes=1024, _info=None, _table=0, _home=0,
-                        _workspaces={}, _lock=threading.RLock())
+    lst.__dict__.update(device=torch.device("cpu"), _index=None, _others=True, count=1,
+                        workspace_bytes=1024, _info=None, _table=0, _home=0, _workspaces={}, _lock=threading.RLock())
     monkeypatch.setattr(T, "_current_device", lambda: None)
     monkeypatch.setattr(T, "_current_raw_stream", lambda index: 0)
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
