@@ -63,7 +63,7 @@ class Trainer:
     def __init__(self, model, lr=0.02, adam_lr=3e-3, max_norm=0.5, fraction=0.5):
         self.matrices = list(model.up) + list(model.down)
         self.rest = [model.embedding, model.head] + list(model.gain)
-        self.lr, self.adam_lr, self.max_norm, self.steps = lr, adam_lr, max_norm, 0
+        self.lr, self.adam_lr, self.max_norm = lr, adam_lr, max_norm
         # Dion3's state: the stack of masters, its gradients as one [batch, n, m] tensor
         n = len(self.matrices)
         self.G = grad_buffer(self.matrices).view(n, WIDTH, WIDTH)
@@ -72,7 +72,9 @@ class Trainer:
         self.k = gns.select_count(WIDTH, fraction)
         self.workspace = torch.empty(gns.dion3_workspace_bytes(torch.bfloat16, n, WIDTH, WIDTH, self.k),
                                      dtype=torch.uint8, device=self.W.device)
-        # AdamW's state: fp32 masters and moments; every step refreshes the bf16 weights
+        # AdamW's state: fp32 masters and moments, and the number of its updates, which is counted on the
+        # GPU because only the GPU knows which steps were skipped; every step refreshes the bf16 weights
+        self.updates = torch.zeros(1, dtype=torch.int64, device=self.W.device)
         self.flat_rest = grad_buffer(self.rest)
         self.masters = [p.detach().float() for p in self.rest]
         decayed = [1.0 if p.dim() == 2 else 0.0 for p in self.rest]
@@ -88,13 +90,12 @@ class Trainer:
         self.flat_rest.zero_()
 
     def step(self):
-        self.steps += 1
         got = gns.grad_norm(self.grads, max_norm=self.max_norm)
         clip = got.clip
         gns.dion3_step(self.W, self.G, self.M, self.v, self.k, synth.NS5_MUON, lr=self.lr, mu=0.9,
                        grad_scale=clip, workspace=self.workspace)
         torch._foreach_copy_([p.detach() for p in self.matrices], list(self.W))
-        gns.adamw_step(self.adamw, self.steps, lr=self.adam_lr, betas=(0.9, 0.95), weight_decay=0.01,
+        gns.adamw_step(self.adamw, count=self.updates, lr=self.adam_lr, betas=(0.9, 0.95), weight_decay=0.01,
                        grad_scale=clip)
         return got
 

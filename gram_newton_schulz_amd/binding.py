@@ -44,7 +44,7 @@ EXPORTS = [
     "gns_call_plan", "gns_check_finite", "gns_select_count", "gns_safety_scale",
     "gns_gram_batched_noalloc",
     "gns_tensor_list_bytes", "gns_tensor_list_build", "gns_tensor_list_workspace_bytes",
-    "gns_grad_norm", "gns_grad_clip", "gns_adamw_step", "gns_dion3_step_clipped",
+    "gns_grad_norm", "gns_grad_clip", "gns_adamw_step", "gns_adamw_step_counted", "gns_dion3_step_clipped",
 ]
 
 
@@ -148,6 +148,8 @@ def lib() -> ctypes.CDLL:
         f.argtypes = [vp, vp, ctypes.c_int, dbl, dbl, vp, vp, vp, vp, sz, vp]
     L.gns_adamw_step.restype = ctypes.c_int
     L.gns_adamw_step.argtypes = [vp, vp, i64, dbl, dbl, dbl, dbl, dbl, vp, vp]
+    L.gns_adamw_step_counted.restype = ctypes.c_int
+    L.gns_adamw_step_counted.argtypes = [vp, vp, vp, dbl, dbl, dbl, dbl, dbl, vp, vp, sz, vp]
     L.gns_timing_enable.argtypes = [ctypes.c_int]
     L.gns_timing_enable.restype = None
     L.gns_timing_reset.restype = None
@@ -239,12 +241,12 @@ def _device_tensor(name: str, t: torch.Tensor, device) -> None:
         raise GnsError(1, f"{name} is on {t.device}, X on {device}")
 
 
-def _scalar_ptr(name: str, t: Optional[torch.Tensor], device) -> Optional[int]:
-    """Address of one float32 on the GPU (None for None)."""
+def _scalar_ptr(name: str, t: Optional[torch.Tensor], device, dtype=torch.float32) -> Optional[int]:
+    """Address of one float32 (or `dtype`) on the GPU (None for None)."""
     if t is None:
         return None
-    if t.dtype != torch.float32 or t.numel() != 1:
-        raise GnsError(3, f"{name} must be one float32 on the GPU")
+    if t.dtype != dtype or t.numel() != 1:
+        raise GnsError(3, f"{name} must be one {str(dtype)[6:]} on the GPU")
     _device_tensor(name, t, device)
     return t.data_ptr()
 

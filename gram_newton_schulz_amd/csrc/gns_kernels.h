@@ -205,14 +205,21 @@ hipError_t launch_list_clip(const ListView &v, int dst, bool max, uint64_t *part
                             const NormArgs &a, float *tensor_norms, hipStream_t s);
 // AdamW over the entries' arrays {gradient, parameter, first moment, second
 // moment[, copy]}; nothing when grad_scale is given and not finite.
+struct AdamwBias {
+  double bias1;          // 1 - beta1^t
+  float inv_sqrt_bias2;  // 1 / sqrt(1 - beta2^t)
+};
 struct AdamwScalars {
   double lr, weight_decay;
   float beta1, one_minus_beta1, beta2, one_minus_beta2;
-  double bias1;          // 1 - beta1^t
-  float inv_sqrt_bias2;  // 1 / sqrt(1 - beta2^t)
+  AdamwBias bias;        // when the step is the host's
   float eps;
 };
-hipError_t launch_list_adamw(const ListView &v, bool copy, const AdamwScalars &h, const float *grad_scale,
-                             hipStream_t s);
+// The step that follows *count, counted there unless grad_scale skips it; its
+// bias factors go to *bias, which launch_list_adamw then takes for h's.
+hipError_t launch_adamw_count(int64_t *count, double beta1, double beta2, const float *grad_scale, AdamwBias *bias,
+                              hipStream_t s);
+hipError_t launch_list_adamw(const ListView &v, bool copy, const AdamwScalars &h, const AdamwBias *bias,
+                             const float *grad_scale, hipStream_t s);
 
 }  // namespace gns

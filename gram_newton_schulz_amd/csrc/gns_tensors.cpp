@@ -23,6 +23,7 @@ using gns::ListChunk;
 using gns::ListEntry;
 using gns::ListView;
 
+static_assert(sizeof(gns::AdamwBias) <= GNS_ADAMW_WORKSPACE_BYTES, "room for the bias factors");
 static_assert(kListArrays == GNS_LIST_MAX_ARRAYS, "header and library agree on the arrays");
 
 constexpr int64_t kMaxCount = int64_t(1) << 20;
@@ -224,6 +225,45 @@ gns_status norm_and_clip(const gns_tensor_list *list, const void *table, gns_nor
   return GNS_OK;
 }
 
+// One update, the step-th or (with count) the one after *count.
+gns_status adamw(const gns_tensor_list *list, const void *table, int64_t step, int64_t *count, double lr,
+                 double beta1, double beta2, double eps, double weight_decay, const float *grad_scale,
+                 gns::AdamwBias *bias, hipStream_t s) {
+  if (!list) return GNS_E_NULL;
+  if (!valid_list(list) || list->arrays < 4) return GNS_E_SHAPE;
+  for (int a = 1; a <= 3; ++a)
+    if (list->dtypes[a] & ~(1u << GNS_F32)) return GNS_E_DTYPE;
+  if ((!count && step < 1) || !std::isfinite(lr) || !std::isfinite(weight_decay) || !(beta1 >= 0.0 && beta1 < 1.0) ||
+      !(beta2 >= 0.0 && beta2 < 1.0) || !std::isfinite(eps) ||
+      !(static_cast<float>(eps) > 0.0f))   // as the kernel has it: 0 / 0 where moments are zero
+    return GNS_E_PARAM;
+  if (list->count > 0 && !table) return GNS_E_NULL;
+  for (int a = 1; a < list->arrays; ++a)
+    for (int b = 0; b < list->arrays; ++b)
+      if (overlap(list, a, b)) return GNS_E_ALIAS;
+  gns::AdamwScalars h{};
+  h.lr = lr;
+  h.weight_decay = weight_decay;
+  h.beta1 = static_cast<float>(beta1);
+  h.one_minus_beta1 = static_cast<float>(1.0 - beta1);
+  h.beta2 = static_cast<float>(beta2);
+  h.one_minus_beta2 = static_cast<float>(1.0 - beta2);
+  h.eps = static_cast<float>(eps);
+  if (!count) {
+    const double t = static_cast<double>(step);
+    h.bias.bias1 = 1.0 - std::pow(beta1, t);
+    h.bias.inv_sqrt_bias2 = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(beta2, t)));
+  }
+  double bytes = list->bytes[0] + list->bytes[4];
+  for (int a = 1; a <= 3; ++a) bytes += 2.0 * list->bytes[a];
+  LaunchScope ls(s, "adamw", count ? "adamw_count+list_adamw" : "list_adamw", 15.0 * list->elements, bytes);
+  hipError_t e = count ? gns::launch_adamw_count(count, beta1, beta2, grad_scale, bias, s) : hipSuccess;
+  if (e == hipSuccess)
+    e = gns::launch_list_adamw(view_of(list, table), list->arrays == 5, h, count ? bias : nullptr, grad_scale, s);
+  ls.done();
+  return e == hipSuccess ? GNS_OK : GNS_E_HIP;
+}
+
 }  // namespace
 
 extern "C" {
@@ -306,36 +346,20 @@ gns_status gns_grad_clip(const gns_tensor_list *list, const void *table, gns_nor
 gns_status gns_adamw_step(const gns_tensor_list *list, const void *table, int64_t step, double lr,
                           double beta1, double beta2, double eps, double weight_decay,
                           const float *grad_scale, void *stream) {
-  if (!list) return GNS_E_NULL;
-  if (!valid_list(list) || list->arrays < 4) return GNS_E_SHAPE;
-  for (int a = 1; a <= 3; ++a)
-    if (list->dtypes[a] & ~(1u << GNS_F32)) return GNS_E_DTYPE;
-  if (step < 1 || !std::isfinite(lr) || !std::isfinite(weight_decay) || !(beta1 >= 0.0 && beta1 < 1.0) ||
-      !(beta2 >= 0.0 && beta2 < 1.0) || !std::isfinite(eps) ||
-      !(static_cast<float>(eps) > 0.0f))   // as the kernel has it: 0 / 0 where moments are zero
-    return GNS_E_PARAM;
-  if (list->count > 0 && !table) return GNS_E_NULL;
-  for (int a = 1; a < list->arrays; ++a)
-    for (int b = 0; b < list->arrays; ++b)
-      if (overlap(list, a, b)) return GNS_E_ALIAS;
-  gns::AdamwScalars h;
-  const double t = static_cast<double>(step);
-  h.lr = lr;
-  h.weight_decay = weight_decay;
-  h.beta1 = static_cast<float>(beta1);
-  h.one_minus_beta1 = static_cast<float>(1.0 - beta1);
-  h.beta2 = static_cast<float>(beta2);
-  h.one_minus_beta2 = static_cast<float>(1.0 - beta2);
-  h.bias1 = 1.0 - std::pow(beta1, t);
-  h.inv_sqrt_bias2 = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(beta2, t)));
-  h.eps = static_cast<float>(eps);
-  hipStream_t s = static_cast<hipStream_t>(stream);
-  double bytes = list->bytes[0] + list->bytes[4];
-  for (int a = 1; a <= 3; ++a) bytes += 2.0 * list->bytes[a];
-  LaunchScope ls(s, "adamw", "list_adamw", 15.0 * list->elements, bytes);
-  const hipError_t e = gns::launch_list_adamw(view_of(list, table), list->arrays == 5, h, grad_scale, s);
-  ls.done();
-  return e == hipSuccess ? GNS_OK : GNS_E_HIP;
+  return adamw(list, table, step, nullptr, lr, beta1, beta2, eps, weight_decay, grad_scale, nullptr,
+               static_cast<hipStream_t>(stream));
+}
+
+gns_status gns_adamw_step_counted(const gns_tensor_list *list, const void *table, int64_t *count, double lr,
+                                  double beta1, double beta2, double eps, double weight_decay,
+                                  const float *grad_scale, void *workspace, size_t workspace_bytes,
+                                  void *stream) {
+  if (!count) return GNS_E_NULL;
+  if (reinterpret_cast<uintptr_t>(count) % sizeof(*count)) return GNS_E_PARAM;
+  if (!workspace || workspace_bytes < GNS_ADAMW_WORKSPACE_BYTES || (reinterpret_cast<uintptr_t>(workspace) & 255))
+    return GNS_E_WORKSPACE;
+  return adamw(list, table, 0, count, lr, beta1, beta2, eps, weight_decay, grad_scale,
+               static_cast<gns::AdamwBias *>(workspace), static_cast<hipStream_t>(stream));
 }
 
 }  // extern "C"

@@ -636,18 +636,32 @@ struct AdamwRule {
   }
 };
 
+// Counts a step on the GPU and leaves its bias factors (fp64 powers, rounded
+// as the host's are) for the update.  A launch of its own, since every
+// workgroup of the update reads what it writes: AdamW of 48 x 1024 fp32 takes
+// 8.8 us per call with it and 3.9 without, of 268M elements 1112 and 1109.
+__global__ void adamw_count(int64_t *count, double beta1, double beta2, const float *grad_scale, AdamwBias *bias) {
+  if (grad_scale && !isfinite(*grad_scale)) return;
+  const int64_t step = *count + 1;
+  *count = step;
+  const double t = static_cast<double>(step);
+  bias->bias1 = 1.0 - pow(beta1, t);
+  bias->inv_sqrt_bias2 = static_cast<float>(1.0 / sqrt(1.0 - pow(beta2, t)));
+}
+
 template <bool COPY>
 __global__ void __launch_bounds__(kThreads)
-list_adamw(ListView v, AdamwScalars h, const float *grad_scale, unsigned parts) {
+list_adamw(ListView v, AdamwScalars h, const AdamwBias *counted, const float *grad_scale, unsigned parts) {
   const float f = grad_scale ? *grad_scale : 1.0f;
   if (!isfinite(f)) return;
   const ListChunk ch = v.chunks[blockIdx.x / parts];
   const ListEntry &e = v.entries[ch.entry];
   const Span s = span_of(e, ch.index * parts + blockIdx.x % parts, v.chunk_units / parts, 1);
   const double eta = h.lr * e.lr_scale;
-  const AdamwRule rule{f, h.beta1, h.one_minus_beta1, h.beta2, h.one_minus_beta2, h.inv_sqrt_bias2, h.eps,
+  const AdamwBias bias = counted ? *counted : h.bias;
+  const AdamwRule rule{f, h.beta1, h.one_minus_beta1, h.beta2, h.one_minus_beta2, bias.inv_sqrt_bias2, h.eps,
                        static_cast<float>(1.0 - eta * (h.weight_decay * e.wd_scale)),
-                       static_cast<float>(eta / h.bias1)};
+                       static_cast<float>(eta / bias.bias1)};
   float *P = static_cast<float *>(e.data[1]), *M = static_cast<float *>(e.data[2]),
         *Q = static_cast<float *>(e.data[3]);
   auto body = [&](auto grad, auto copy) {
@@ -766,13 +780,19 @@ hipError_t launch_list_clip(const ListView &v, int dst, bool max, uint64_t *part
   return hipGetLastError();
 }
 
-hipError_t launch_list_adamw(const ListView &v, bool copy, const AdamwScalars &h, const float *grad_scale,
-                             hipStream_t s) {
+hipError_t launch_adamw_count(int64_t *count, double beta1, double beta2, const float *grad_scale, AdamwBias *bias,
+                              hipStream_t s) {
+  adamw_count<<<1, 1, 0, s>>>(count, beta1, beta2, grad_scale, bias);
+  return hipGetLastError();
+}
+
+hipError_t launch_list_adamw(const ListView &v, bool copy, const AdamwScalars &h, const AdamwBias *bias,
+                             const float *grad_scale, hipStream_t s) {
   if (v.n_chunks == 0) return hipSuccess;
   const unsigned parts = parts_of(v, kAdamwUnits);
   const dim3 grid(static_cast<unsigned>(v.n_chunks) * parts);
-  if (copy) list_adamw<true><<<grid, kThreads, 0, s>>>(v, h, grad_scale, parts);
-  else list_adamw<false><<<grid, kThreads, 0, s>>>(v, h, grad_scale, parts);
+  if (copy) list_adamw<true><<<grid, kThreads, 0, s>>>(v, h, bias, grad_scale, parts);
+  else list_adamw<false><<<grid, kThreads, 0, s>>>(v, h, bias, grad_scale, parts);
   return hipGetLastError();
 }
 

@@ -1,6 +1,6 @@
 """Lists of tensors: global gradient norm, clipping and AdamW over every
 tensor of a model in a few launches (the C ABI's gns_tensor_list,
-gns_grad_norm, gns_grad_clip and gns_adamw_step).
+gns_grad_norm, gns_grad_clip, gns_adamw_step and gns_adamw_step_counted).
 
 A :class:`TensorList` names its tensors once and is then passed to the calls,
 which take no per-tensor arguments and run on the tensors' device, whichever
@@ -23,6 +23,7 @@ from .binding import GnsError, _DT, _check, _device_tensor, _dtype_code, _ptr, _
 
 NORM_L2, NORM_MAX = 0, 1
 _NORMS = {2: NORM_L2, math.inf: NORM_MAX}
+ADAMW_WORKSPACE_BYTES = 256
 
 # the current stream's handle without the Stream object around it, which costs
 # 1.8 us of a call that takes 6
@@ -291,18 +292,40 @@ def clip_grad_norm_(grads: Union[TensorList, Sequence[torch.Tensor]], max_norm: 
     return _norm_call(lib().gns_grad_clip, grads, max_norm, ord, eps, inv_scale, per_tensor, workspace, stream)
 
 
-def adamw_step(tensors: TensorList, step: int, *, lr: float, betas: Sequence[float] = (0.9, 0.999),
+def adamw_step(tensors: TensorList, step: Optional[int] = None, *, lr: float, betas: Sequence[float] = (0.9, 0.999),
                eps: float = 1e-8, weight_decay: float = 0.01, grad_scale: Optional[torch.Tensor] = None,
-               stream=None) -> None:
+               count: Optional[torch.Tensor] = None, stream=None) -> None:
     """One AdamW update of every parameter of an :func:`adamw_list`, the
     ``step``-th (from 1), with decoupled weight decay (gns_adamw_step).
     ``grad_scale`` (a float32 on the GPU) multiplies the gradients; when it is
-    not finite nothing changes."""
+    not finite nothing changes.
+
+    A step that was skipped so is no update, which the program does not learn
+    without waiting for the GPU.  ``count`` (one int64 on the GPU, zero before
+    the first update) takes the place of ``step``: the updates made so far,
+    counted up by every call that is not skipped (gns_adamw_step_counted).
+    Save it with the moments.  In a captured graph every replay is then the
+    next update; ``step``, ``lr`` and the other numbers are replayed as they
+    were captured.
+
+    Like all calls of this package that write in place, it does not raise the
+    tensors' version counters: autograd does not notice that a parameter was
+    updated between a forward pass and its backward pass."""
+    if (step is None) is (count is None):
+        raise GnsError(11, "either step or count")
     if tensors._others and _current_device() != tensors._index:
         with torch.cuda.device(tensors.device):
             return adamw_step(tensors, step, lr=lr, betas=betas, eps=eps, weight_decay=weight_decay,
-                              grad_scale=grad_scale, stream=stream)
+                              grad_scale=grad_scale, count=count, stream=stream)
     s = tensors._on(stream)
-    _check(lib().gns_adamw_step(tensors._info, tensors._table, int(step), float(lr), float(betas[0]),
-                                float(betas[1]), float(eps), float(weight_decay),
-                                _scalar_ptr("grad_scale", grad_scale, tensors.device), s))
+    scale = None if grad_scale is None else _scalar_ptr("grad_scale", grad_scale, tensors.device)
+    if count is None:
+        _check(lib().gns_adamw_step(tensors._info, tensors._table, int(step), float(lr), float(betas[0]),
+                                    float(betas[1]), float(eps), float(weight_decay), scale, s))
+        return
+    with contextlib.nullcontext() if stream is None else torch.cuda.stream(tensors._stream(s)):
+        ws = torch.empty(ADAMW_WORKSPACE_BYTES, dtype=torch.uint8, device=tensors.device)
+    _check(lib().gns_adamw_step_counted(tensors._info, tensors._table,
+                                        _scalar_ptr("count", count, tensors.device, torch.int64), float(lr),
+                                        float(betas[0]), float(betas[1]), float(eps), float(weight_decay), scale,
+                                        ws.data_ptr(), ws.numel(), s))

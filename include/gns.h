@@ -518,6 +518,10 @@ gns_status gns_grad_clip(const gns_tensor_list *list, const void *table, gns_nor
  * in fp32 arithmetic; the gradients are read only.  grad_scale is a (device)
  * float such as gns_grad_norm's clip; when it is not finite the update is
  * skipped: nothing is written.
+ * step counts the updates of these moments, and a skipped call is none; where
+ * that happens the caller cannot know the count without waiting for the GPU,
+ * so use gns_adamw_step_counted.  step and the hyperparameters are taken by
+ * value: a graph that captured the call repeats them.
  * GNS_E_SHAPE (a list of other arrays), GNS_E_DTYPE (parameters or moments
  * not fp32), GNS_E_PARAM (step < 1, a hyperparameter that is not finite, betas
  * outside [0, 1), eps not above zero in fp32), GNS_E_NULL, GNS_E_ALIAS.
@@ -525,6 +529,24 @@ gns_status gns_grad_clip(const gns_tensor_list *list, const void *table, gns_nor
 gns_status gns_adamw_step(const gns_tensor_list *list, const void *table, int64_t step, double lr,
                           double beta1, double beta2, double eps, double weight_decay,
                           const float *grad_scale, void *stream);
+
+/*
+ * gns_adamw_step whose step is counted on the GPU: t = *count + 1, and *count
+ * becomes t unless the update is skipped.  A skipped call leaves no trace, and
+ * every replay of a graph that captured the call is the next update (with the
+ * captured hyperparameters).
+ *   count        (device) the updates made so far, >= 0 (0 before the first
+ *                from zero moments); part of the state, like the moments.
+ *   workspace    (device) >= GNS_ADAMW_WORKSPACE_BYTES bytes, 256-byte aligned,
+ *                clobbered.
+ * Neither may be memory of the list.
+ * GNS_E_WORKSPACE; else as gns_adamw_step.
+ */
+#define GNS_ADAMW_WORKSPACE_BYTES 256
+gns_status gns_adamw_step_counted(const gns_tensor_list *list, const void *table, int64_t *count, double lr,
+                                  double beta1, double beta2, double eps, double weight_decay,
+                                  const float *grad_scale, void *workspace, size_t workspace_bytes,
+                                  void *stream);
 
 /*
  * Enqueue a check of a row subset: writes to *result (device int32) 0 when

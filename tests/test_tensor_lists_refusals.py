@@ -1,5 +1,6 @@
 """Calls on lists of tensors that are refused before anything reaches the GPU
 (none needed here)."""
+import ctypes
 import os
 import threading
 
@@ -8,7 +9,7 @@ import torch
 
 gns = pytest.importorskip("gram_newton_schulz_amd")
 from gram_newton_schulz_amd import binding, tensors as T  # noqa: E402
-from test_tensor_lists_host import BASE, E, F32, adamw, build, norm  # noqa: E402
+from test_tensor_lists_host import BASE, E, F32, WS, adamw, build, norm  # noqa: E402
 
 pytestmark = pytest.mark.skipif(not os.path.exists(gns.LIB_PATH),
                                 reason="libgns.so not built (run __graft_entry__.build())")
@@ -56,3 +57,19 @@ def test_adamw_eps_is_checked_as_it_is_used():
         assert adamw(info, eps=eps) == E["PARAM"], eps
     # the smallest that is one of fp32 passes this check (and stops at the table)
     assert adamw(info, eps=2.0 ** -149, table=None) == E["NULL"]
+
+
+def test_counted_adamw_refusals():
+    info = build([[(BASE + 4096 * a, 1, 8, 8, F32)] for a in range(4)])[1]
+
+    def call(info=info, count=WS, eps=1e-8, b1=0.9, table=None, ws=WS + 4096, ws_bytes=T.ADAMW_WORKSPACE_BYTES):
+        return gns.lib().gns_adamw_step_counted(ctypes.byref(info), table, count, 0.1, b1, 0.99, eps, 0.0, None, ws,
+                                                ws_bytes, None)
+
+    assert call() == E["NULL"] and call(count=None) == E["NULL"]
+    assert call(count=WS + 4) == E["PARAM"] and call(eps=0.0) == E["PARAM"] and call(b1=1.0) == E["PARAM"]
+    for kw in ({"ws": None}, {"ws": WS + 16}, {"ws_bytes": 255}):
+        assert call(**kw) == E["WORKSPACE"], kw
+    assert call(info=build([[(BASE, 1, 8, 8, F32)]])[1]) == E["SHAPE"]
+    shared = build([[(BASE + 4096 * min(a, 2), 1, 8, 8, F32)] for a in range(4)])[1]
+    assert call(info=shared, table=BASE) == E["ALIAS"]
