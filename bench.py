@@ -71,7 +71,8 @@ def short_kernel(name):
     for k in ("norm_partial", "row_partials", "scale_transpose", "scale_rows_f32", "transpose_sumsq",
               "norm_finish", "row_l1",
               "select_topk", "check_rows", "momentum_l1", "row_sumsq", "normuon_factors",
-              "dion3_update", "list_partials", "list_finish", "list_scale", "list_adamw"):
+              "dion3_update", "list_partials", "list_norm_once", "list_finish", "list_scale", "list_adamw",
+              "adamw_count"):
         if k in name:
             return k
     return name.split("(")[0][:60]
@@ -273,7 +274,7 @@ def summarize_pmc(fetch_dir, write_dir, calib_mib, workload):
 HBM_KERNELS = ("norm_partial", "row_partials", "scale_transpose", "scale_rows_f32", "transpose_sumsq", "norm_finish",
                "momentum_l1",
                "row_sumsq", "normuon_factors", "dion3_update", "select_topk",
-               "list_partials", "list_finish", "list_scale", "list_adamw")
+               "list_partials", "list_norm_once", "list_finish", "list_scale", "list_adamw", "adamw_count")
 
 
 def mfma_from_profile(kernel, workload):
