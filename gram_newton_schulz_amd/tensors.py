@@ -184,8 +184,9 @@ class TensorList:
         elif isinstance(stream, int):
             raw = stream
         else:
-            if stream.device.index != self._index:
-                raise GnsError(11, f"stream is on {stream.device}, the list on {self.device}")
+            device = getattr(stream, "device", self.device)     # (anything with a handle is taken)
+            if device.index != self._index:
+                raise GnsError(11, f"stream is on {device}, the list on {self.device}")
             raw = stream.cuda_stream
         if raw != self._home:
             with torch.cuda.stream(self._stream(raw)):
@@ -288,7 +289,8 @@ def clip_grad_norm_(grads: Union[TensorList, Sequence[torch.Tensor]], max_norm: 
                     workspace: Optional[torch.Tensor] = None, stream=None) -> GradNorm:
     """:func:`grad_norm`, then the gradients times its ``clip``: in place, or
     into the outputs of a list built with ``out`` (gns_grad_clip).  Gradients
-    whose norm is not finite are left as they are."""
+    whose norm is not finite are left as they are.  ``inv_scale`` and
+    ``workspace`` must not be memory that is written."""
     return _norm_call(lib().gns_grad_clip, grads, max_norm, ord, eps, inv_scale, per_tensor, workspace, stream)
 
 
@@ -297,8 +299,8 @@ def adamw_step(tensors: TensorList, step: Optional[int] = None, *, lr: float, be
                count: Optional[torch.Tensor] = None, stream=None) -> None:
     """One AdamW update of every parameter of an :func:`adamw_list`, the
     ``step``-th (from 1), with decoupled weight decay (gns_adamw_step).
-    ``grad_scale`` (a float32 on the GPU) multiplies the gradients; when it is
-    not finite nothing changes.
+    ``grad_scale`` (a float32 on the GPU, not memory of the list) multiplies
+    the gradients; when it is not finite nothing changes.
 
     A step that was skipped so is no update, which the program does not learn
     without waiting for the GPU.  ``count`` (one int64 on the GPU, zero before

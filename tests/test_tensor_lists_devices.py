@@ -75,3 +75,9 @@ def test_streams_of_another_device_are_refused(machine):
             f()
         assert e.value.name == "GNS_E_PARAM"
     assert not machine.calls and machine.current == 0
+
+
+def test_any_object_with_a_handle_is_a_stream(machine):
+    lst = on(Second())
+    gns.adamw_step(lst, 1, lr=0.1, stream=SimpleNamespace(cuda_stream=0))
+    assert machine.calls == [(1, 0)]
