@@ -551,9 +551,31 @@ def bench_lists(gns, torch, steps):
             gns.adamw_step(lst, 10, lr=1e-3, weight_decay=0.1, grad_scale=got.clip)
         return step, 28.0 * lst.info.elements
 
+    # small ones, bound by their launches: one for the norm, two for clipping (of odd column slices) and for
+    # an update counted on the GPU
+    def norm_small():
+        lst = gns.tensor_list(tensors(24, 1, 1024, torch.float32))
+        return lambda: gns.grad_norm(lst, max_norm=1.0), 4.0 * lst.info.elements
+
+    def clip_columns():
+        g = tensors(1, 513, 3 * 777, torch.bfloat16)[0]
+        out = torch.empty_like(g)
+        cut = [slice(777 * i, 777 * (i + 1)) for i in range(3)]
+        lst = gns.tensor_list([g[:, c] for c in cut], out=[out[:, c] for c in cut])
+        return lambda: gns.clip_grad_norm_(lst, 1.0), 4.0 * lst.info.elements
+
+    def adamw_small():
+        lst = gns.adamw_list(*(tensors(48, 1, 1024, torch.float32) for _ in range(3)),
+                             [t.square_() for t in tensors(48, 1, 1024, torch.float32)])
+        count = torch.zeros(1, dtype=torch.int64, device="cuda")
+        return lambda: gns.adamw_step(lst, count=count, lr=1e-3), 28.0 * lst.info.elements
+
     out = {}
     for name, make in (("grad_norm 8 x 4096x16384 bf16", norm), ("clip 16 x 1024x4096 fp16 to fp32", clip),
-                       ("grad_norm + adamw 2 x 32768x4096, bf16 gradients and copies", adamw)):
+                       ("grad_norm + adamw 2 x 32768x4096, bf16 gradients and copies", adamw),
+                       ("grad_norm 24 x 1024 fp32", norm_small),
+                       ("clip 3 x 513x777 bf16 column slices", clip_columns),
+                       ("adamw 48 x 1024 fp32, counted on the GPU", adamw_small)):
         log(f"timing {name}")
         calls = [make() for _ in range(3)]
         for f, _ in calls:
