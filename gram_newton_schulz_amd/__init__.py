@@ -2,7 +2,8 @@
 
 The computation lives in the HIP library libgns.so behind the C ABI of
 include/gns.h; this package is its thin Python binding.  tensors.py binds the
-operators over lists of tensors (gradient norm, clipping, AdamW).
+operators over lists of tensors (gradient norm, clipping, AdamW), layers.py the
+token embedding and products in 4-bit floating point.
 """
 from .binding import (  # noqa: F401
     GnsError, gram_ns_batched, standard_ns_batched, gram_workspace_bytes,
@@ -13,4 +14,8 @@ from .binding import (  # noqa: F401
 )
 from .tensors import (  # noqa: F401
     TensorList, GradNorm, tensor_list, adamw_list, grad_norm, clip_grad_norm_, adamw_step,
+)
+from .layers import (  # noqa: F401
+    MXFP4, mxfp4_empty, mxfp4_quantize, mxfp4_quantize_both, mxfp4_dequantize, mxfp4_matmul,
+    mxfp4_matmul_workspace_bytes, embedding, embedding_grad, embedding_grad_workspace_bytes,
 )

@@ -45,6 +45,9 @@ EXPORTS = [
     "gns_gram_batched_noalloc",
     "gns_tensor_list_bytes", "gns_tensor_list_build", "gns_tensor_list_workspace_bytes",
     "gns_grad_norm", "gns_grad_clip", "gns_adamw_step", "gns_adamw_step_counted", "gns_dion3_step_clipped",
+    "gns_embedding", "gns_embedding_grad_workspace_bytes", "gns_embedding_grad",
+    "gns_mxfp4_code_bytes", "gns_mxfp4_scale_bytes", "gns_mxfp4_quantize", "gns_mxfp4_dequantize",
+    "gns_mxfp4_matmul_workspace_bytes", "gns_mxfp4_matmul", "gns_mxfp4_linear_workspace_bytes", "gns_mxfp4_linear",
 ]
 
 
@@ -150,6 +153,28 @@ def lib() -> ctypes.CDLL:
     L.gns_adamw_step.argtypes = [vp, vp, i64, dbl, dbl, dbl, dbl, dbl, vp, vp]
     L.gns_adamw_step_counted.restype = ctypes.c_int
     L.gns_adamw_step_counted.argtypes = [vp, vp, vp, dbl, dbl, dbl, dbl, dbl, vp, vp, sz, vp]
+    # layers (layers.py); gns_mxfp4 structures are passed by address
+    cint = ctypes.c_int
+    L.gns_embedding.restype = cint
+    L.gns_embedding.argtypes = [vp, cint, i64, vp, cint, i64, i64, i64, dbl, vp, cint, i64, vp]
+    L.gns_embedding_grad_workspace_bytes.restype = sz
+    L.gns_embedding_grad_workspace_bytes.argtypes = [i64, i64, i64]
+    L.gns_embedding_grad.restype = cint
+    L.gns_embedding_grad.argtypes = [vp, cint, i64, vp, cint, i64, i64, i64, dbl, vp, cint, i64, cint, vp, sz, vp]
+    for f in (L.gns_mxfp4_code_bytes, L.gns_mxfp4_scale_bytes):
+        f.restype = sz
+        f.argtypes = [i64, i64, i64]
+    L.gns_mxfp4_quantize.restype = cint
+    L.gns_mxfp4_quantize.argtypes = [vp, cint, i64, i64, vp, vp, vp, vp]
+    L.gns_mxfp4_dequantize.restype = cint
+    L.gns_mxfp4_dequantize.argtypes = [vp, vp, cint, vp]
+    for f in (L.gns_mxfp4_matmul_workspace_bytes, L.gns_mxfp4_linear_workspace_bytes):
+        f.restype = sz
+        f.argtypes = [i64, i64, i64, i64]
+    L.gns_mxfp4_matmul.restype = cint
+    L.gns_mxfp4_matmul.argtypes = [vp, vp, vp, cint, i64, i64, cint, vp, sz, vp]
+    L.gns_mxfp4_linear.restype = cint
+    L.gns_mxfp4_linear.argtypes = [vp, cint, i64, i64, i64, vp, vp, cint, i64, i64, cint, vp, sz, vp]
     L.gns_timing_enable.argtypes = [ctypes.c_int]
     L.gns_timing_enable.restype = None
     L.gns_timing_reset.restype = None

@@ -222,4 +222,54 @@ hipError_t launch_adamw_count(int64_t *count, double beta1, double beta2, const 
 hipError_t launch_list_adamw(const ListView &v, bool copy, const AdamwScalars &h, const AdamwBias *bias,
                              const float *grad_scale, hipStream_t s);
 
+// --------------------------------------------------------------------------
+// token embedding (gns_embedding.hip)
+// --------------------------------------------------------------------------
+struct TokenRows {       // a [.][width] array in rows
+  void *data;
+  int dtype;
+  int64_t pitch;         // elements
+};
+// out[i] = scale * weight[tokens[i]], zero for a token outside [0, vocab)
+hipError_t launch_embedding(const void *tokens, int token_bits, int64_t count, const TokenRows &weight, int64_t vocab,
+                            int64_t width, float scale, const TokenRows &out, hipStream_t s);
+size_t embedding_grad_bytes(int64_t count, int64_t vocab, int64_t width);
+hipError_t launch_embedding_grad(const void *tokens, int token_bits, int64_t count, const TokenRows &grad,
+                                 int64_t vocab, int64_t width, float scale, const TokenRows &grad_weight,
+                                 bool accumulate, void *workspace, hipStream_t s);
+
+// --------------------------------------------------------------------------
+// microscaled 4-bit floats (gns_mxfp4.hip); the layout is gns_mxfp4's
+// --------------------------------------------------------------------------
+constexpr int kMxBlock = 32;             // values per scale
+constexpr int kMxGroup = 128;            // columns per word of scales
+struct MxMatrix {
+  uint8_t *codes;
+  uint8_t *scales;
+  int64_t batch, rows, cols;
+  __host__ __device__ int64_t groups() const { return (cols + kMxGroup - 1) / kMxGroup; }
+  __host__ __device__ int64_t pitch() const { return groups() * (kMxGroup / 2); }          // bytes of a row
+  __host__ __device__ int64_t row_blocks() const { return (rows + 31) / 32; }
+  __host__ __device__ int64_t code_bytes() const { return batch * rows * pitch(); }
+  __host__ __device__ int64_t scale_bytes() const { return batch * row_blocks() * groups() * 128; }
+};
+struct MxInput {
+  const void *x;
+  int dtype;
+  int64_t pitch, batch_stride;           // elements
+  const uint8_t *noise;                  // [batch][rows][cols] or null
+};
+struct MxOutput {
+  void *out;
+  int dtype;
+  int64_t pitch, batch_stride;           // elements
+  bool accumulate;
+};
+// by_rows, by_columns: codes null where not wanted
+hipError_t launch_mx_quantize(const MxInput &in, int64_t batch, int64_t rows, int64_t cols, const MxMatrix &by_rows,
+                              const MxMatrix &by_columns, hipStream_t s);
+hipError_t launch_mx_dequantize(const MxMatrix &q, void *out, int dtype, hipStream_t s);
+size_t mx_matmul_bytes(int64_t batch, int64_t m, int64_t n, int64_t k);
+hipError_t launch_mx_matmul(const MxMatrix &a, const MxMatrix &b, const MxOutput &out, void *workspace, hipStream_t s);
+
 }  // namespace gns

@@ -549,6 +549,144 @@ gns_status gns_adamw_step_counted(const gns_tensor_list *list, const void *table
                                   void *stream);
 
 /*
+ * Token embedding: the first layer of a model, and its gradient, which goes
+ * into the gradients that the calls above take the norm of and update from.
+ *   out[i]  = scale * weight[tokens[i]]                     (gns_embedding)
+ *   grad_weight[v] (+)= scale * sum over i with tokens[i] = v of grad[i]
+ *                                                      (gns_embedding_grad)
+ * A token outside [0, vocab) is padding: its output row is zero and its
+ * gradient row is not read.
+ *   tokens       (device) [count] int32 or int64 (token_bits 32 or 64).
+ *   weight, grad_weight  (device) [vocab][width], rows `*_pitch` elements apart.
+ *   out, grad    (device) [count][width], rows `*_pitch` elements apart.
+ *   *_dtype      GNS_F32, GNS_BF16 or GNS_F16, chosen freely.
+ *   scale        finite, used in fp32.
+ * Products and sums are fp32, and each output is rounded once to its type.
+ * Buffers need the alignment of their elements, no more.  A pitch is at least
+ * the width where rows are written; rows that are read may share memory.
+ * GNS_E_SHAPE (a negative size, count > 2^30, vocab >= 2^31, width > 2^24, or
+ * such a pitch), GNS_E_DTYPE, GNS_E_NULL, GNS_E_PARAM (token_bits, a scale
+ * that is not finite, a misaligned address), GNS_E_ALIAS (written memory that
+ * may be read or written as another argument, too).
+ */
+gns_status gns_embedding(const void *tokens, int token_bits, int64_t count, const void *weight,
+                         gns_dtype weight_dtype, int64_t vocab, int64_t width, int64_t weight_pitch,
+                         double scale, void *out, gns_dtype out_dtype, int64_t out_pitch, void *stream);
+
+/*
+ * The gradient.  With accumulate = 0 every row of grad_weight is written (zero
+ * where no token names it); with accumulate = 1 the sums are added in fp32 to
+ * what the rows hold, and rows that no token names are neither read nor
+ * written.  Tokens are sorted first, so that a row's gradients are added up in
+ * an order that depends on the tokens alone: the result is the same in every
+ * run.
+ *   workspace    (device) >= gns_embedding_grad_workspace_bytes(count, vocab,
+ *                width) bytes, 256-byte aligned, clobbered.
+ */
+size_t gns_embedding_grad_workspace_bytes(int64_t count, int64_t vocab, int64_t width);
+gns_status gns_embedding_grad(const void *tokens, int token_bits, int64_t count, const void *grad,
+                              gns_dtype grad_dtype, int64_t grad_pitch, int64_t vocab, int64_t width,
+                              double scale, void *grad_weight, gns_dtype grad_weight_dtype,
+                              int64_t grad_weight_pitch, int accumulate, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/*
+ * Microscaled 4-bit floating point (MXFP4, "OCP Microscaling Formats (MX)
+ * Specification" v1.0): blocks of 32 consecutive values of a row, each a 4-bit
+ * float (E2M1: 0, 0.5, 1, 1.5, 2, 3, 4, 6 with a sign) times one power of two
+ * per block (E8M0).  The products of a linear layer y = x w^T and of its
+ * gradients take both factors so, with blocks along the axis they sum over:
+ *   y  = Q(x) Q(w)^T      dx = Q(dy) Q(w^T)^T      dw = Q(dy^T) Q(x^T)^T
+ * The weights are those that gns_dion3_step and gns_adamw_step keep in fp32.
+ *
+ * A batch of rows x cols matrices, K = cols rounded up to 128:
+ *   codes   (device) [batch][rows][K / 2] bytes; element 2 i of a row in the
+ *           low half of byte i.  16-byte aligned.
+ *   scales  (device) [batch][ceil(rows / 32)][K / 128][32][4] bytes: the four
+ *           scales of 128 columns of one row are one word, and the words of 32
+ *           rows one line of the cache.  Byte s is 2^(s - 127), 255 is NaN.
+ *           16-byte aligned.
+ * Codes past a row's end, and scales of blocks and rows that do not exist, are
+ * written as zero and are expected to be zero.
+ */
+typedef struct {
+  void *codes;
+  void *scales;
+  int64_t batch, rows, cols;   /* rows, cols <= 2^23 */
+} gns_mxfp4;
+
+/* Bytes of codes and of scales (0 for sizes that the calls refuse). */
+size_t gns_mxfp4_code_bytes(int64_t batch, int64_t rows, int64_t cols);
+size_t gns_mxfp4_scale_bytes(int64_t batch, int64_t rows, int64_t cols);
+
+/*
+ * Quantises x, in blocks along its rows, along its columns, or both in one
+ * pass over x.
+ *   x            (device) [batch][rows][cols] in dtype (GNS_F32, GNS_BF16 or
+ *                GNS_F16); rows `pitch` and matrices `batch_stride` elements
+ *                apart, elements of a row consecutive.
+ *   by_rows      batch x rows x cols: Q(x), or NULL.
+ *   by_columns   batch x cols x rows: Q(x^T), or NULL.
+ *   noise        (device) [batch][rows][cols] bytes, or NULL.
+ * With a = max |x| of a block, its scale is 2^(floor(log2 a) - 2) (no smaller
+ * than 2^-127, also for a block of zeros), and values are rounded to nearest,
+ * ties to the even code, those above 6 times the scale to 6.
+ * With noise values are rounded up with their probability: from n + f steps
+ * of the grid to n + 1 where 256 f > noise + 0.5.  There the scale is doubled
+ * when a would be above 6, so that no value is cut off and uniform bytes leave
+ * the mean in place (to 1/512 of a step).
+ * A block that holds Inf or NaN has scale 255 and zero codes: it stands for
+ * NaN.
+ * GNS_E_SHAPE (sizes of the three that differ, negative or too large, a
+ * negative pitch), GNS_E_DTYPE, GNS_E_NULL, GNS_E_PARAM (a misaligned
+ * address), GNS_E_ALIAS (written memory that overlaps another argument).
+ */
+gns_status gns_mxfp4_quantize(const void *x, gns_dtype dtype, int64_t pitch, int64_t batch_stride,
+                              const uint8_t *noise, const gns_mxfp4 *by_rows, const gns_mxfp4 *by_columns,
+                              void *stream);
+
+/*
+ * The values that codes and scales stand for.
+ *   out          (device) [batch][rows][cols] contiguous, in dtype.  Exact in
+ *                GNS_F32 and GNS_BF16 (but for 2^128, to which noise may round
+ *                the largest of their numbers up: Inf); rounded once in GNS_F16.
+ */
+gns_status gns_mxfp4_dequantize(const gns_mxfp4 *q, void *out, gns_dtype dtype, void *stream);
+
+/*
+ * out = a b^T for every matrix of the batch: [a.rows][b.rows], summed over
+ * cols.  Products are exact, sums are fp32, and a result is rounded once.
+ *   out          (device) rows `out_pitch` (>= b.rows) and matrices
+ *                `out_batch_stride` elements apart, in out_dtype.
+ *   accumulate   1: out += a b^T, the sum in fp32 rounded once.
+ *   workspace    (device) >= gns_mxfp4_matmul_workspace_bytes(batch, a.rows,
+ *                b.rows, cols) bytes, 256-byte aligned, clobbered; may be NULL
+ *                where that is 0.
+ * Sums have a fixed order: the result is the same in every run.
+ * GNS_E_SHAPE (different batches or cols, matrices of out that overlap),
+ * GNS_E_DTYPE, GNS_E_NULL, GNS_E_PARAM (a misaligned address, accumulate not
+ * 0 or 1), GNS_E_WORKSPACE, GNS_E_ALIAS.
+ */
+size_t gns_mxfp4_matmul_workspace_bytes(int64_t batch, int64_t m, int64_t n, int64_t k);
+gns_status gns_mxfp4_matmul(const gns_mxfp4 *a, const gns_mxfp4 *b, void *out, gns_dtype out_dtype,
+                            int64_t out_pitch, int64_t out_batch_stride, int accumulate, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
+/*
+ * out = Q(x) w^T, or out += Q(x) w^T: gns_mxfp4_quantize of x by rows, then
+ * gns_mxfp4_matmul, with Q(x) in the workspace.
+ *   x            (device) [w.batch][m][w.cols] in dtype, as for
+ *                gns_mxfp4_quantize.
+ *   workspace    (device) >= gns_mxfp4_linear_workspace_bytes(w.batch, m,
+ *                w.rows, w.cols) bytes, 256-byte aligned, clobbered.
+ */
+size_t gns_mxfp4_linear_workspace_bytes(int64_t batch, int64_t m, int64_t n, int64_t k);
+gns_status gns_mxfp4_linear(const void *x, gns_dtype dtype, int64_t pitch, int64_t batch_stride, int64_t m,
+                            const gns_mxfp4 *w, void *out, gns_dtype out_dtype, int64_t out_pitch,
+                            int64_t out_batch_stride, int accumulate, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
+/*
  * Enqueue a check of a row subset: writes to *result (device int32) 0 when
  * every row_idx[b][i] is in [0, n) and the k indices of each matrix are
  * distinct, 1 when an index is out of range, 2 when an index repeats.

@@ -9,3 +9,4 @@ from .newton_schulz import (  # noqa: F401
     flops_standard, flops_gram, restart_model, restart_sweep,
 )
 from .tensor_ops import adamw, grad_norm  # noqa: F401
+from . import layers  # noqa: F401
