@@ -69,11 +69,15 @@ struct EmbeddingSizes {
   int token_bytes() const { return token_bits / 8; }
 };
 
+bool embedding_size(int64_t count, int64_t vocab, int64_t width) {
+  return count >= 0 && count <= kMaxTokens && vocab >= 0 && vocab <= kMaxVocab && width >= 0 && width <= kMaxWidth &&
+         (width == 0 || std::max(count, vocab) <= kMaxElements / width);
+}
+
 gns_status check_embedding(const EmbeddingSizes &z, const void *table, gns_dtype table_dtype, int64_t table_pitch,
                            const void *rows, gns_dtype rows_dtype, int64_t rows_pitch, double scale,
                            bool table_written) {
-  if (z.count < 0 || z.count > kMaxTokens || z.vocab < 0 || z.vocab > kMaxVocab || z.width < 0 ||
-      z.width > kMaxWidth || table_pitch < 0 || rows_pitch < 0 || table_pitch > kMaxSpan / kMaxVocab ||
+  if (!embedding_size(z.count, z.vocab, z.width) || table_pitch < 0 || rows_pitch < 0 || table_pitch > kMaxSpan / kMaxVocab ||
       rows_pitch > kMaxSpan / kMaxTokens)
     return GNS_E_SHAPE;
   if ((table_written ? z.vocab : z.count) > 1 && (table_written ? table_pitch : rows_pitch) < z.width)
@@ -178,7 +182,7 @@ gns_status gns_embedding(const void *tokens, int token_bits, int64_t count, cons
 }
 
 size_t gns_embedding_grad_workspace_bytes(int64_t count, int64_t vocab, int64_t width) {
-  if (count < 0 || count > kMaxTokens || vocab < 0 || vocab > kMaxVocab || width < 0 || width > kMaxWidth) return 0;
+  if (!embedding_size(count, vocab, width)) return 0;
   return std::max<size_t>(round_256(gns::embedding_grad_bytes(count, vocab, width)), 256);
 }
 
