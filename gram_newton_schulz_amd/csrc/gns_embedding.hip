@@ -19,14 +19,13 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "gns_elem.h"
 #include "gns_kernels.h"
 
 namespace gns {
 namespace {
-
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 template <class F>
 hipError_t with_type(int dtype, F &&f) {
@@ -69,97 +68,117 @@ struct Tokens {
 // rows of a table or of gradients, eight elements per thread
 // ---------------------------------------------------------------------------
 // Threads work in groups of `lanes` (a power of two up to 256) on one row, and
-// a thread has eight columns: eight consecutive ones where rows begin on 16
-// bytes (WIDE), else every lanes-th, so that a group's accesses stay together.
+// a thread has eight columns of a block of 8 lanes:
+//   OCTETS   eight consecutive ones: both arrays have 16 bits and rows that
+//            begin on 16 bytes
+//   QUADS    twice four consecutive ones, so that neighbours' 16-byte accesses
+//            of an fp32 array meet: rows on 16 bytes, or 8 of a 16-bit array
+//   SINGLES  every lanes-th one: any other rows
+enum Spread { SINGLES, QUADS, OCTETS };
 constexpr int kColumns = 8;
 
 struct Columns {
-  int64_t first;      // the thread's first column
-  int step;           // to its next one
-  int n;              // how many it has
+  int first, lanes, width;
+  __device__ __forceinline__ Columns(Spread m, int64_t block, int lane, int lanes_, int64_t width_)
+      : first(static_cast<int>(block) * lanes_ * kColumns + lane * (m == OCTETS ? 8 : m == QUADS ? 4 : 1)),
+        lanes(lanes_), width(static_cast<int>(width_)) {}
+  template <Spread M>
+  __device__ __forceinline__ int at(int k) const {
+    return M == OCTETS ? first + k : M == QUADS ? first + k / 4 * 4 * lanes + k % 4 : first + k * lanes;
+  }
 };
 
-template <bool WIDE>
-__device__ __forceinline__ Columns columns_of(int64_t block, int lane, int lanes, int64_t width) {
-  const int64_t base = block * lanes * kColumns;
-  Columns c;
-  c.first = base + (WIDE ? lane * kColumns : lane);
-  c.step = WIDE ? 1 : lanes;
-  const int64_t left = width - c.first;
-  c.n = left <= 0 ? 0 : static_cast<int>(min<int64_t>(kColumns, WIDE ? left : (left + lanes - 1) / lanes));
-  return c;
-}
-
-// (a row's last piece may be short; the others are whole and take 16-byte accesses)
-template <class T, bool WIDE>
+// (a row's last piece may be short; the others take one access each)
+template <class T, Spread M>
 __device__ __forceinline__ void load_columns(const typename T::S *row, const Columns &c, float *v) {
   using S = typename T::S;
-  if (WIDE && c.n == kColumns) {
-    const u32x4 *p = reinterpret_cast<const u32x4 *>(row + c.first);
-    if constexpr (sizeof(S) == 4) {
-      const u32x4 a = p[0], b = p[1];
+  constexpr int N = M == OCTETS ? 8 : M == QUADS ? 4 : 1;      // of one access
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[i] = __uint_as_float(a[i]);
-        v[4 + i] = __uint_as_float(b[i]);
+  for (int k = 0; k < kColumns; k += N) {
+    const int at = c.at<M>(k);
+    if (N > 1 && at + N <= c.width) {
+      if constexpr (sizeof(S) == 4) {
+#pragma unroll
+        for (int q = 0; q < N; q += 4) {
+          const float4 a = *reinterpret_cast<const float4 *>(row + at + q);
+          v[k + q] = a.x, v[k + q + 1] = a.y, v[k + q + 2] = a.z, v[k + q + 3] = a.w;
+        }
+      } else {
+        uint32_t a[4];
+        if constexpr (M == OCTETS) *reinterpret_cast<uint4 *>(a) = *reinterpret_cast<const uint4 *>(row + at);
+        else *reinterpret_cast<uint2 *>(a) = *reinterpret_cast<const uint2 *>(row + at);
+#pragma unroll
+        for (int q = 0; q < N; q += 2) {
+          v[k + q] = T::ld(static_cast<S>(a[q / 2] & 0xffff));
+          v[k + q + 1] = T::ld(static_cast<S>(a[q / 2] >> 16));
+        }
       }
     } else {
-      const u32x4 a = p[0];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = T::ld(static_cast<S>(a[i] & 0xffff));
-        v[2 * i + 1] = T::ld(static_cast<S>(a[i] >> 16));
-      }
+      for (int q = 0; q < N; ++q) v[k + q] = at + q < c.width ? T::ld(row[at + q]) : 0.0f;
     }
-    return;
   }
-#pragma unroll
-  for (int i = 0; i < kColumns; ++i) v[i] = i < c.n ? T::ld(row[c.first + i * c.step]) : 0.0f;
 }
 
-template <class T, bool WIDE>
+// ONCE: fp32 rows that are not read again here have the streaming hint (32768 x
+// 4096 fp32 rows of a gradient, mostly cleared: 210 us with it, 227 without).
+template <class T, Spread M, bool ONCE = false>
 __device__ __forceinline__ void store_columns(typename T::S *row, const Columns &c, const float *v) {
   using S = typename T::S;
-  if (WIDE && c.n == kColumns) {
-    u32x4 *p = reinterpret_cast<u32x4 *>(row + c.first);
-    if constexpr (sizeof(S) == 4) {
-      u32x4 a, b;
+  constexpr int N = M == OCTETS ? 8 : M == QUADS ? 4 : 1;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        a[i] = __float_as_uint(v[i]);
-        b[i] = __float_as_uint(v[4 + i]);
+  for (int k = 0; k < kColumns; k += N) {
+    const int at = c.at<M>(k);
+    if (N > 1 && at + N <= c.width) {
+      if constexpr (sizeof(S) == 4) {
+#pragma unroll
+        for (int q = 0; q < N; q += 4) {
+          const float4 a = make_float4(v[k + q], v[k + q + 1], v[k + q + 2], v[k + q + 3]);
+          if constexpr (ONCE) st_once(reinterpret_cast<float4 *>(row + at + q), a);
+          else *reinterpret_cast<float4 *>(row + at + q) = a;
+        }
+      } else {
+        uint32_t a[4];
+#pragma unroll
+        for (int q = 0; q < N; q += 2) a[q / 2] = T::st2(v[k + q], v[k + q + 1]);
+        if constexpr (M == OCTETS) *reinterpret_cast<uint4 *>(row + at) = *reinterpret_cast<uint4 *>(a);
+        else *reinterpret_cast<uint2 *>(row + at) = *reinterpret_cast<uint2 *>(a);
       }
-      p[0] = a;
-      p[1] = b;
     } else {
-      u32x4 a;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) a[i] = T::st2(v[2 * i], v[2 * i + 1]);
-      p[0] = a;
+      for (int q = 0; q < N; ++q)
+        if (at + q < c.width) row[at + q] = T::st(v[k + q]);
     }
-    return;
   }
-#pragma unroll
-  for (int i = 0; i < kColumns; ++i)
-    if (i < c.n) row[c.first + i * c.step] = T::st(v[i]);
 }
 
-// Threads to a row: enough for its columns, at most a workgroup.
-int lanes_for(int64_t width) {
+// Threads to a row: enough for its columns, at most `most`.
+int lanes_for(int64_t width, int most = 256) {
   int lanes = 1;
-  while (lanes < 256 && lanes * kColumns < width) lanes *= 2;
+  while (lanes < most && lanes * kColumns < width) lanes *= 2;
   return lanes;
 }
 
-bool wide_rows(const TokenRows &r) {
-  const int64_t elem = dtype_size(r.dtype);
-  return reinterpret_cast<uintptr_t>(r.data) % 16 == 0 && r.pitch * elem % 16 == 0;
+Spread spread_of(const TokenRows &a, const TokenRows &b) {
+  auto on = [](const TokenRows &r, int bytes) {
+    return reinterpret_cast<uintptr_t>(r.data) % bytes == 0 && r.pitch * dtype_size(r.dtype) % bytes == 0;
+  };
+  if (a.dtype != DT_F32 && b.dtype != DT_F32 && on(a, 16) && on(b, 16)) return OCTETS;
+  return on(a, 4 * dtype_size(a.dtype)) && on(b, 4 * dtype_size(b.dtype)) ? QUADS : SINGLES;
+}
+
+// f(the spread as a constant)
+template <class F>
+hipError_t with_spread(Spread m, F &&f) {
+  if (m == OCTETS) return f(std::integral_constant<Spread, OCTETS>{});
+  if (m == QUADS) return f(std::integral_constant<Spread, QUADS>{});
+  return f(std::integral_constant<Spread, SINGLES>{});
 }
 
 // ---------------------------------------------------------------------------
 // lookup
 // ---------------------------------------------------------------------------
-template <class TW, class TO, bool WIDE>
+template <class TW, class TO, Spread M>
 __global__ void __launch_bounds__(256)
 embedding_rows(Tokens tokens, int64_t count, const typename TW::S *weight, int64_t vocab, int64_t width,
                int64_t weight_pitch, float scale, typename TO::S *out, int64_t out_pitch, int lanes, int64_t blocks) {
@@ -168,27 +187,30 @@ embedding_rows(Tokens tokens, int64_t count, const typename TW::S *weight, int64
   const int64_t i = unit / blocks;
   if (i >= count) return;
   const int64_t t = tokens[i];
-  const Columns c = columns_of<WIDE>(unit % blocks, lane, lanes, width);
+  const Columns c(M, unit % blocks, lane, lanes, width);
   float v[kColumns] = {0, 0, 0, 0, 0, 0, 0, 0};
   if (t >= 0 && t < vocab) {
-    load_columns<TW, WIDE>(weight + t * weight_pitch, c, v);
+    load_columns<TW, M>(weight + t * weight_pitch, c, v);
 #pragma unroll
     for (int k = 0; k < kColumns; ++k) v[k] = times(v[k], scale);
   }
-  store_columns<TO, WIDE>(out + i * out_pitch, c, v);
+  store_columns<TO, M>(out + i * out_pitch, c, v);
 }
 
 // ---------------------------------------------------------------------------
 // sort
 // ---------------------------------------------------------------------------
-constexpr int kTile = 4096;            // tokens per workgroup of 1024 threads
-constexpr int kEach = kTile / 1024;
+constexpr int kOnce = 4;               // tokens per thread of 1024: of the sort in one workgroup
+constexpr int kEach = 2;               // ... and of a tile
+constexpr int kTile = kEach * 1024;
+constexpr int kFewTiles = 32;          // so few are summed by every workgroup itself
 constexpr int kMaxBits = 10;           // of a digit: one thread per value
 
-// Rank of each of a tile's tokens among those of its digit.  Wave w holds
-// tokens 256 w .. 256 w + 255, 64 at a time in order, so ranks keep the order.
+// Rank of each of a workgroup's tokens among those of its digit.  A wave holds
+// 64 N consecutive tokens, 64 at a time in order, so ranks keep the order.
 // before[w * bins + d] becomes the number of digit d in earlier waves, *total
 // (thread d) that of the whole tile.
+template <int N>
 __device__ __forceinline__ void tile_ranks(const uint32_t *digit, const bool *live, int bits, uint16_t *before,
                                            uint32_t *rank, uint32_t *total) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, bins = 1 << bits;
@@ -197,12 +219,14 @@ __device__ __forceinline__ void tile_ranks(const uint32_t *digit, const bool *li
   volatile uint16_t *mine = before + wave * bins;
   const uint64_t lower = (uint64_t(1) << lane) - 1;
 #pragma unroll
-  for (int j = 0; j < kEach; ++j) {
+  for (int j = 0; j < N; ++j) {
     uint64_t same = __ballot(live[j]);
-    for (int b = 0; b < bits; ++b) {
-      const bool one = digit[j] >> b & 1;
-      const uint64_t with = __ballot(one);
-      same &= one ? with : ~with;
+#pragma unroll
+    for (int b = 0; b < kMaxBits; ++b) {
+      if (b >= bits) break;
+      const int32_t one = static_cast<int32_t>(digit[j] << (31 - b)) >> 31;   // the bit, in every place
+      const uint64_t with = __ballot(one), flip = ~static_cast<uint64_t>(static_cast<int64_t>(one));
+      same &= with ^ flip;
     }
     if (live[j]) {
       const uint32_t so_far = mine[digit[j]];
@@ -247,41 +271,45 @@ __device__ __forceinline__ uint32_t scan_1024(uint32_t v, uint32_t *parts, uint3
   return base + run - v;
 }
 
-// Up to kTile tokens: all digits in one workgroup.
+// Up to 1024 N tokens: all digits in one workgroup.
+template <int N>
 __global__ void __launch_bounds__(1024)
-token_sort_once(Tokens tokens, int count, uint32_t vocab, int passes, int bits, uint32_t *keys, uint32_t *places) {
+token_sort_once(Tokens tokens, int count, uint32_t vocab, int passes, int bits, uint32_t *keys, uint32_t *places,
+                uint32_t *joins) {
+  if (threadIdx.x < 2) joins[threadIdx.x] = 0;
   __shared__ uint16_t before[16 << kMaxBits];
   __shared__ uint32_t first[1 << kMaxBits], parts[16];
-  __shared__ uint32_t key_at[kTile], place_at[kTile];
+  __shared__ uint32_t key_at[1024 * N];
+  __shared__ uint16_t place_at[1024 * N];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int mine = wave * 64 * kEach + lane;
-  uint32_t key[kEach], place[kEach];
-  bool live[kEach];
+  const int mine = wave * 64 * N + lane;
+  uint32_t key[N], place[N];
+  bool live[N];
 #pragma unroll
-  for (int j = 0; j < kEach; ++j) {
+  for (int j = 0; j < N; ++j) {
     const int i = mine + 64 * j;
     live[j] = i < count;
     key[j] = live[j] ? tokens.key(i, vocab) : 0;
     place[j] = i;
   }
   for (int pass = 0; pass < passes; ++pass) {
-    uint32_t digit[kEach], rank[kEach], total, all;
+    uint32_t digit[N], rank[N], total, all;
 #pragma unroll
-    for (int j = 0; j < kEach; ++j) digit[j] = key[j] >> (pass * bits) & ((1u << bits) - 1);
-    tile_ranks(digit, live, bits, before, rank, &total);
+    for (int j = 0; j < N; ++j) digit[j] = key[j] >> (pass * bits) & ((1u << bits) - 1);
+    tile_ranks<N>(digit, live, bits, before, rank, &total);
     const uint32_t at = scan_1024(tid < (1 << bits) ? total : 0, parts, &all);
     if (tid < (1 << bits)) first[tid] = at;
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < kEach; ++j) {
+    for (int j = 0; j < N; ++j) {
       if (!live[j]) continue;
       const uint32_t to = first[digit[j]] + before[(wave << bits) + digit[j]] + rank[j];
       key_at[to] = key[j];
-      place_at[to] = place[j];
+      place_at[to] = static_cast<uint16_t>(place[j]);
     }
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < kEach; ++j) {
+    for (int j = 0; j < N; ++j) {
       if (!live[j]) continue;
       key[j] = key_at[mine + 64 * j];
       place[j] = place_at[mine + 64 * j];
@@ -289,7 +317,7 @@ token_sort_once(Tokens tokens, int count, uint32_t vocab, int passes, int bits, 
     __syncthreads();
   }
 #pragma unroll
-  for (int j = 0; j < kEach; ++j) {
+  for (int j = 0; j < N; ++j) {
     if (!live[j]) continue;
     keys[mine + 64 * j] = key[j];
     places[mine + 64 * j] = place[j];
@@ -312,7 +340,8 @@ token_count(Tokens tokens, const uint32_t *keys, int64_t count, uint32_t vocab, 
   if (tid < (1 << bits)) counts[static_cast<int64_t>(tid) * gridDim.x + blockIdx.x] = n[tid];
 }
 
-// ... the sums of those before each, in place ...
+// ... the sums of those before each, in place (of few tiles the next kernel
+// takes them itself, a launch less: 4.6 us) ...
 __global__ void __launch_bounds__(1024) token_scan(uint32_t *counts, int64_t n) {
   __shared__ uint32_t parts[16];
   uint32_t carry = 0;
@@ -334,9 +363,10 @@ __global__ void __launch_bounds__(1024) token_scan(uint32_t *counts, int64_t n) 
 // ... and every token to its place.
 __global__ void __launch_bounds__(1024)
 token_scatter(Tokens tokens, const uint32_t *keys, const uint32_t *places, int64_t count, uint32_t vocab, int shift,
-              int bits, const uint32_t *counts, uint32_t *keys_out, uint32_t *places_out) {
+              int bits, const uint32_t *counts, uint32_t *keys_out, uint32_t *places_out, uint32_t *joins) {
   __shared__ uint16_t before[16 << kMaxBits];
-  __shared__ uint32_t first[1 << kMaxBits];
+  __shared__ uint32_t first[1 << kMaxBits], parts[16];
+  if (blockIdx.x == 0 && threadIdx.x < 2) joins[threadIdx.x] = 0;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t mine = static_cast<int64_t>(blockIdx.x) * kTile + wave * 64 * kEach + lane;
   uint32_t key[kEach], place[kEach], digit[kEach], rank[kEach], total;
@@ -349,8 +379,22 @@ token_scatter(Tokens tokens, const uint32_t *keys, const uint32_t *places, int64
     place[j] = !live[j] ? 0 : keys ? places[i] : static_cast<uint32_t>(i);
     digit[j] = key[j] >> shift & ((1u << bits) - 1);
   }
-  if (tid < (1 << bits)) first[tid] = counts[static_cast<int64_t>(tid) * gridDim.x + blockIdx.x];
-  tile_ranks(digit, live, bits, before, rank, &total);
+  const int tiles = gridDim.x;
+  if (tiles > kFewTiles) {
+    if (tid < (1 << bits)) first[tid] = counts[static_cast<int64_t>(tid) * tiles + blockIdx.x];
+  } else {
+    uint32_t all, earlier = 0, sum = 0;
+    if (tid < (1 << bits)) {
+      for (int k = 0; k < tiles; ++k) {
+        const uint32_t n = counts[tid * tiles + k];
+        earlier += k < static_cast<int>(blockIdx.x) ? n : 0;
+        sum += n;
+      }
+    }
+    const uint32_t base = scan_1024(sum, parts, &all);
+    if (tid < (1 << bits)) first[tid] = base + earlier;
+  }
+  tile_ranks<kEach>(digit, live, bits, before, rank, &total);
   __syncthreads();
 #pragma unroll
   for (int j = 0; j < kEach; ++j) {
@@ -375,10 +419,14 @@ struct Sums {
   int64_t pieces;
   int lanes;                       // threads to a row
   int64_t blocks;                  // blocks of columns
-  float *partials;                 // [pieces][2][width]: of the run that reaches in, of the one that reaches out
-  int64_t clear_groups;            // workgroups that clear rows
+  float *partials;                 // [pieces][2][partial_pitch]
+  int64_t partial_pitch;           // the width, in whole 16 bytes
+  int64_t work;                    // workgroups that add rows up; those behind them clear rows
+  uint32_t *joins;                 // pieces with a run that begins there and reaches out: how many short ones, how
+                                   // many long ones, which (the long ones from the end)
 };
-constexpr int kClearRows = 16;     // rows of the table per such workgroup
+constexpr int kClearRows = 8;     // rows of the table per such workgroup
+constexpr int kShortRun = 8;       // pieces of a run that one group of threads adds up
 
 __device__ __forceinline__ int64_t first_not_below(const uint32_t *keys, int64_t n, uint32_t v) {
   int64_t low = 0, high = n;
@@ -390,7 +438,7 @@ __device__ __forceinline__ int64_t first_not_below(const uint32_t *keys, int64_t
   return low;
 }
 
-template <class TW, bool WIDE>
+template <class TW, Spread M>
 __device__ __forceinline__ void write_row(const Sums &p, typename TW::S *weight, uint32_t v, const Columns &c,
                                           float *acc) {
   typename TW::S *row = weight + static_cast<int64_t>(v) * p.weight_pitch;
@@ -399,28 +447,26 @@ __device__ __forceinline__ void write_row(const Sums &p, typename TW::S *weight,
   for (int k = 0; k < kColumns; ++k) out[k] = times(acc[k], p.scale);
   if (p.accumulate) {
     float old[kColumns];
-    load_columns<TW, WIDE>(row, c, old);
+    load_columns<TW, M>(row, c, old);
 #pragma unroll
     for (int k = 0; k < kColumns; ++k) out[k] += old[k];
   }
-  store_columns<TW, WIDE>(row, c, out);
+  store_columns<TW, M, true>(row, c, out);
 }
 
-__device__ __forceinline__ void write_partial(const Sums &p, int64_t piece, int which, const Columns &c,
-                                              const float *acc) {
-  float *row = p.partials + (piece * 2 + which) * p.width;
-#pragma unroll
-  for (int k = 0; k < kColumns; ++k)
-    if (k < c.n) row[c.first + k * c.step] = acc[k];
+// Partial sums: of the run that reaches into a piece (which = 0) or out of it.
+__device__ __forceinline__ float *partial_row(const Sums &p, int64_t piece, int which) {
+  return p.partials + (piece * 2 + which) * p.partial_pitch;
 }
 
-template <class TG, class TW, bool WIDE>
+template <class TG, class TW, Spread M, bool WAVE>
 __global__ void __launch_bounds__(256)
 embedding_sums(Sums p, const typename TG::S *grad, typename TW::S *weight) {
   const int64_t group = group_index();
-  if (group < p.clear_groups) {
+  if (group >= p.work) {
+    if (p.accumulate) return;           // (a grid in two dimensions may have some to spare)
     __shared__ int absent[kClearRows];
-    const int64_t row0 = group * kClearRows;
+    const int64_t row0 = (group - p.work) * kClearRows;
     if (threadIdx.x < kClearRows) {
       const int64_t v = row0 + threadIdx.x;
       bool none = v < p.vocab;
@@ -436,39 +482,49 @@ embedding_sums(Sums p, const typename TG::S *grad, typename TW::S *weight) {
       if (!absent[r]) continue;
       typename TW::S *row = weight + (row0 + r) * p.weight_pitch;
       for (int64_t b = 0; b * 256 * kColumns < p.width; ++b)
-        store_columns<TW, WIDE>(row, columns_of<WIDE>(b, threadIdx.x, 256, p.width), zero);
+        store_columns<TW, M, true>(row, Columns(M, b, threadIdx.x, 256, p.width), zero);
     }
     return;
   }
   const int groups = 256 / p.lanes, lane = threadIdx.x % p.lanes;
-  const int64_t unit = (group - p.clear_groups) * groups + threadIdx.x / p.lanes;
+  const int64_t unit = group * groups + threadIdx.x / p.lanes;
   const int64_t piece = unit / p.blocks;
   if (piece >= p.pieces) return;
-  const Columns c = columns_of<WIDE>(unit % p.blocks, lane, p.lanes, p.width);
+  const Columns c(M, unit % p.blocks, lane, p.lanes, p.width);
   const int64_t begin = piece * p.piece, end = min(begin + p.piece, p.count);
-  uint32_t run = p.keys[begin];
+  const int n = static_cast<int>(end - begin);
+  // A wave that has one piece holds its tokens, one per lane, and takes them
+  // from there; narrow rows' groups share waves and read them one by one.
+  const int at = static_cast<int>(min<int64_t>(threadIdx.x & 63, n - 1));
+  const uint32_t my_key = p.keys[begin + at], my_place = p.places[begin + at];
+  auto key_of = [&](int i) -> uint32_t {
+    return WAVE ? static_cast<uint32_t>(__builtin_amdgcn_readlane(my_key, i)) : p.keys[begin + i];
+  };
+  auto place_of = [&](int i) -> uint32_t {
+    return WAVE ? static_cast<uint32_t>(__builtin_amdgcn_readlane(my_place, i)) : p.places[begin + i];
+  };
+  uint32_t run = key_of(0);
   bool reaches_in = begin > 0 && p.keys[begin - 1] == run;
   float acc[kColumns] = {0, 0, 0, 0, 0, 0, 0, 0};
-  constexpr int kAhead = 4;
-  for (int64_t i = begin; i < end; i += kAhead) {
+  constexpr int kAhead = 8;
+  for (int i = 0; i < n; i += kAhead) {
     uint32_t key[kAhead];
     float v[kAhead][kColumns];
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
-      const bool in = i + a < end;
-      key[a] = in ? p.keys[i + a] : p.vocab;
-      if (key[a] < p.vocab) load_columns<TG, WIDE>(grad + static_cast<int64_t>(p.places[i + a]) * p.grad_pitch, c, v[a]);
+      key[a] = i + a < n ? key_of(i + a) : p.vocab;
+      if (key[a] < p.vocab) load_columns<TG, M>(grad + static_cast<int64_t>(place_of(i + a)) * p.grad_pitch, c, v[a]);
     }
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
-      if (key[a] != run && run < p.vocab && i + a < end) {
-        if (reaches_in) write_partial(p, piece, 0, c, acc);
-        else write_row<TW, WIDE>(p, weight, run, c, acc);
+      if (key[a] != run && run < p.vocab && i + a < n) {
+        if (reaches_in) store_columns<EF32, M>(partial_row(p, piece, 0), c, acc);
+        else write_row<TW, M>(p, weight, run, c, acc);
         reaches_in = false;
 #pragma unroll
         for (int k = 0; k < kColumns; ++k) acc[k] = 0.0f;
       }
-      if (i + a < end) run = key[a];
+      if (i + a < n) run = key[a];
       if (key[a] < p.vocab) {
 #pragma unroll
         for (int k = 0; k < kColumns; ++k) acc[k] += v[a][k];
@@ -477,38 +533,73 @@ embedding_sums(Sums p, const typename TG::S *grad, typename TW::S *weight) {
   }
   if (run >= p.vocab) return;                          // padding
   const bool reaches_out = end < p.count && p.keys[end] == run;
-  if (reaches_in || reaches_out) write_partial(p, piece, reaches_in ? 0 : 1, c, acc);
-  else write_row<TW, WIDE>(p, weight, run, c, acc);
+  if (reaches_out && !reaches_in && lane == 0 && unit % p.blocks == 0) {
+    const int64_t far = begin + static_cast<int64_t>(kShortRun) * p.piece;
+    const bool is_long = far < p.count && p.keys[far] == run;
+    const int64_t i = atomicAdd(p.joins + (is_long ? 1 : 0), 1u);
+    p.joins[is_long ? 1 + p.pieces - i : 2 + i] = static_cast<uint32_t>(piece);
+  }
+  if (reaches_in || reaches_out) store_columns<EF32, M>(partial_row(p, piece, reaches_in ? 0 : 1), c, acc);
+  else write_row<TW, M>(p, weight, run, c, acc);
 }
 
-// The runs that begin in a piece and reach out of it.
-template <class TW, bool WIDE>
-__global__ void __launch_bounds__(256) embedding_join(Sums p, typename TW::S *weight) {
-  const int groups = 256 / p.lanes, lane = threadIdx.x % p.lanes;
-  const int64_t unit = group_index() * groups + threadIdx.x / p.lanes;
-  const int64_t piece = unit / p.blocks, begin = piece * p.piece, end = begin + p.piece;
-  if (piece >= p.pieces || end >= p.count) return;
-  const uint32_t run = p.keys[end - 1];
-  if (run >= p.vocab || p.keys[end] != run) return;
-  if (p.keys[begin] == run && begin > 0 && p.keys[begin - 1] == run) return;
-  const int64_t last = (first_not_below(p.keys, p.count, run + 1) - 1) / p.piece;
-  const Columns c = columns_of<WIDE>(unit % p.blocks, lane, p.lanes, p.width);
-  float acc[kColumns];
-  load_columns<EF32, false>(p.partials + (piece * 2 + 1) * p.width, c, acc);
-  constexpr int kAhead = 4;
-  for (int64_t i = piece + 1; i <= last; i += kAhead) {
-    float v[kAhead][kColumns];
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a)
-      if (i + a <= last) load_columns<EF32, false>(p.partials + (i + a) * 2 * p.width, c, v[a]);
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
-      if (i + a > last) continue;
-#pragma unroll
-      for (int k = 0; k < kColumns; ++k) acc[k] += v[a][k];
+// The runs that begin in a piece and reach out of it, whose number is known on
+// the GPU only: workgroups take them from the lists that embedding_sums left.
+// The partial sums of a run are cut into as many consecutive parts as there
+// are groups of threads on a row; each group adds one up, and then the first
+// those in order.  Short runs have groups as wide as the row (up to 256
+// threads), long ones of kJoinLanes, so that 16 share their parts.  (10007 x
+// 1531 values with a run of 370 partial sums: 98 us with wide groups only; 32768
+// x 4096 with 600 short runs: 65 us with narrow groups only.)
+constexpr int kJoinLanes = 16;
+constexpr int kJoinGroups = 2048;
+
+template <class TW, Spread M>
+__global__ void __launch_bounds__(256) embedding_join(Sums p, typename TW::S *weight, int long_lanes, int64_t long_blocks) {
+  __shared__ float sums[256][kColumns + 1];
+  const int64_t n_short = p.joins[0] * p.blocks, n_long = p.joins[1] * long_blocks;
+  for (int64_t item = blockIdx.x; item < n_short + n_long; item += gridDim.x) {
+    const bool is_long = item < n_long;               // the longest work first
+    const int lanes = is_long ? long_lanes : p.lanes, groups = 256 / lanes;
+    const int64_t blocks = is_long ? long_blocks : p.blocks, i = is_long ? item : item - n_long;
+    const int64_t piece = p.joins[is_long ? 1 + p.pieces - i / blocks : 2 + i / blocks];
+    const uint32_t run = p.keys[(piece + 1) * p.piece - 1];
+    // the pieces that begin within the run
+    int64_t parts = 1;
+    for (int more = 256; more == 256;) {
+      const int64_t at = (piece + parts + threadIdx.x) * p.piece;
+      more = __syncthreads_count(at < p.count && p.keys[at] == run);
+      parts += more;
     }
+    const int lane = threadIdx.x % lanes, mine = threadIdx.x / lanes;
+    const Columns c(M, i % blocks, lane, lanes, p.width);
+    const int64_t from = parts * mine / groups, to = parts * (mine + 1) / groups;
+    float acc[kColumns] = {0, 0, 0, 0, 0, 0, 0, 0};
+    constexpr int kAhead = 4;
+    for (int64_t k0 = from; k0 < to; k0 += kAhead) {
+      float v[kAhead][kColumns];
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a)
+        if (k0 + a < to) load_columns<EF32, M>(partial_row(p, piece + k0 + a, k0 + a == 0), c, v[a]);
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) {
+        if (k0 + a >= to) continue;
+#pragma unroll
+        for (int k = 0; k < kColumns; ++k) acc[k] += v[a][k];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kColumns; ++k) sums[threadIdx.x][k] = acc[k];
+    __syncthreads();
+    if (mine == 0) {
+      for (int g = 1; g < groups; ++g) {
+#pragma unroll
+        for (int k = 0; k < kColumns; ++k) acc[k] += sums[g * lanes + lane][k];
+      }
+      write_row<TW, M>(p, weight, run, c, acc);
+    }
+    __syncthreads();
   }
-  write_row<TW, WIDE>(p, weight, run, c, acc);
 }
 
 // ---------------------------------------------------------------------------
@@ -516,10 +607,11 @@ __global__ void __launch_bounds__(256) embedding_join(Sums p, typename TW::S *we
 // ---------------------------------------------------------------------------
 struct Plan {
   int passes, bits;                  // digits of the sort
+  bool many;                         // more than one workgroup's
   int64_t tiles;
   int lanes, piece;
   int64_t blocks, pieces;
-  size_t keys, places, keys2, places2, counts, partials, bytes;   // offsets in the workspace
+  size_t keys, places, keys2, places2, counts, joins, partials, bytes;   // offsets in the workspace
 };
 
 Plan plan_of(int64_t count, int64_t vocab, int64_t width) {
@@ -529,10 +621,11 @@ Plan plan_of(int64_t count, int64_t vocab, int64_t width) {
   p.passes = (bits + kMaxBits - 1) / kMaxBits;
   p.bits = (bits + p.passes - 1) / p.passes;
   p.tiles = (count + kTile - 1) / kTile;
+  p.many = count > kOnce * 1024;
   p.lanes = lanes_for(width);
   p.blocks = (width + static_cast<int64_t>(p.lanes) * kColumns - 1) / (p.lanes * kColumns);
-  // pieces of 8 to 64 tokens: about a thousand workgroups where there are so many
-  p.piece = static_cast<int>(std::clamp<int64_t>(count * p.blocks * p.lanes / 256 / 1024, 8, 64));
+  // pieces of 8 to 64 tokens (a lane each): about 2048 workgroups where there are so many
+  p.piece = static_cast<int>(std::clamp<int64_t>(count * p.blocks * p.lanes / 256 / 2048, 8, 64));
   p.pieces = (count + p.piece - 1) / p.piece;
   size_t at = 0;
   auto take = [&](size_t n) {
@@ -542,10 +635,11 @@ Plan plan_of(int64_t count, int64_t vocab, int64_t width) {
   };
   p.keys = take(4 * count);
   p.places = take(4 * count);
-  p.keys2 = p.tiles > 1 ? take(4 * count) : 0;
-  p.places2 = p.tiles > 1 ? take(4 * count) : 0;
-  p.counts = p.tiles > 1 ? take(4 * (p.tiles << p.bits)) : 0;
-  p.partials = take(8 * p.pieces * width);
+  p.keys2 = p.many ? take(4 * count) : 0;
+  p.places2 = p.many ? take(4 * count) : 0;
+  p.counts = p.many ? take(4 * (p.tiles << p.bits)) : 0;
+  p.joins = take(4 * (2 + p.pieces));
+  p.partials = take(8 * p.pieces * ((width + 3) / 4 * 4));
   p.bytes = at;
   return p;
 }
@@ -557,19 +651,16 @@ hipError_t launch_embedding(const void *tokens, int token_bits, int64_t count, c
   const int lanes = lanes_for(width);
   const int64_t blocks = (width + static_cast<int64_t>(lanes) * kColumns - 1) / (lanes * kColumns);
   const int64_t grid = (count * blocks + 256 / lanes - 1) / (256 / lanes);
-  const bool wide = wide_rows(weight) && wide_rows(out);
   return with_type(weight.dtype, [&](auto tw) {
     return with_type(out.dtype, [&](auto to) {
-      using TW = decltype(tw);
-      using TO = decltype(to);
-      auto run = [&](auto kernel) {
-        kernel<<<grid_of(grid), dim3(256), 0, s>>>(Tokens{tokens, token_bits}, count,
-                                               static_cast<const typename TW::S *>(weight.data), vocab, width,
-                                               weight.pitch, scale, static_cast<typename TO::S *>(out.data), out.pitch,
-                                               lanes, blocks);
+      return with_spread(spread_of(weight, out), [&](auto m) {
+        using TW = decltype(tw);
+        using TO = decltype(to);
+        embedding_rows<TW, TO, m.value><<<grid_of(grid), dim3(256), 0, s>>>(
+            Tokens{tokens, token_bits}, count, static_cast<const typename TW::S *>(weight.data), vocab, width,
+            weight.pitch, scale, static_cast<typename TO::S *>(out.data), out.pitch, lanes, blocks);
         return hipGetLastError();
-      };
-      return wide ? run(embedding_rows<TW, TO, true>) : run(embedding_rows<TW, TO, false>);
+      });
     });
   });
 }
@@ -584,42 +675,48 @@ hipError_t launch_embedding_grad(const void *tokens, int token_bits, int64_t cou
   auto words = [&](size_t at) { return reinterpret_cast<uint32_t *>(ws + at); };
   const Tokens t{tokens, token_bits};
   const uint32_t v = static_cast<uint32_t>(vocab);
-  uint32_t *keys = words(plan.keys), *places = words(plan.places);
-  if (plan.tiles == 1) {
-    token_sort_once<<<dim3(1), dim3(1024), 0, s>>>(t, static_cast<int>(count), v, plan.passes, plan.bits, keys, places);
-  } else if (plan.tiles > 1) {
+  uint32_t *keys = words(plan.keys), *places = words(plan.places), *joins = words(plan.joins);
+  if (count > 0 && !plan.many) {
+    token_sort_once<kOnce><<<dim3(1), dim3(1024), 0, s>>>(t, static_cast<int>(count), v, plan.passes, plan.bits, keys,
+                                                         places, joins);
+  } else if (count > 0) {
     uint32_t *keys2 = words(plan.keys2), *places2 = words(plan.places2), *counts = words(plan.counts);
     for (int pass = 0; pass < plan.passes; ++pass) {
       const uint32_t *from = pass ? keys2 : nullptr;
       const int shift = pass * plan.bits;
       token_count<<<dim3(plan.tiles), dim3(1024), 0, s>>>(t, from, count, v, shift, plan.bits, counts);
-      token_scan<<<dim3(1), dim3(1024), 0, s>>>(counts, plan.tiles << plan.bits);
+      if (plan.tiles > kFewTiles) token_scan<<<dim3(1), dim3(1024), 0, s>>>(counts, plan.tiles << plan.bits);
       token_scatter<<<dim3(plan.tiles), dim3(1024), 0, s>>>(t, from, places2, count, v, shift, plan.bits, counts, keys,
-                                                           places);
+                                                           places, joins);
       if (pass + 1 < plan.passes) std::swap(keys, keys2), std::swap(places, places2);
     }
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  Sums p{keys, places, count, v, width, grad.pitch, grad_weight.pitch, scale, accumulate ? 1 : 0, plan.piece,
-         plan.pieces, plan.lanes, plan.blocks, reinterpret_cast<float *>(ws + plan.partials),
-         accumulate ? 0 : (vocab + kClearRows - 1) / kClearRows};
   const int groups = 256 / plan.lanes;
   const int64_t work = (plan.pieces * plan.blocks + groups - 1) / groups;
-  const bool wide = wide_rows(grad) && wide_rows(grad_weight);
+  Sums p{keys, places, count, v, width, grad.pitch, grad_weight.pitch, scale, accumulate ? 1 : 0, plan.piece,
+         plan.pieces, plan.lanes, plan.blocks, reinterpret_cast<float *>(ws + plan.partials),
+         (width + 3) / 4 * 4,
+         work, joins};
+  const int64_t clear = accumulate ? 0 : (vocab + kClearRows - 1) / kClearRows;
+  const int join_lanes = lanes_for(width, kJoinLanes);
+  const int64_t join_blocks = (width + join_lanes * kColumns - 1) / (join_lanes * kColumns);
   return with_type(grad.dtype, [&](auto tg) {
     return with_type(grad_weight.dtype, [&](auto tw) {
-      using TG = decltype(tg);
-      using TW = decltype(tw);
-      auto run = [&](auto sums, auto join) {
-        const typename TG::S *g = static_cast<const typename TG::S *>(grad.data);
+      return with_spread(spread_of(grad, grad_weight), [&](auto m) {
+        using TG = decltype(tg);
+        using TW = decltype(tw);
         typename TW::S *w = static_cast<typename TW::S *>(grad_weight.data);
-        if (p.clear_groups + work > 0) sums<<<grid_of(p.clear_groups + work), dim3(256), 0, s>>>(p, g, w);
-        if (plan.pieces > 1) join<<<grid_of(work), dim3(256), 0, s>>>(p, w);
+        const typename TG::S *g = static_cast<const typename TG::S *>(grad.data);
+        const dim3 grid = grid_of(clear + work);
+        if (plan.lanes >= 64) embedding_sums<TG, TW, m.value, true><<<grid, dim3(256), 0, s>>>(p, g, w);
+        else embedding_sums<TG, TW, m.value, false><<<grid, dim3(256), 0, s>>>(p, g, w);
+        if (plan.pieces > 1)
+          embedding_join<TW, m.value><<<dim3(std::min<int64_t>(plan.pieces * join_blocks, kJoinGroups)), dim3(256), 0,
+                                        s>>>(p, w, join_lanes, join_blocks);
         return hipGetLastError();
-      };
-      return wide ? run(embedding_sums<TG, TW, true>, embedding_join<TW, true>)
-                  : run(embedding_sums<TG, TW, false>, embedding_join<TW, false>);
+      });
     });
   });
 }
