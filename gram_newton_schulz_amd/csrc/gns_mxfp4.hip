@@ -14,6 +14,7 @@ namespace {
 
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // ---------------------------------------------------------------------------
@@ -44,71 +45,266 @@ __device__ __forceinline__ uint32_t noisy_code(float x, float inverse, uint32_t 
   return (static_cast<uint32_t>(whole) + up) | (__float_as_uint(x) >> 31 << 3);
 }
 
-// A thread per block of 32: elements along `along`, blocks of one line, lines
-// `across` apart.  Also the blocks that only pad a line, and the scales of
-// lines that only pad the last 32.
+// Eight consecutive values of a row, as they lie in memory.
 template <class T>
-__global__ void __launch_bounds__(256)
-mx_quantize_blocks(const typename T::S *x, int64_t sb, int64_t along, int64_t across, const uint8_t *noise,
-                   int64_t noise_along, int64_t noise_across, int64_t batch, int64_t lines, int64_t length,
-                   uint8_t *codes, uint8_t *scales) {
-  const int64_t groups = (length + kMxGroup - 1) / kMxGroup, blocks = groups * 4;
-  const int64_t line_blocks = (lines + 31) / 32;
-  const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (at >= batch * line_blocks * 32 * blocks) return;
-  const int64_t blk = at % blocks, line = at / blocks % (line_blocks * 32), b = at / blocks / (line_blocks * 32);
-  uint8_t *scale_at = scales + (((b * line_blocks + line / 32) * groups + blk / 4) * 32 + line % 32) * 4 + blk % 4;
-  if (line >= lines) {
-    *scale_at = 0;
-    return;
+struct Octet {
+  static constexpr bool k16 = sizeof(typename T::S) == 2;
+  uint32_t w[k16 ? 4 : 8];
+
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (k16) return T::ld(static_cast<typename T::S>(w[i / 2] >> (16 * (i & 1))));
+    else return __uint_as_float(w[i]);
   }
-  const typename T::S *src = x + b * sb + line * across;
-  float v[32];
-  uint32_t largest = 0;
-  for (int i = 0; i < 32; ++i) {
-    const int64_t k = blk * 32 + i;
-    v[i] = k < length ? T::ld(src[k * along]) : 0.0f;
-    largest = max(largest, __float_as_uint(v[i]) & 0x7fffffffu);
-  }
-  const uint32_t s = scale_byte(largest, noise != nullptr);
-  uint32_t word[4] = {0, 0, 0, 0};
-  if (s != 255) {
-    for (int i = 0; i < 32; i += 2) {
-      uint32_t pair;
-      if (noise) {
-        const uint8_t *r = noise + b * lines * length + line * noise_across;
-        const int64_t k = blk * 32 + i;
-        const uint32_t r0 = k < length ? r[k * noise_along] : 0, r1 = k + 1 < length ? r[(k + 1) * noise_along] : 0;
-        pair = noisy_code(v[i], inverse_scale(s), r0) | noisy_code(v[i + 1], inverse_scale(s), r1) << 4;
-      } else {
-        pair = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, v[i], v[i + 1], scale_of(s), 0) & 0xff;
-      }
-      word[i / 8] |= pair << (4 * (i % 8));
+  // bits of the largest magnitude, as a float's
+  __device__ __forceinline__ uint32_t largest() const {
+    if constexpr (k16) {
+      u16x2 m{0, 0};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, w[i] & 0x7fff7fffu));
+      return __float_as_uint(T::ld(max(m[0], m[1])));
+    } else {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7fffffffu);
+      return m;
     }
   }
-  *reinterpret_cast<uint4 *>(codes + ((b * lines + line) * groups * 64) + blk * 16) =
-      make_uint4(word[0], word[1], word[2], word[3]);
-  *scale_at = static_cast<uint8_t>(s);
+};
+
+// Two codes into byte SEL of old: the conversion divides by the scale, rounds
+// to nearest with ties to even and cuts off at 6.
+template <class T, int SEL>
+__device__ __forceinline__ uint32_t two_codes(uint32_t old, uint32_t low, uint32_t high, float scale) {
+  if constexpr (T::code == DT_F32) {
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(old, __uint_as_float(low), __uint_as_float(high), scale, SEL);
+  } else {
+    const uint32_t pair = __builtin_amdgcn_perm(high, low, 0x05040100u);   // their low halves
+    if constexpr (T::code == DT_BF16)
+      return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(old, __builtin_bit_cast(bf16x2_t, pair), scale, SEL);
+    else
+      return __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(old, __builtin_bit_cast(f16x2_t, pair), scale, SEL);
+  }
 }
 
-template <class T>
-__global__ void __launch_bounds__(256) mx_dequantize_values(MxMatrix q, typename T::S *out) {
-  const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  const int64_t groups = q.groups();
-  if (at >= q.batch * q.rows * groups * 4) return;
-  const int64_t blk = at % (groups * 4), row = at / (groups * 4) % q.rows, b = at / (groups * 4) / q.rows;
-  const uint4 w = *reinterpret_cast<const uint4 *>(q.codes + (b * q.rows + row) * q.pitch() + blk * 16);
-  const uint32_t s = q.scales[(((b * q.row_blocks() + row / 32) * groups + blk / 4) * 32 + row % 32) * 4 + blk % 4];
-  const uint32_t word[4] = {w.x, w.y, w.z, w.w};
-  typename T::S *dst = out + (b * q.rows + row) * q.cols;
-  for (int i = 0; i < 32; ++i) {
-    const int64_t k = blk * 32 + i;
-    if (k >= q.cols) break;
-    const uint32_t c = word[i / 8] >> (4 * (i % 8)) & 15;
-    const uint32_t m = c & 7;
-    const float t = m < 4 ? 0.5f * m : m < 6 ? static_cast<float>(m) - 2.0f : 2.0f * m - 8.0f;
-    const float val = s == 255 ? __uint_as_float(0x7fc00000u) : (c & 8 ? -t : t) * scale_of(s);
-    dst[k] = T::st(val);
+// Eight codes of values given by their bits (16-bit ones in the low half).
+template <class T, bool NOISE>
+__device__ __forceinline__ uint32_t eight_codes(const uint32_t *bits, const uint32_t *noise, uint32_t s) {
+  uint32_t word = 0;
+  if constexpr (NOISE) {
+    const float inverse = inverse_scale(s);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float v;
+      if constexpr (T::code == DT_F32) v = __uint_as_float(bits[i]);
+      else v = T::ld(static_cast<typename T::S>(bits[i]));
+      word |= noisy_code(v, inverse, noise[i]) << (4 * i);
+    }
+  } else {
+    const float scale = scale_of(s);
+    word = two_codes<T, 0>(word, bits[0], bits[1], scale);
+    word = two_codes<T, 1>(word, bits[2], bits[3], scale);
+    word = two_codes<T, 2>(word, bits[4], bits[5], scale);
+    word = two_codes<T, 3>(word, bits[6], bits[7], scale);
+  }
+  return s == 255 ? 0 : word;
+}
+
+struct MxQuantize {
+  const void *x;
+  int64_t pitch, batch_stride;
+  const uint8_t *noise;
+  int64_t rows, cols;
+  MxMatrix by_rows, by_columns;
+  int tiles_r, tiles_c;
+};
+
+// A workgroup per 128 x 128 tile, the extent of one word of scales either way.
+// Along the rows 16 threads share a row, eight values each, and four of them a
+// block.  Along the columns the tile lies in LDS, and a thread takes 32 rows
+// of one column (of two neighbouring ones of a 16-bit type); the four threads
+// of a column are neighbours, so that they write its 64 bytes of codes
+// together.  A row of LDS has its 16-byte pieces exchanged by its block of 32
+// rows, which puts those four threads on different banks.
+template <class T, bool ROWS, bool COLS, bool NOISE, bool WIDE>
+__global__ void __launch_bounds__(256) mx_quantize(MxQuantize p) {
+  using S = typename T::S;
+  constexpr bool k16 = sizeof(S) == 2;
+  constexpr int kRowWords = k16 ? 64 : 128;                  // of LDS
+  __shared__ __attribute__((aligned(16))) uint32_t tile[COLS ? 128 * kRowWords : 4];
+  __shared__ __attribute__((aligned(16))) uint32_t noises[COLS && NOISE ? 128 * 32 : 4];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int64_t per_matrix = static_cast<int64_t>(p.tiles_r) * p.tiles_c;
+  const int64_t mat = blockIdx.x / per_matrix;
+  const int in = static_cast<int>(blockIdx.x - mat * per_matrix);
+  const int64_t row0 = static_cast<int64_t>(in / p.tiles_c) * 128, col0 = static_cast<int64_t>(in % p.tiles_c) * 128;
+  const S *x = static_cast<const S *>(p.x) + mat * p.batch_stride;
+  const uint8_t *noise = NOISE ? p.noise + mat * p.rows * p.cols : nullptr;
+  const int r_in = tid >> 4, c_in = (tid & 15) * 8;
+  const int64_t col = col0 + c_in;
+  const int left = static_cast<int>(min<int64_t>(8, p.cols - col));       // of the eight
+  const int64_t groups = p.by_rows.groups(), row_blocks = p.by_rows.row_blocks();
+
+  constexpr int kAhead = 4;
+  const int64_t last = COLS ? row0 + 128 : min<int64_t>(row0 + 128, (p.rows + 31) / 32 * 32);
+  for (int k0 = 0; k0 < 128 && row0 + k0 < last; k0 += 16 * kAhead) {
+    Octet<T> v[kAhead];
+    uint32_t r[kAhead][2];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      const int64_t row = row0 + k0 + 16 * a + r_in;
+#pragma unroll
+      for (int i = 0; i < (k16 ? 4 : 8); ++i) v[a].w[i] = 0;
+      r[a][0] = r[a][1] = 0;
+      if (row >= p.rows || left <= 0) continue;
+      const S *src = x + row * p.pitch + col;
+      if (WIDE && left == 8) {
+#pragma unroll
+        for (int i = 0; i < (k16 ? 1 : 2); ++i)
+          *reinterpret_cast<uint4 *>(v[a].w + 4 * i) = reinterpret_cast<const uint4 *>(src)[i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (i >= left) break;
+          if constexpr (k16) v[a].w[i / 2] |= static_cast<uint32_t>(src[i]) << (16 * (i & 1));
+          else v[a].w[i] = __float_as_uint(src[i]);
+        }
+      }
+      if constexpr (NOISE) {
+        const uint8_t *from = noise + row * p.cols + col;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i < left) r[a][i / 4] |= static_cast<uint32_t>(from[i]) << (8 * (i & 3));
+      }
+    }
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      const int in_tile = k0 + 16 * a + r_in;
+      const int64_t row = row0 + in_tile;
+      if constexpr (COLS) {
+        // (piece of 16 bytes ^ 4 x block of 32 rows)
+        uint4 *to = reinterpret_cast<uint4 *>(tile + in_tile * kRowWords);
+        const int turn = (in_tile >> 5) << 2;
+#pragma unroll
+        for (int i = 0; i < (k16 ? 1 : 2); ++i)
+          to[((tid & 15) * (k16 ? 1 : 2) + i) ^ turn] = *reinterpret_cast<const uint4 *>(v[a].w + 4 * i);
+        if constexpr (NOISE)
+          *reinterpret_cast<uint2 *>(noises + in_tile * 32 + ((2 * (tid & 15)) ^ (turn << 1))) = make_uint2(r[a][0], r[a][1]);
+      }
+      if constexpr (ROWS) {
+        uint32_t largest = v[a].largest();
+        largest = max(largest, __shfl_xor(largest, 1));
+        largest = max(largest, __shfl_xor(largest, 2));
+        const uint32_t s = scale_byte(largest, NOISE);
+        uint32_t bits[8], bytes[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          bits[i] = k16 ? v[a].w[i / 2] >> (16 * (i & 1)) & 0xffff : v[a].w[k16 ? 0 : i];
+          bytes[i] = NOISE ? r[a][i / 4] >> (8 * (i & 3)) & 0xff : 0;
+        }
+        const uint32_t word = eight_codes<T, NOISE>(bits, bytes, s);
+        uint32_t scales = s << (8 * ((lane >> 2) & 3));
+        scales |= __shfl_xor(scales, 4);
+        scales |= __shfl_xor(scales, 8);
+        if (row < p.rows) {
+          *reinterpret_cast<uint32_t *>(p.by_rows.codes + (mat * p.rows + row) * (groups * 64) + (col0 + c_in) / 2) = word;
+        } else {
+          scales = 0;
+        }
+        if ((tid & 15) == 0 && row < row_blocks * 32)
+          *reinterpret_cast<uint32_t *>(p.by_rows.scales + (((mat * row_blocks + row / 32) * groups + col0 / 128) * 32 +
+                                                            row % 32) * 4) = scales;
+      }
+    }
+  }
+  if constexpr (COLS) {
+    __syncthreads();
+    const int64_t t_groups = p.by_columns.groups(), t_blocks = p.by_columns.row_blocks();
+    const int rb = lane & 3, turn = rb << 4;
+    constexpr int kSub = k16 ? 2 : 1;                        // columns of a thread at a time
+#pragma unroll 1
+    for (int it = 0; it < (k16 ? 1 : 2); ++it) {
+      const int c = (lane >> 2) + 16 * (tid >> 6) + 64 * it; // column, or pair of columns
+      uint32_t raw[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) raw[i] = tile[(32 * rb + i) * kRowWords + (c ^ turn)];
+#pragma unroll
+      for (int h = 0; h < kSub; ++h) {
+        const int64_t column = col0 + c * kSub + h;
+        uint32_t bits[32], bytes[32], largest = 0;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          bits[i] = k16 ? raw[i] >> (16 * h) & 0xffff : raw[i];
+          largest = max(largest, bits[i] & (k16 ? 0x7fffu : 0x7fffffffu));
+          const int b = c * kSub + h;                        // its byte of noise
+          bytes[i] = NOISE ? noises[(32 * rb + i) * 32 + ((b >> 2) ^ (rb << 3))] >> (8 * (b & 3)) & 0xff : 0;
+        }
+        if constexpr (k16) largest = __float_as_uint(T::ld(static_cast<S>(largest)));
+        const uint32_t s = scale_byte(largest, NOISE);
+        uint4 word;
+        word.x = eight_codes<T, NOISE>(bits, bytes, s);
+        word.y = eight_codes<T, NOISE>(bits + 8, bytes + 8, s);
+        word.z = eight_codes<T, NOISE>(bits + 16, bytes + 16, s);
+        word.w = eight_codes<T, NOISE>(bits + 24, bytes + 24, s);
+        uint32_t scales = s << (8 * rb);
+        scales |= __shfl_xor(scales, 1);
+        scales |= __shfl_xor(scales, 2);
+        if (column < p.cols) {
+          *reinterpret_cast<uint4 *>(p.by_columns.codes + (mat * p.cols + column) * (t_groups * 64) + row0 / 2 + rb * 16) =
+              word;
+        } else {
+          scales = 0;
+        }
+        if (rb == 0 && column < t_blocks * 32)
+          *reinterpret_cast<uint32_t *>(p.by_columns.scales + (((mat * t_blocks + column / 32) * t_groups + row0 / 128) * 32 +
+                                                               column % 32) * 4) = scales;
+      }
+    }
+  }
+}
+
+// The values of a 128 x 128 tile, eight per thread.
+template <class T, bool WIDE>
+__global__ void __launch_bounds__(256) mx_dequantize(MxMatrix q, typename T::S *out, int tiles_r, int tiles_c) {
+  using S = typename T::S;
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  const int tid = threadIdx.x;
+  const int64_t per_matrix = static_cast<int64_t>(tiles_r) * tiles_c, mat = blockIdx.x / per_matrix;
+  const int in = static_cast<int>(blockIdx.x - mat * per_matrix);
+  const int64_t row0 = static_cast<int64_t>(in / tiles_c) * 128, group = in % tiles_c, groups = q.groups();
+  const int64_t col = group * 128 + (tid & 15) * 8;
+  if (col >= q.cols) return;
+#pragma unroll
+  for (int k = 0; k < 128; k += 16) {
+    const int64_t row = row0 + k + (tid >> 4);
+    if (row >= q.rows) return;
+    const uint32_t w = *reinterpret_cast<const uint32_t *>(q.codes + (mat * q.rows + row) * q.pitch() + col / 2);
+    const uint32_t s =
+        q.scales[(((mat * q.row_blocks() + row / 32) * groups + group) * 32 + row % 32) * 4 + ((tid >> 2) & 3)];
+    const float scale = s == 255 ? __uint_as_float(0x7fc00000u) : scale_of(s);
+    float v[8];
+    const auto two = [&](int i, f32x2 x) {
+      // (a scale of NaN by itself: the conversion takes its exponent only)
+      v[i] = s == 255 ? scale : x[0];
+      v[i + 1] = s == 255 ? scale : x[1];
+    };
+    two(0, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, 0));
+    two(2, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, 1));
+    two(4, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, 2));
+    two(6, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, 3));
+    S *to = out + (mat * q.rows + row) * q.cols + col;
+    if (WIDE && col + 8 <= q.cols) {
+      if constexpr (sizeof(S) == 4) {
+        reinterpret_cast<float4 *>(to)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4 *>(to)[1] = make_float4(v[4], v[5], v[6], v[7]);
+      } else {
+        *reinterpret_cast<uint4 *>(to) =
+            make_uint4(T::st2(v[0], v[1]), T::st2(v[2], v[3]), T::st2(v[4], v[5]), T::st2(v[6], v[7]));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (col + i < q.cols) to[i] = T::st(v[i]);
+    }
   }
 }
 
@@ -120,6 +316,11 @@ hipError_t with_type(int dtype, F &&f) {
   if (dtype == DT_F32) return f(EF32{});
   if (dtype == DT_BF16) return f(EBF16{});
   return f(EF16{});
+}
+
+template <class F>
+hipError_t with_flag(bool on, F &&f) {
+  return on ? f(std::true_type{}) : f(std::false_type{});
 }
 
 __device__ __forceinline__ i32x8 fp4_operand(uint4 v) {
@@ -418,26 +619,40 @@ __global__ void __launch_bounds__((MxTile<TILE>::THREADS)) mx_gemm(MxGemm p) {
 
 hipError_t launch_mx_quantize(const MxInput &in, int64_t batch, int64_t rows, int64_t cols, const MxMatrix &by_rows,
                               const MxMatrix &by_columns, hipStream_t s) {
+  MxQuantize p{in.x, in.pitch, in.batch_stride, in.noise, rows, cols, by_rows, by_columns,
+               static_cast<int>((rows + 127) / 128), static_cast<int>((cols + 127) / 128)};
+  const int64_t tiles = batch * p.tiles_r * p.tiles_c;
+  const int64_t elem = dtype_size(in.dtype);
+  const bool wide = reinterpret_cast<uintptr_t>(in.x) % 16 == 0 && in.pitch * elem % 16 == 0 &&
+                    in.batch_stride * elem % 16 == 0;
   return with_type(in.dtype, [&](auto t) {
     using T = decltype(t);
-    const typename T::S *x = static_cast<const typename T::S *>(in.x);
-    auto run = [&](const MxMatrix &q, int64_t along, int64_t across, int64_t na, int64_t nc) {
-      const int64_t n = batch * q.row_blocks() * 32 * q.groups() * 4;
-      mx_quantize_blocks<T><<<dim3((n + 255) / 256), dim3(256), 0, s>>>(x, in.batch_stride, along, across, in.noise, na,
-                                                                       nc, batch, q.rows, q.cols, q.codes, q.scales);
-    };
-    if (by_rows.codes) run(by_rows, 1, in.pitch, 1, cols);
-    if (by_columns.codes) run(by_columns, in.pitch, 1, cols, 1);
-    return hipGetLastError();
+    return with_flag(in.noise != nullptr, [&](auto noise) {
+      return with_flag(wide, [&](auto w) {
+        auto run = [&](auto kernel) {
+          kernel<<<dim3(tiles), dim3(256), 0, s>>>(p);
+          return hipGetLastError();
+        };
+        constexpr bool N = decltype(noise)::value, W = decltype(w)::value;
+        if (!by_columns.codes) return run(mx_quantize<T, true, false, N, W>);
+        if (!by_rows.codes) return run(mx_quantize<T, false, true, N, W>);
+        return run(mx_quantize<T, true, true, N, W>);
+      });
+    });
   });
 }
 
 hipError_t launch_mx_dequantize(const MxMatrix &q, void *out, int dtype, hipStream_t s) {
+  const int tiles_r = static_cast<int>((q.rows + 127) / 128), tiles_c = static_cast<int>((q.cols + 127) / 128);
+  const int64_t tiles = q.batch * tiles_r * tiles_c;
+  const bool wide = reinterpret_cast<uintptr_t>(out) % 16 == 0 && q.cols * dtype_size(dtype) % 16 == 0;
   return with_type(dtype, [&](auto t) {
-    using T = decltype(t);
-    const int64_t n = q.batch * q.rows * q.groups() * 4;
-    mx_dequantize_values<T><<<dim3((n + 255) / 256), dim3(256), 0, s>>>(q, static_cast<typename T::S *>(out));
-    return hipGetLastError();
+    return with_flag(wide, [&](auto w) {
+      using T = decltype(t);
+      mx_dequantize<T, decltype(w)::value>
+          <<<dim3(tiles), dim3(256), 0, s>>>(q, static_cast<typename T::S *>(out), tiles_r, tiles_c);
+      return hipGetLastError();
+    });
   });
 }
 
