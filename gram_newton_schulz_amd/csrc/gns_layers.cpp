@@ -315,6 +315,7 @@ gns_status gns_mxfp4_matmul(const gns_mxfp4 *a, const gns_mxfp4 *b, void *out, g
 
 size_t gns_mxfp4_linear_workspace_bytes(int64_t batch, int64_t m, int64_t n, int64_t k) {
   if (!mx_size(batch, m, k) || !mx_size(batch, n, k) || !grid_fits(batch, m, n)) return 0;
+  if (gns::mx_linear_quantizes(m, k)) return 0;
   return round_256(gns_mxfp4_code_bytes(batch, m, k)) + round_256(gns_mxfp4_scale_bytes(batch, m, k)) +
          gns_mxfp4_matmul_workspace_bytes(batch, m, n, k);
 }
@@ -347,15 +348,24 @@ gns_status gns_mxfp4_linear(const void *x, gns_dtype dtype, int64_t pitch, int64
   for (const Region &r : {rows_at(x, batch, m, k, pitch, batch_stride, elem), bytes_at(mw.codes, mw.code_bytes()),
                           bytes_at(mw.scales, mw.scale_bytes())})
     if (meet(written, r) || meet(scratch, r)) return GNS_E_ALIAS;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const gns::MxInput in{x, dtype, pitch, batch_stride, nullptr};
+  if (gns::mx_linear_quantizes(m, k)) {
+    const double each = static_cast<double>(batch) * m;
+    LaunchScope ls(s, "mxfp4_matmul", "mx_thin", 2.0 * each * n * k,
+                   each * k * elem + mx_bytes(mw) + each * n * gns::dtype_size(out_dtype) * (accumulate ? 2 : 1));
+    const hipError_t e = gns::launch_mx_linear(in, m, mw, o, s);
+    ls.done();
+    return e == hipSuccess ? GNS_OK : GNS_E_HIP;
+  }
   uint8_t *at = static_cast<uint8_t *>(workspace);
   MxMatrix q{at, nullptr, batch, m, k};
   q.scales = at + round_256(q.code_bytes());
-  hipStream_t s = static_cast<hipStream_t>(stream);
   if (k > 0) {
     const double each = static_cast<double>(batch) * m * k;
     LaunchScope ls(s, "mxfp4_quantize", "mx_quantize", 4.0 * each, each * elem + mx_bytes(q));
     const hipError_t e =
-        gns::launch_mx_quantize(gns::MxInput{x, dtype, pitch, batch_stride, nullptr}, batch, m, k, q, MxMatrix{}, s);
+        gns::launch_mx_quantize(in, batch, m, k, q, MxMatrix{}, s);
     ls.done();
     if (e != hipSuccess) return GNS_E_HIP;
   }

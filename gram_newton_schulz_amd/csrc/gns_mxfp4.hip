@@ -15,6 +15,7 @@ namespace {
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // ---------------------------------------------------------------------------
@@ -615,6 +616,146 @@ __global__ void __launch_bounds__((MxTile<TILE>::THREADS)) mx_gemm(MxGemm p) {
   }
 }
 
+// Few rows of A, as when single tokens are answered: what counts is reading B
+// once.  A workgroup takes 16 rows of B (16 x 16 x 128 MFMA, B's fragments as
+// the instruction's rows) and its W waves share the contraction, their sums
+// joined in LDS in order; a wave has eight steps of 128 columns in flight, 8
+// KiB of codes.  MB: blocks of 16 rows of A.
+// With QUANTIZE the workgroup quantises A itself, as mx_quantize would, which
+// saves a launch, while the first loads of B are on their way.
+constexpr int kThinRows = 32;               // of A
+constexpr int kThinValues = 64 * 1024;      // of A that a workgroup quantises (up to 16 rows)
+
+struct MxThin {
+  MxMatrix a, b;                            // a: without codes where x is quantised here
+  MxOutput o;
+  const void *x;
+  int64_t x_pitch, x_batch_stride;
+  int wide;                                 // rows of x begin on 16 bytes
+};
+
+template <class TX, class TO, int MB, int W, bool QUANTIZE>
+__global__ void __launch_bounds__(64 * W) mx_thin(MxThin p) {
+  constexpr int kSteps = 8;
+  __shared__ __attribute__((aligned(16))) f32x4 sums[W][MB][64];
+  __shared__ __attribute__((aligned(16))) uint8_t codes[QUANTIZE ? kThinValues / 2 + 16 * 16 : 16];
+  __shared__ __attribute__((aligned(16))) uint32_t scales[QUANTIZE ? kThinValues / kMxGroup : 1];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t blocks = (p.b.rows + 15) / 16, mat = blockIdx.x / blocks;
+  const int64_t row0 = (blockIdx.x - mat * blocks) * 16;
+  const int groups = static_cast<int>(p.b.groups()), m = static_cast<int>(p.a.rows);
+  const int lr = lane & 15, chunk = lane >> 4;
+  const int64_t n = row0 + lr;
+  const bool real = n < p.b.rows;
+  const uint8_t *bc = p.b.codes + (mat * p.b.rows + (real ? n : row0)) * (groups * 64) + chunk * 16;
+  const uint8_t *bs = p.b.scales + ((mat * p.b.row_blocks() + n / 32) * groups * 32 + n % 32) * 4;
+  const int per = (groups + W - 1) / W, begin = wave * per, end = min(begin + per, groups);
+
+  uint4 fb[kSteps];
+  uint32_t xb[kSteps];
+  auto load = [&](int at) {
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      fb[i] = make_uint4(0, 0, 0, 0);
+      xb[i] = 0;
+      if (at + i < end && real) {
+        fb[i] = *reinterpret_cast<const uint4 *>(bc + static_cast<int64_t>(at + i) * 64);
+        xb[i] = *reinterpret_cast<const uint32_t *>(bs + static_cast<int64_t>(at + i) * 128);
+      }
+    }
+  };
+  load(begin);
+
+  const int lds_pitch = groups * 64 + 16;     // (rows on different banks)
+  if constexpr (QUANTIZE) {
+    using S = typename TX::S;
+    constexpr bool k16 = sizeof(S) == 2;
+    const S *x = static_cast<const S *>(p.x) + mat * p.x_batch_stride;
+    for (int u = tid; u < m * groups * 16; u += 64 * W) {
+      const int row = u / (groups * 16), at = u - row * groups * 16;
+      const int64_t col = static_cast<int64_t>(at) * 8;
+      const S *src = x + row * p.x_pitch + col;
+      Octet<TX> v;
+#pragma unroll
+      for (int i = 0; i < (k16 ? 4 : 8); ++i) v.w[i] = 0;
+      if (p.wide && col + 8 <= p.b.cols) {
+#pragma unroll
+        for (int i = 0; i < (k16 ? 1 : 2); ++i)
+          *reinterpret_cast<uint4 *>(v.w + 4 * i) = reinterpret_cast<const uint4 *>(src)[i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (col + i >= p.b.cols) break;
+          if constexpr (k16) v.w[i / 2] |= static_cast<uint32_t>(src[i]) << (16 * (i & 1));
+          else v.w[i] = __float_as_uint(src[i]);
+        }
+      }
+      uint32_t largest = v.largest();
+      largest = max(largest, __shfl_xor(largest, 1));
+      largest = max(largest, __shfl_xor(largest, 2));
+      const uint32_t s = scale_byte(largest, false);
+      uint32_t bits[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) bits[i] = k16 ? v.w[i / 2] >> (16 * (i & 1)) & 0xffff : v.w[k16 ? 0 : i];
+      *reinterpret_cast<uint32_t *>(codes + row * lds_pitch + at * 4) = eight_codes<TX, false>(bits, nullptr, s);
+      if ((at & 3) == 0) reinterpret_cast<uint8_t *>(scales)[row * groups * 4 + at / 4] = static_cast<uint8_t>(s);
+    }
+    __syncthreads();
+  }
+
+  f32x4 acc[MB];
+#pragma unroll
+  for (int j = 0; j < MB; ++j) acc[j] = f32x4{0, 0, 0, 0};
+  for (int at = begin; at < end; at += kSteps) {
+    if (at > begin) load(at);
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      if (at + i >= end) break;
+#pragma unroll
+      for (int j = 0; j < MB; ++j) {
+        const int row = 16 * j + lr;
+        uint4 fa = make_uint4(0, 0, 0, 0);
+        uint32_t xa = 0;
+        if (row < m) {
+          if constexpr (QUANTIZE) {
+            fa = *reinterpret_cast<const uint4 *>(codes + row * lds_pitch + (at + i) * 64 + chunk * 16);
+            xa = scales[row * groups + at + i];
+          } else {
+            fa = *reinterpret_cast<const uint4 *>(p.a.codes + (mat * m + row) * (static_cast<int64_t>(groups) * 64) +
+                                                  static_cast<int64_t>(at + i) * 64 + chunk * 16);
+            xa = *reinterpret_cast<const uint32_t *>(
+                p.a.scales + (((mat * p.a.row_blocks() + row / 32) * groups + at + i) * 32 + row % 32) * 4);
+          }
+        }
+        acc[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fp4_operand(fb[i]), fp4_operand(fa), acc[j], 4, 4, 0,
+                                                                 xb[i] >> (8 * chunk), 0, xa >> (8 * chunk));
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < MB; ++j) sums[wave][j][lane] = acc[j];
+  __syncthreads();
+  // thread: row lane % 16 of A's block, four rows of B from 4 (lane / 16)
+  for (int k = tid; k < MB * 256; k += 64 * W) {
+    const int row = k / 16, col = k % 16, j = row / 16, from = (col / 4) * 16 + row % 16;
+    if (row >= m || row0 + col >= p.b.rows) continue;
+    float sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) sum += reinterpret_cast<const float *>(&sums[w][j][from])[col % 4];
+    typename TO::S *to = static_cast<typename TO::S *>(p.o.out) + mat * p.o.batch_stride + row * p.o.pitch + row0 + col;
+    *to = TO::st(p.o.accumulate ? TO::ld(*to) + sum : sum);
+  }
+}
+
+template <class TX, class TO, int MB, bool QUANTIZE>
+hipError_t run_thin(const MxThin &p, hipStream_t s) {
+  // about 4096 waves, at most 16 to a workgroup
+  const int64_t grid = p.b.batch * ((p.b.rows + 15) / 16);
+  if (grid <= 512 && p.b.groups() >= 16) mx_thin<TX, TO, MB, 16, QUANTIZE><<<dim3(grid), dim3(1024), 0, s>>>(p);
+  else mx_thin<TX, TO, MB, 4, QUANTIZE><<<dim3(grid), dim3(256), 0, s>>>(p);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_mx_quantize(const MxInput &in, int64_t batch, int64_t rows, int64_t cols, const MxMatrix &by_rows,
@@ -658,7 +799,25 @@ hipError_t launch_mx_dequantize(const MxMatrix &q, void *out, int dtype, hipStre
 
 size_t mx_matmul_bytes(int64_t, int64_t, int64_t, int64_t) { return 0; }
 
+bool mx_linear_quantizes(int64_t m, int64_t k) { return m <= 16 && m * ((k + kMxGroup - 1) / kMxGroup) * kMxGroup <= kThinValues; }
+
+hipError_t launch_mx_linear(const MxInput &in, int64_t m, const MxMatrix &w, const MxOutput &out, hipStream_t s) {
+  const int64_t elem = dtype_size(in.dtype);
+  const MxThin p{MxMatrix{nullptr, nullptr, w.batch, m, w.cols}, w, out, in.x, in.pitch, in.batch_stride,
+                 reinterpret_cast<uintptr_t>(in.x) % 16 == 0 && in.pitch * elem % 16 == 0 &&
+                     in.batch_stride * elem % 16 == 0};
+  return with_type(in.dtype, [&](auto tx) {
+    return with_type(out.dtype, [&](auto to) { return run_thin<decltype(tx), decltype(to), 1, true>(p, s); });
+  });
+}
+
 hipError_t launch_mx_matmul(const MxMatrix &a, const MxMatrix &b, const MxOutput &out, void *, hipStream_t s) {
+  if (a.rows <= kThinRows)
+    return with_type(out.dtype, [&](auto t) {
+      using T = decltype(t);
+      const MxThin p{a, b, out, nullptr, 0, 0, 0};
+      return a.rows <= 16 ? run_thin<EF32, T, 1, false>(p, s) : run_thin<EF32, T, 2, false>(p, s);
+    });
   return with_type(out.dtype, [&](auto t) {
     using T = decltype(t);
     auto run = [&](auto tile) {
