@@ -69,22 +69,24 @@ struct Tokens {
 // ---------------------------------------------------------------------------
 // Threads work in groups of `lanes` (a power of two up to 256) on one row, and
 // a thread has eight columns of a block of 8 lanes:
-//   OCTETS   eight consecutive ones: both arrays have 16 bits and rows that
-//            begin on 16 bytes
+//   OCTETS   eight consecutive ones: both arrays have 16 bits
 //   QUADS    twice four consecutive ones, so that neighbours' 16-byte accesses
-//            of an fp32 array meet: rows on 16 bytes, or 8 of a 16-bit array
-//   SINGLES  every lanes-th one: any other rows
-enum Spread { SINGLES, QUADS, OCTETS };
+//            of an fp32 array meet
+// Accesses of 16 bytes need no alignment beyond the element's; rows of odd
+// widths take them too (20000 x 1531 bf16 gradients: 73 us, against 106 with an
+// element per access).
+enum Spread { QUADS, OCTETS };
 constexpr int kColumns = 8;
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 
 struct Columns {
   int first, lanes, width;
   __device__ __forceinline__ Columns(Spread m, int64_t block, int lane, int lanes_, int64_t width_)
-      : first(static_cast<int>(block) * lanes_ * kColumns + lane * (m == OCTETS ? 8 : m == QUADS ? 4 : 1)),
-        lanes(lanes_), width(static_cast<int>(width_)) {}
+      : first(static_cast<int>(block) * lanes_ * kColumns + lane * (m == OCTETS ? 8 : 4)), lanes(lanes_),
+        width(static_cast<int>(width_)) {}
   template <Spread M>
   __device__ __forceinline__ int at(int k) const {
-    return M == OCTETS ? first + k : M == QUADS ? first + k / 4 * 4 * lanes + k % 4 : first + k * lanes;
+    return M == OCTETS ? first + k : first + k / 4 * 4 * lanes + k % 4;
   }
 };
 
@@ -92,21 +94,19 @@ struct Columns {
 template <class T, Spread M>
 __device__ __forceinline__ void load_columns(const typename T::S *row, const Columns &c, float *v) {
   using S = typename T::S;
-  constexpr int N = M == OCTETS ? 8 : M == QUADS ? 4 : 1;      // of one access
+  constexpr int N = M == OCTETS ? 8 : 4;                       // of one access
 #pragma unroll
   for (int k = 0; k < kColumns; k += N) {
     const int at = c.at<M>(k);
-    if (N > 1 && at + N <= c.width) {
+    if (at + N <= c.width) {
       if constexpr (sizeof(S) == 4) {
 #pragma unroll
         for (int q = 0; q < N; q += 4) {
-          const float4 a = *reinterpret_cast<const float4 *>(row + at + q);
-          v[k + q] = a.x, v[k + q + 1] = a.y, v[k + q + 2] = a.z, v[k + q + 3] = a.w;
+          __builtin_memcpy(v + k + q, row + at + q, 16);
         }
       } else {
         uint32_t a[4];
-        if constexpr (M == OCTETS) *reinterpret_cast<uint4 *>(a) = *reinterpret_cast<const uint4 *>(row + at);
-        else *reinterpret_cast<uint2 *>(a) = *reinterpret_cast<const uint2 *>(row + at);
+        __builtin_memcpy(a, row + at, 2 * N);
 #pragma unroll
         for (int q = 0; q < N; q += 2) {
           v[k + q] = T::ld(static_cast<S>(a[q / 2] & 0xffff));
@@ -125,24 +125,23 @@ __device__ __forceinline__ void load_columns(const typename T::S *row, const Col
 template <class T, Spread M, bool ONCE = false>
 __device__ __forceinline__ void store_columns(typename T::S *row, const Columns &c, const float *v) {
   using S = typename T::S;
-  constexpr int N = M == OCTETS ? 8 : M == QUADS ? 4 : 1;
+  constexpr int N = M == OCTETS ? 8 : 4;
 #pragma unroll
   for (int k = 0; k < kColumns; k += N) {
     const int at = c.at<M>(k);
-    if (N > 1 && at + N <= c.width) {
+    if (at + N <= c.width) {
       if constexpr (sizeof(S) == 4) {
 #pragma unroll
         for (int q = 0; q < N; q += 4) {
-          const float4 a = make_float4(v[k + q], v[k + q + 1], v[k + q + 2], v[k + q + 3]);
-          if constexpr (ONCE) st_once(reinterpret_cast<float4 *>(row + at + q), a);
-          else *reinterpret_cast<float4 *>(row + at + q) = a;
+          const f32x4_any a{v[k + q], v[k + q + 1], v[k + q + 2], v[k + q + 3]};
+          if constexpr (ONCE) __builtin_nontemporal_store(a, reinterpret_cast<f32x4_any *>(row + at + q));
+          else *reinterpret_cast<f32x4_any *>(row + at + q) = a;
         }
       } else {
         uint32_t a[4];
 #pragma unroll
         for (int q = 0; q < N; q += 2) a[q / 2] = T::st2(v[k + q], v[k + q + 1]);
-        if constexpr (M == OCTETS) *reinterpret_cast<uint4 *>(row + at) = *reinterpret_cast<uint4 *>(a);
-        else *reinterpret_cast<uint2 *>(row + at) = *reinterpret_cast<uint2 *>(a);
+        __builtin_memcpy(row + at, a, 2 * N);
       }
     } else {
 #pragma unroll
@@ -159,20 +158,20 @@ int lanes_for(int64_t width, int most = 256) {
   return lanes;
 }
 
+int64_t blocks_of(int64_t width, int lanes) {
+  const int64_t each = static_cast<int64_t>(lanes) * kColumns;
+  return (width + each - 1) / each;
+}
+
 Spread spread_of(const TokenRows &a, const TokenRows &b) {
-  auto on = [](const TokenRows &r, int bytes) {
-    return reinterpret_cast<uintptr_t>(r.data) % bytes == 0 && r.pitch * dtype_size(r.dtype) % bytes == 0;
-  };
-  if (a.dtype != DT_F32 && b.dtype != DT_F32 && on(a, 16) && on(b, 16)) return OCTETS;
-  return on(a, 4 * dtype_size(a.dtype)) && on(b, 4 * dtype_size(b.dtype)) ? QUADS : SINGLES;
+  return a.dtype != DT_F32 && b.dtype != DT_F32 ? OCTETS : QUADS;
 }
 
 // f(the spread as a constant)
 template <class F>
 hipError_t with_spread(Spread m, F &&f) {
   if (m == OCTETS) return f(std::integral_constant<Spread, OCTETS>{});
-  if (m == QUADS) return f(std::integral_constant<Spread, QUADS>{});
-  return f(std::integral_constant<Spread, SINGLES>{});
+  return f(std::integral_constant<Spread, QUADS>{});
 }
 
 // ---------------------------------------------------------------------------
@@ -271,12 +270,22 @@ __device__ __forceinline__ uint32_t scan_1024(uint32_t v, uint32_t *parts, uint3
   return base + run - v;
 }
 
+__device__ __forceinline__ int64_t first_not_below(const uint32_t *keys, int64_t n, uint32_t v) {
+  int64_t low = 0, high = n;
+  while (low < high) {
+    const int64_t mid = (low + high) / 2;
+    if (keys[mid] < v) low = mid + 1;
+    else high = mid;
+  }
+  return low;
+}
+
 // Up to 1024 N tokens: all digits in one workgroup.
 template <int N>
 __global__ void __launch_bounds__(1024)
 token_sort_once(Tokens tokens, int count, uint32_t vocab, int passes, int bits, uint32_t *keys, uint32_t *places,
-                uint32_t *joins) {
-  if (threadIdx.x < 2) joins[threadIdx.x] = 0;
+                uint32_t *joins, uint32_t *starts) {
+  if (joins && threadIdx.x < 2) joins[threadIdx.x] = 0;
   __shared__ uint16_t before[16 << kMaxBits];
   __shared__ uint32_t first[1 << kMaxBits], parts[16];
   __shared__ uint32_t key_at[1024 * N];
@@ -315,6 +324,10 @@ token_sort_once(Tokens tokens, int count, uint32_t vocab, int passes, int bits, 
       place[j] = place_at[mine + 64 * j];
     }
     __syncthreads();
+  }
+  if (starts) {
+    // where each row's tokens begin (key_at holds the sorted keys)
+    for (uint32_t v = tid; v <= vocab; v += 1024) starts[v] = static_cast<uint32_t>(first_not_below(key_at, count, v));
   }
 #pragma unroll
   for (int j = 0; j < N; ++j) {
@@ -427,16 +440,6 @@ struct Sums {
 };
 constexpr int kClearRows = 8;     // rows of the table per such workgroup
 constexpr int kShortRun = 8;       // pieces of a run that one group of threads adds up
-
-__device__ __forceinline__ int64_t first_not_below(const uint32_t *keys, int64_t n, uint32_t v) {
-  int64_t low = 0, high = n;
-  while (low < high) {
-    const int64_t mid = (low + high) / 2;
-    if (keys[mid] < v) low = mid + 1;
-    else high = mid;
-  }
-  return low;
-}
 
 template <class TW, Spread M>
 __device__ __forceinline__ void write_row(const Sums &p, typename TW::S *weight, uint32_t v, const Columns &c,
@@ -602,16 +605,58 @@ __global__ void __launch_bounds__(256) embedding_join(Sums p, typename TW::S *we
   }
 }
 
+// Few tokens of a small vocabulary: a workgroup per row of the table and
+// kJoinLanes * 8 columns, its groups of threads adding up consecutive parts of
+// the row's tokens, and then theirs in order.  One launch instead of two (4096 x
+// 128 into 256 rows: 15 us with the sort, 21 in pieces).
+template <class TG, class TW, Spread M>
+__global__ void __launch_bounds__(256)
+embedding_row_sums(Sums p, const uint32_t *starts, const typename TG::S *grad, typename TW::S *weight) {
+  __shared__ float sums[256][kColumns + 1];
+  const int64_t v = blockIdx.x / p.blocks, begin = starts[v];
+  const int n = static_cast<int>(starts[v + 1] - begin);
+  if (n == 0 && p.accumulate) return;
+  const int groups = 256 / p.lanes, lane = threadIdx.x % p.lanes, mine = threadIdx.x / p.lanes;
+  const Columns c(M, blockIdx.x % p.blocks, lane, p.lanes, p.width);
+  const int from = n * mine / groups, to = n * (mine + 1) / groups;
+  float acc[kColumns] = {0, 0, 0, 0, 0, 0, 0, 0};
+  constexpr int kAhead = 8;
+  for (int i = from; i < to; i += kAhead) {
+    float x[kAhead][kColumns];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a)
+      if (i + a < to) load_columns<TG, M>(grad + static_cast<int64_t>(p.places[begin + i + a]) * p.grad_pitch, c, x[a]);
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      if (i + a >= to) continue;
+#pragma unroll
+      for (int k = 0; k < kColumns; ++k) acc[k] += x[a][k];
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kColumns; ++k) sums[threadIdx.x][k] = acc[k];
+  __syncthreads();
+  if (mine > 0) return;
+  for (int g = 1; g < groups; ++g) {
+#pragma unroll
+    for (int k = 0; k < kColumns; ++k) acc[k] += sums[g * p.lanes + lane][k];
+  }
+  write_row<TW, M>(p, weight, static_cast<uint32_t>(v), c, acc);
+}
+
 // ---------------------------------------------------------------------------
 // plan of a gradient call
 // ---------------------------------------------------------------------------
+constexpr int64_t kRowGroups = 4096;   // workgroups that go by rows, at most
+
 struct Plan {
   int passes, bits;                  // digits of the sort
   bool many;                         // more than one workgroup's
+  bool by_row;                       // a workgroup per row of the table
   int64_t tiles;
   int lanes, piece;
   int64_t blocks, pieces;
-  size_t keys, places, keys2, places2, counts, joins, partials, bytes;   // offsets in the workspace
+  size_t keys, places, keys2, places2, counts, joins, partials, starts, bytes;   // offsets in the workspace
 };
 
 Plan plan_of(int64_t count, int64_t vocab, int64_t width) {
@@ -622,8 +667,10 @@ Plan plan_of(int64_t count, int64_t vocab, int64_t width) {
   p.bits = (bits + p.passes - 1) / p.passes;
   p.tiles = (count + kTile - 1) / kTile;
   p.many = count > kOnce * 1024;
-  p.lanes = lanes_for(width);
-  p.blocks = (width + static_cast<int64_t>(p.lanes) * kColumns - 1) / (p.lanes * kColumns);
+  p.lanes = lanes_for(width, kJoinLanes);
+  p.by_row = !p.many && vocab * blocks_of(width, p.lanes) <= kRowGroups;
+  if (!p.by_row) p.lanes = lanes_for(width);
+  p.blocks = blocks_of(width, p.lanes);
   // pieces of 8 to 64 tokens (a lane each): about 2048 workgroups where there are so many
   p.piece = static_cast<int>(std::clamp<int64_t>(count * p.blocks * p.lanes / 256 / 2048, 8, 64));
   p.pieces = (count + p.piece - 1) / p.piece;
@@ -638,8 +685,9 @@ Plan plan_of(int64_t count, int64_t vocab, int64_t width) {
   p.keys2 = p.many ? take(4 * count) : 0;
   p.places2 = p.many ? take(4 * count) : 0;
   p.counts = p.many ? take(4 * (p.tiles << p.bits)) : 0;
-  p.joins = take(4 * (2 + p.pieces));
-  p.partials = take(8 * p.pieces * ((width + 3) / 4 * 4));
+  p.starts = p.by_row ? take(4 * (vocab + 1)) : 0;
+  p.joins = p.by_row ? 0 : take(4 * (2 + p.pieces));
+  p.partials = p.by_row ? 0 : take(8 * p.pieces * ((width + 3) / 4 * 4));
   p.bytes = at;
   return p;
 }
@@ -649,7 +697,7 @@ Plan plan_of(int64_t count, int64_t vocab, int64_t width) {
 hipError_t launch_embedding(const void *tokens, int token_bits, int64_t count, const TokenRows &weight, int64_t vocab,
                             int64_t width, float scale, const TokenRows &out, hipStream_t s) {
   const int lanes = lanes_for(width);
-  const int64_t blocks = (width + static_cast<int64_t>(lanes) * kColumns - 1) / (lanes * kColumns);
+  const int64_t blocks = blocks_of(width, lanes);
   const int64_t grid = (count * blocks + 256 / lanes - 1) / (256 / lanes);
   return with_type(weight.dtype, [&](auto tw) {
     return with_type(out.dtype, [&](auto to) {
@@ -678,7 +726,8 @@ hipError_t launch_embedding_grad(const void *tokens, int token_bits, int64_t cou
   uint32_t *keys = words(plan.keys), *places = words(plan.places), *joins = words(plan.joins);
   if (count > 0 && !plan.many) {
     token_sort_once<kOnce><<<dim3(1), dim3(1024), 0, s>>>(t, static_cast<int>(count), v, plan.passes, plan.bits, keys,
-                                                         places, joins);
+                                                         places, plan.by_row ? nullptr : joins,
+                                                         plan.by_row ? words(plan.starts) : nullptr);
   } else if (count > 0) {
     uint32_t *keys2 = words(plan.keys2), *places2 = words(plan.places2), *counts = words(plan.counts);
     for (int pass = 0; pass < plan.passes; ++pass) {
@@ -701,7 +750,7 @@ hipError_t launch_embedding_grad(const void *tokens, int token_bits, int64_t cou
          work, joins};
   const int64_t clear = accumulate ? 0 : (vocab + kClearRows - 1) / kClearRows;
   const int join_lanes = lanes_for(width, kJoinLanes);
-  const int64_t join_blocks = (width + join_lanes * kColumns - 1) / (join_lanes * kColumns);
+  const int64_t join_blocks = blocks_of(width, join_lanes);
   return with_type(grad.dtype, [&](auto tg) {
     return with_type(grad_weight.dtype, [&](auto tw) {
       return with_spread(spread_of(grad, grad_weight), [&](auto m) {
@@ -709,6 +758,10 @@ hipError_t launch_embedding_grad(const void *tokens, int token_bits, int64_t cou
         using TW = decltype(tw);
         typename TW::S *w = static_cast<typename TW::S *>(grad_weight.data);
         const typename TG::S *g = static_cast<const typename TG::S *>(grad.data);
+        if (plan.by_row && count > 0) {
+          embedding_row_sums<TG, TW, m.value><<<dim3(vocab * plan.blocks), dim3(256), 0, s>>>(p, words(plan.starts), g, w);
+          return hipGetLastError();
+        }
         const dim3 grid = grid_of(clear + work);
         if (plan.lanes >= 64) embedding_sums<TG, TW, m.value, true><<<grid, dim3(256), 0, s>>>(p, g, w);
         else embedding_sums<TG, TW, m.value, false><<<grid, dim3(256), 0, s>>>(p, g, w);

@@ -52,9 +52,21 @@ struct Octet {
   static constexpr bool k16 = sizeof(typename T::S) == 2;
   uint32_t w[k16 ? 4 : 8];
 
-  __device__ __forceinline__ float at(int i) const {
-    if constexpr (k16) return T::ld(static_cast<typename T::S>(w[i / 2] >> (16 * (i & 1))));
-    else return __uint_as_float(w[i]);
+  // `left` of them are there, the others are zero.  (16-byte accesses need no
+  // alignment beyond the element's.)
+  __device__ __forceinline__ void load(const typename T::S *src, int left) {
+    if (left >= 8) {
+      __builtin_memcpy(w, src, sizeof(w));
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < (k16 ? 4 : 8); ++i) w[i] = 0;
+#pragma unroll
+    for (int i = 0; i < 7; ++i) {
+      if (i >= left) break;
+      if constexpr (k16) w[i / 2] |= static_cast<uint32_t>(src[i]) << (16 * (i & 1));
+      else w[i] = __float_as_uint(src[i]);
+    }
   }
   // bits of the largest magnitude, as a float's
   __device__ __forceinline__ uint32_t largest() const {
@@ -71,6 +83,15 @@ struct Octet {
     }
   }
 };
+
+// The value of another lane of 16, where values are equal within the groups
+// that it spans: lane ^ 1, ^ 2 (quads), ^ 4 (mirrored halves) or ^ 8 (mirrored
+// rows of 16 lanes).
+template <int D>
+__device__ __forceinline__ uint32_t other_lane(uint32_t v) {
+  constexpr int kControl = D == 1 ? 0xb1 : D == 2 ? 0x4e : D == 4 ? 0x141 : 0x140;
+  return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), kControl, 0xf, 0xf, true));
+}
 
 // Two codes into byte SEL of old: the conversion divides by the scale, rounds
 // to nearest with ties to even and cuts off at 6.
@@ -126,7 +147,7 @@ struct MxQuantize {
 // of a column are neighbours, so that they write its 64 bytes of codes
 // together.  A row of LDS has its 16-byte pieces exchanged by its block of 32
 // rows, which puts those four threads on different banks.
-template <class T, bool ROWS, bool COLS, bool NOISE, bool WIDE>
+template <class T, bool ROWS, bool COLS, bool NOISE>
 __global__ void __launch_bounds__(256) mx_quantize(MxQuantize p) {
   using S = typename T::S;
   constexpr bool k16 = sizeof(S) == 2;
@@ -153,28 +174,18 @@ __global__ void __launch_bounds__(256) mx_quantize(MxQuantize p) {
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
       const int64_t row = row0 + k0 + 16 * a + r_in;
-#pragma unroll
-      for (int i = 0; i < (k16 ? 4 : 8); ++i) v[a].w[i] = 0;
+      const int here = row < p.rows ? left : 0;
+      v[a].load(x + row * p.pitch + col, here);
       r[a][0] = r[a][1] = 0;
-      if (row >= p.rows || left <= 0) continue;
-      const S *src = x + row * p.pitch + col;
-      if (WIDE && left == 8) {
-#pragma unroll
-        for (int i = 0; i < (k16 ? 1 : 2); ++i)
-          *reinterpret_cast<uint4 *>(v[a].w + 4 * i) = reinterpret_cast<const uint4 *>(src)[i];
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (i >= left) break;
-          if constexpr (k16) v[a].w[i / 2] |= static_cast<uint32_t>(src[i]) << (16 * (i & 1));
-          else v[a].w[i] = __float_as_uint(src[i]);
-        }
-      }
       if constexpr (NOISE) {
         const uint8_t *from = noise + row * p.cols + col;
+        if (here >= 8) {
+          __builtin_memcpy(r[a], from, 8);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (i < left) r[a][i / 4] |= static_cast<uint32_t>(from[i]) << (8 * (i & 3));
+          for (int i = 0; i < 7; ++i)
+            if (i < here) r[a][i / 4] |= static_cast<uint32_t>(from[i]) << (8 * (i & 3));
+        }
       }
     }
 #pragma unroll
@@ -193,8 +204,8 @@ __global__ void __launch_bounds__(256) mx_quantize(MxQuantize p) {
       }
       if constexpr (ROWS) {
         uint32_t largest = v[a].largest();
-        largest = max(largest, __shfl_xor(largest, 1));
-        largest = max(largest, __shfl_xor(largest, 2));
+        largest = max(largest, other_lane<1>(largest));
+        largest = max(largest, other_lane<2>(largest));
         const uint32_t s = scale_byte(largest, NOISE);
         uint32_t bits[8], bytes[8];
 #pragma unroll
@@ -204,8 +215,8 @@ __global__ void __launch_bounds__(256) mx_quantize(MxQuantize p) {
         }
         const uint32_t word = eight_codes<T, NOISE>(bits, bytes, s);
         uint32_t scales = s << (8 * ((lane >> 2) & 3));
-        scales |= __shfl_xor(scales, 4);
-        scales |= __shfl_xor(scales, 8);
+        scales |= other_lane<4>(scales);
+        scales |= other_lane<8>(scales);
         if (row < p.rows) {
           *reinterpret_cast<uint32_t *>(p.by_rows.codes + (mat * p.rows + row) * (groups * 64) + (col0 + c_in) / 2) = word;
         } else {
@@ -247,8 +258,8 @@ __global__ void __launch_bounds__(256) mx_quantize(MxQuantize p) {
         word.z = eight_codes<T, NOISE>(bits + 16, bytes + 16, s);
         word.w = eight_codes<T, NOISE>(bits + 24, bytes + 24, s);
         uint32_t scales = s << (8 * rb);
-        scales |= __shfl_xor(scales, 1);
-        scales |= __shfl_xor(scales, 2);
+        scales |= other_lane<1>(scales);
+        scales |= other_lane<2>(scales);
         if (column < p.cols) {
           *reinterpret_cast<uint4 *>(p.by_columns.codes + (mat * p.cols + column) * (t_groups * 64) + row0 / 2 + rb * 16) =
               word;
@@ -264,7 +275,7 @@ __global__ void __launch_bounds__(256) mx_quantize(MxQuantize p) {
 }
 
 // The values of a 128 x 128 tile, eight per thread.
-template <class T, bool WIDE>
+template <class T>
 __global__ void __launch_bounds__(256) mx_dequantize(MxMatrix q, typename T::S *out, int tiles_r, int tiles_c) {
   using S = typename T::S;
   typedef float f32x2 __attribute__((ext_vector_type(2)));
@@ -293,13 +304,13 @@ __global__ void __launch_bounds__(256) mx_dequantize(MxMatrix q, typename T::S *
     two(4, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, 2));
     two(6, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, 3));
     S *to = out + (mat * q.rows + row) * q.cols + col;
-    if (WIDE && col + 8 <= q.cols) {
+    if (col + 8 <= q.cols) {
+      // (16-byte accesses need no alignment beyond the element's)
       if constexpr (sizeof(S) == 4) {
-        reinterpret_cast<float4 *>(to)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4 *>(to)[1] = make_float4(v[4], v[5], v[6], v[7]);
+        __builtin_memcpy(to, v, 32);
       } else {
-        *reinterpret_cast<uint4 *>(to) =
-            make_uint4(T::st2(v[0], v[1]), T::st2(v[2], v[3]), T::st2(v[4], v[5]), T::st2(v[6], v[7]));
+        const uint32_t words[4] = {T::st2(v[0], v[1]), T::st2(v[2], v[3]), T::st2(v[4], v[5]), T::st2(v[6], v[7])};
+        __builtin_memcpy(to, words, 16);
       }
     } else {
 #pragma unroll
@@ -631,7 +642,6 @@ struct MxThin {
   MxOutput o;
   const void *x;
   int64_t x_pitch, x_batch_stride;
-  int wide;                                 // rows of x begin on 16 bytes
 };
 
 template <class TX, class TO, int MB, int W, bool QUANTIZE>
@@ -674,25 +684,11 @@ __global__ void __launch_bounds__(64 * W) mx_thin(MxThin p) {
     for (int u = tid; u < m * groups * 16; u += 64 * W) {
       const int row = u / (groups * 16), at = u - row * groups * 16;
       const int64_t col = static_cast<int64_t>(at) * 8;
-      const S *src = x + row * p.x_pitch + col;
       Octet<TX> v;
-#pragma unroll
-      for (int i = 0; i < (k16 ? 4 : 8); ++i) v.w[i] = 0;
-      if (p.wide && col + 8 <= p.b.cols) {
-#pragma unroll
-        for (int i = 0; i < (k16 ? 1 : 2); ++i)
-          *reinterpret_cast<uint4 *>(v.w + 4 * i) = reinterpret_cast<const uint4 *>(src)[i];
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (col + i >= p.b.cols) break;
-          if constexpr (k16) v.w[i / 2] |= static_cast<uint32_t>(src[i]) << (16 * (i & 1));
-          else v.w[i] = __float_as_uint(src[i]);
-        }
-      }
+      v.load(x + row * p.x_pitch + col, static_cast<int>(min<int64_t>(8, p.b.cols - col)));
       uint32_t largest = v.largest();
-      largest = max(largest, __shfl_xor(largest, 1));
-      largest = max(largest, __shfl_xor(largest, 2));
+      largest = max(largest, other_lane<1>(largest));
+      largest = max(largest, other_lane<2>(largest));
       const uint32_t s = scale_byte(largest, false);
       uint32_t bits[8];
 #pragma unroll
@@ -763,22 +759,17 @@ hipError_t launch_mx_quantize(const MxInput &in, int64_t batch, int64_t rows, in
   MxQuantize p{in.x, in.pitch, in.batch_stride, in.noise, rows, cols, by_rows, by_columns,
                static_cast<int>((rows + 127) / 128), static_cast<int>((cols + 127) / 128)};
   const int64_t tiles = batch * p.tiles_r * p.tiles_c;
-  const int64_t elem = dtype_size(in.dtype);
-  const bool wide = reinterpret_cast<uintptr_t>(in.x) % 16 == 0 && in.pitch * elem % 16 == 0 &&
-                    in.batch_stride * elem % 16 == 0;
   return with_type(in.dtype, [&](auto t) {
     using T = decltype(t);
     return with_flag(in.noise != nullptr, [&](auto noise) {
-      return with_flag(wide, [&](auto w) {
-        auto run = [&](auto kernel) {
-          kernel<<<dim3(tiles), dim3(256), 0, s>>>(p);
-          return hipGetLastError();
-        };
-        constexpr bool N = decltype(noise)::value, W = decltype(w)::value;
-        if (!by_columns.codes) return run(mx_quantize<T, true, false, N, W>);
-        if (!by_rows.codes) return run(mx_quantize<T, false, true, N, W>);
-        return run(mx_quantize<T, true, true, N, W>);
-      });
+      auto run = [&](auto kernel) {
+        kernel<<<dim3(tiles), dim3(256), 0, s>>>(p);
+        return hipGetLastError();
+      };
+      constexpr bool N = decltype(noise)::value;
+      if (!by_columns.codes) return run(mx_quantize<T, true, false, N>);
+      if (!by_rows.codes) return run(mx_quantize<T, false, true, N>);
+      return run(mx_quantize<T, true, true, N>);
     });
   });
 }
@@ -786,14 +777,10 @@ hipError_t launch_mx_quantize(const MxInput &in, int64_t batch, int64_t rows, in
 hipError_t launch_mx_dequantize(const MxMatrix &q, void *out, int dtype, hipStream_t s) {
   const int tiles_r = static_cast<int>((q.rows + 127) / 128), tiles_c = static_cast<int>((q.cols + 127) / 128);
   const int64_t tiles = q.batch * tiles_r * tiles_c;
-  const bool wide = reinterpret_cast<uintptr_t>(out) % 16 == 0 && q.cols * dtype_size(dtype) % 16 == 0;
   return with_type(dtype, [&](auto t) {
-    return with_flag(wide, [&](auto w) {
-      using T = decltype(t);
-      mx_dequantize<T, decltype(w)::value>
-          <<<dim3(tiles), dim3(256), 0, s>>>(q, static_cast<typename T::S *>(out), tiles_r, tiles_c);
-      return hipGetLastError();
-    });
+    using T = decltype(t);
+    mx_dequantize<T><<<dim3(tiles), dim3(256), 0, s>>>(q, static_cast<typename T::S *>(out), tiles_r, tiles_c);
+    return hipGetLastError();
   });
 }
 
@@ -802,10 +789,7 @@ size_t mx_matmul_bytes(int64_t, int64_t, int64_t, int64_t) { return 0; }
 bool mx_linear_quantizes(int64_t m, int64_t k) { return m <= 16 && m * ((k + kMxGroup - 1) / kMxGroup) * kMxGroup <= kThinValues; }
 
 hipError_t launch_mx_linear(const MxInput &in, int64_t m, const MxMatrix &w, const MxOutput &out, hipStream_t s) {
-  const int64_t elem = dtype_size(in.dtype);
-  const MxThin p{MxMatrix{nullptr, nullptr, w.batch, m, w.cols}, w, out, in.x, in.pitch, in.batch_stride,
-                 reinterpret_cast<uintptr_t>(in.x) % 16 == 0 && in.pitch * elem % 16 == 0 &&
-                     in.batch_stride * elem % 16 == 0};
+  const MxThin p{MxMatrix{nullptr, nullptr, w.batch, m, w.cols}, w, out, in.x, in.pitch, in.batch_stride};
   return with_type(in.dtype, [&](auto tx) {
     return with_type(out.dtype, [&](auto to) { return run_thin<decltype(tx), decltype(to), 1, true>(p, s); });
   });
@@ -815,7 +799,7 @@ hipError_t launch_mx_matmul(const MxMatrix &a, const MxMatrix &b, const MxOutput
   if (a.rows <= kThinRows)
     return with_type(out.dtype, [&](auto t) {
       using T = decltype(t);
-      const MxThin p{a, b, out, nullptr, 0, 0, 0};
+      const MxThin p{a, b, out, nullptr, 0, 0};
       return a.rows <= 16 ? run_thin<EF32, T, 1, false>(p, s) : run_thin<EF32, T, 2, false>(p, s);
     });
   return with_type(out.dtype, [&](auto t) {

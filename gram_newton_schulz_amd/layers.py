@@ -10,22 +10,38 @@ counter.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
+import math
 from typing import Optional, Sequence, Tuple, Union
 
 import torch
 
-from .binding import GnsError, _DT, _check, _device_tensor, _dtype_code, _ptr, _workspace, lib
+from .binding import GnsError, _DT, _check, _device_tensor, _workspace, lib
 from .tensors import _current_device, _current_raw_stream
 
 _TOKEN_BITS = {torch.int32: 32, torch.int64: 64}
+_STRIDED = torch.strided
 
 
 class Matrix(ctypes.Structure):
     """gns_mxfp4."""
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("batch", ctypes.c_int64),
                 ("rows", ctypes.c_int64), ("cols", ctypes.c_int64)]
+
+
+# The calls of small problems take about as long as Python does around them (a
+# launch is 3.3 us), so the checks below ask each question once, and in the
+# form that costs least.
+
+@contextlib.contextmanager
+def _elsewhere(index: int, stream):
+    """Makes the device, and the stream that a caller passed, current: what a
+    call allocates then belongs to that stream."""
+    device = torch.device("cuda", index)
+    with torch.cuda.device(device), torch.cuda.stream(_stream_on(device, stream)):
+        yield
 
 
 def _stream_on(device: torch.device, stream) -> "torch.cuda.Stream":
@@ -44,33 +60,32 @@ def _stream_on(device: torch.device, stream) -> "torch.cuda.Stream":
     return torch.cuda.ExternalStream(stream, device=device)
 
 
-def _placed(position: int, name: str):
-    """Runs a call on the device of the named argument and on ``stream``, with
-    both current: what it allocates belongs to that stream."""
-    def wrap(fn):
-        @functools.wraps(fn)
-        def call(*args, stream=None, **kwargs):
-            device = getattr(args[position] if len(args) > position else kwargs.get(name), "device", None)
-            if device is None or device.type != "cuda":
-                return fn(*args, **kwargs)                       # (which raises)
-            if stream is None and device.index == _current_device():
-                return fn(*args, **kwargs)
-            with torch.cuda.device(device), torch.cuda.stream(_stream_on(device, stream)):
-                return fn(*args, **kwargs)
-        return call
-    return wrap
-
-
-def _need(name: str, t, device=None) -> None:
-    if not isinstance(t, torch.Tensor) or t.layout is not torch.strided:
+def _index_of(name: str, t) -> int:
+    """Device index of a dense tensor on a GPU."""
+    if not isinstance(t, torch.Tensor) or t.layout is not _STRIDED:
         raise GnsError(1, f"{name} is not a dense tensor: {type(t).__name__}")
-    _device_tensor(name, t, device)
+    if not t.is_cuda:
+        _device_tensor(name, t, None)
+    return t.get_device()
+
+
+def _need(name: str, t, index: int) -> None:
+    """Raise unless t is a dense tensor on that GPU."""
+    if _index_of(name, t) != index:
+        _device_tensor(name, t, torch.device("cuda", index))
 
 
 def _type(name: str, t: torch.Tensor) -> int:
     code = _DT.get(t.dtype)
     if code is None:
         raise GnsError(3, f"{name} has dtype {t.dtype}")
+    return code
+
+
+def _type_of(dtype) -> int:
+    code = _DT.get(dtype)
+    if code is None:
+        raise GnsError(3, f"unsupported dtype {dtype}")
     return code
 
 
@@ -100,49 +115,59 @@ def _rows_of(name: str, t: torch.Tensor, lead: Sequence[int]) -> int:
 
 
 def _tokens(tokens) -> int:
-    _need("tokens", tokens)
-    if tokens.dtype not in _TOKEN_BITS:
+    bits = _TOKEN_BITS.get(tokens.dtype)
+    if bits is None:
         raise GnsError(3, f"tokens have dtype {tokens.dtype}: int32 or int64 is needed")
     if not tokens.is_contiguous():
         raise GnsError(2, "tokens must be contiguous")
-    return _TOKEN_BITS[tokens.dtype]
+    return bits
 
 
-@_placed(0, "tokens")
+def _table(name: str, t: torch.Tensor, index: int):
+    """(vocab, width, pitch, type) of a table."""
+    _need(name, t, index)
+    shape = t.shape
+    if len(shape) != 2:
+        raise GnsError(2, f"{name} must be [vocab, width], got {tuple(shape)}")
+    vocab, width = shape
+    return vocab, width, width if t.is_contiguous() else _rows_of(name, t, (vocab,)), _type(name, t)
+
+
 def embedding(tokens: torch.Tensor, weight: torch.Tensor, *, scale: float = 1.0, dtype: Optional[torch.dtype] = None,
-              out: Optional[torch.Tensor] = None) -> torch.Tensor:
+              out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """``scale * weight[tokens]`` in one pass (gns_embedding): tokens (int32 or
     int64, any shape) into rows of weight ([vocab, width]), in ``dtype``
     (weight's by default) or into ``out`` ([*tokens.shape, width]).  A token
     outside the vocabulary is padding and gives a row of zeros."""
+    index = _index_of("tokens", tokens)
+    if stream is not None or index != _current_device():
+        with _elsewhere(index, stream):
+            return embedding(tokens, weight, scale=scale, dtype=dtype, out=out)
     bits = _tokens(tokens)
-    device = tokens.device
-    _need("weight", weight, device)
-    if weight.dim() != 2:
-        raise GnsError(2, f"weight must be [vocab, width], got {tuple(weight.shape)}")
-    vocab, width = weight.shape
+    vocab, width, pitch, code = _table("weight", weight, index)
     if out is None:
-        out = torch.empty(*tokens.shape, width, dtype=dtype or weight.dtype, device=device)
+        dtype = dtype or weight.dtype
+        out_code, out_pitch = _type_of(dtype), width
+        out = torch.empty((*tokens.shape, width), dtype=dtype, device=tokens.device)
     else:
-        _need("out", out, device)
+        _need("out", out, index)
         if out.dim() == 0 or out.shape[-1] != width:
             raise GnsError(2, f"out has shape {tuple(out.shape)}, rows of weight have {width}")
         if dtype is not None and out.dtype != dtype:
             raise GnsError(3, f"out has dtype {out.dtype}, dtype is {dtype}")
-    _check(lib().gns_embedding(tokens.data_ptr(), bits, tokens.numel(), weight.data_ptr(), _type("weight", weight),
-                               vocab, width, _rows_of("weight", weight, (vocab,)), float(scale), out.data_ptr(),
-                               _type("out", out), _rows_of("out", out, tokens.shape),
-                               _current_raw_stream(device.index)))
+        out_code, out_pitch = _type("out", out), _rows_of("out", out, tokens.shape)
+    _check(lib().gns_embedding(tokens.data_ptr(), bits, tokens.numel(), weight.data_ptr(), code, vocab, width, pitch,
+                               float(scale), out.data_ptr(), out_code, out_pitch, _current_raw_stream(index)))
     return out
 
 
+@functools.lru_cache(maxsize=1024)
 def embedding_grad_workspace_bytes(count: int, vocab: int, width: int) -> int:
     return int(lib().gns_embedding_grad_workspace_bytes(count, vocab, width))
 
 
-@_placed(0, "tokens")
 def embedding_grad(tokens: torch.Tensor, grad: torch.Tensor, grad_weight: torch.Tensor, *, scale: float = 1.0,
-                   accumulate: bool = False, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+                   accumulate: bool = False, workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The gradient of :func:`embedding` with respect to its weight
     (gns_embedding_grad): row v of grad_weight ([vocab, width], written in
     place) becomes ``scale`` times the sum of the rows of grad
@@ -151,23 +176,25 @@ def embedding_grad(tokens: torch.Tensor, grad: torch.Tensor, grad_weight: torch.
     once; the three may have different types.  Padding tokens are left out.
     grad_weight may be a slice of a gradient bucket, ready for grad_norm and
     adamw_step.  Returns grad_weight."""
+    index = _index_of("tokens", tokens)
+    if stream is not None or index != _current_device():
+        with _elsewhere(index, stream):
+            return embedding_grad(tokens, grad, grad_weight, scale=scale, accumulate=accumulate, workspace=workspace)
     bits = _tokens(tokens)
-    device = tokens.device
-    _need("grad", grad, device)
-    _need("grad_weight", grad_weight, device)
-    if grad_weight.dim() != 2:
-        raise GnsError(2, f"grad_weight must be [vocab, width], got {tuple(grad_weight.shape)}")
-    vocab, width = grad_weight.shape
+    _need("grad", grad, index)
+    vocab, width, pitch, code = _table("grad_weight", grad_weight, index)
     if grad.dim() == 0 or grad.shape[-1] != width:
         raise GnsError(2, f"grad has shape {tuple(grad.shape)}, rows of grad_weight have {width}")
-    L, count = lib(), tokens.numel()
-    ws = _workspace(0 if workspace is not None else L.gns_embedding_grad_workspace_bytes(count, vocab, width), device,
-                    workspace)
-    _check(L.gns_embedding_grad(tokens.data_ptr(), bits, count, grad.data_ptr(), _type("grad", grad),
-                                _rows_of("grad", grad, tokens.shape), vocab, width, float(scale),
-                                grad_weight.data_ptr(), _type("grad_weight", grad_weight),
-                                _rows_of("grad_weight", grad_weight, (vocab,)), 1 if accumulate else 0, ws.data_ptr(),
-                                ws.numel() * ws.element_size(), _current_raw_stream(device.index)))
+    grad_pitch, count = _rows_of("grad", grad, tokens.shape), tokens.numel()
+    if workspace is None:
+        need = embedding_grad_workspace_bytes(count, vocab, width)
+        ws = torch.empty(need, dtype=torch.uint8, device=tokens.device)
+    else:
+        ws = _workspace(0, tokens.device, workspace)
+        need = ws.numel() * ws.element_size()
+    _check(lib().gns_embedding_grad(tokens.data_ptr(), bits, count, grad.data_ptr(), _type("grad", grad), grad_pitch,
+                                    vocab, width, float(scale), grad_weight.data_ptr(), code, pitch, 1 if accumulate else 0,
+                                    ws.data_ptr(), need, _current_raw_stream(index)))
     return grad_weight
 
 
@@ -180,26 +207,51 @@ class MXFP4:
     ``codes`` ([..., rows, K / 2], K the columns rounded up to 128) and
     ``scales`` ([..., row blocks, K / 128, 32, 4]) are uint8.  Index a batch for
     one of its matrices."""
-    __slots__ = ("codes", "scales", "shape", "_c", "_ref")
+    __slots__ = ("shape", "_codes", "_scales", "_room", "_index", "_c", "_ref", "_dims")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, shape: Sequence[int]):
         shape = torch.Size(shape)
-        if len(shape) not in (2, 3):
-            raise GnsError(2, f"shape must be [rows, cols] or [batch, rows, cols], got {tuple(shape)}")
-        lead, (rows, cols) = shape[:-2], shape[-2:]
+        lead, rows, cols = _sizes(shape)
         groups = -(-cols // 128)
         wanted = {"codes": (*lead, rows, groups * 64), "scales": (*lead, -(-rows // 32), groups, 32, 4)}
+        index = _index_of("codes", codes)
+        _need("scales", scales, index)
         for name, t in (("codes", codes), ("scales", scales)):
-            _need(name, t, codes.device)
             if t.dtype != torch.uint8 or tuple(t.shape) != wanted[name] or not t.is_contiguous():
                 raise GnsError(2, f"{name} must be contiguous uint8 {wanted[name]}, got {t.dtype} {tuple(t.shape)}")
-        self.codes, self.scales, self.shape = codes, scales, shape
-        self._c = Matrix(codes.data_ptr(), scales.data_ptr(), lead[0] if lead else 1, rows, cols)
+        self._set(shape, codes.data_ptr(), scales.data_ptr(), index)
+        self._codes, self._scales = codes, scales
+
+    def _set(self, shape, codes: int, scales: int, index: int) -> None:
+        self.shape, self._index = shape, index
+        self._dims = batch, rows, cols = (1, *shape) if len(shape) == 2 else tuple(shape)
+        self._codes = self._scales = self._room = None
+        self._c = Matrix(codes, scales, batch, rows, cols)
         self._ref = ctypes.byref(self._c)
+
+    def _view(self, offset: int, shape) -> torch.Tensor:
+        n = math.prod(shape)
+        return self._room[offset:offset + n].view(shape)
+
+    @property
+    def codes(self) -> torch.Tensor:
+        if self._codes is None:
+            lead, rows, cols = _sizes(self.shape)
+            self._codes = self._view(self._c.codes - self._room.data_ptr() if self._c.codes else 0,
+                                     (*lead, rows, -(-cols // 128) * 64))
+        return self._codes
+
+    @property
+    def scales(self) -> torch.Tensor:
+        if self._scales is None:
+            lead, rows, cols = _sizes(self.shape)
+            self._scales = self._view(self._c.scales - self._room.data_ptr() if self._c.scales else 0,
+                                      (*lead, -(-rows // 32), -(-cols // 128), 32, 4))
+        return self._scales
 
     @property
     def device(self) -> torch.device:
-        return self.codes.device
+        return torch.device("cuda", self._index)
 
     @property
     def nbytes(self) -> int:
@@ -217,116 +269,160 @@ class MXFP4:
         return f"MXFP4({tuple(self.shape)}, device={str(self.device)!r})"
 
 
+def _sizes(shape):
+    if len(shape) == 2:
+        return (), *shape
+    if len(shape) == 3:
+        return shape[:1], *shape[1:]
+    raise GnsError(2, f"shape must be [rows, cols] or [batch, rows, cols], got {tuple(shape)}")
+
+
+def _rooms(shapes, index: int):
+    """MXFP4 objects of the shapes in one allocation, each array on 256 bytes."""
+    at, places = 0, []
+    for shape in shapes:
+        lead, rows, cols = _sizes(shape)
+        batch, groups = lead[0] if lead else 1, -(-cols // 128)
+        scales = at + (batch * rows * groups * 64 + 255) // 256 * 256
+        places.append((shape, at, scales))
+        at = scales + (batch * -(-rows // 32) * groups * 128 + 255) // 256 * 256
+    room = torch.empty(at, dtype=torch.uint8, device=torch.device("cuda", index))
+    base, made = room.data_ptr(), []
+    for shape, codes, scales in places:
+        q = object.__new__(MXFP4)
+        q._set(shape, base + codes, base + scales, index)
+        q._room = room
+        made.append(q)
+    return made
+
+
 def mxfp4_empty(shape: Sequence[int], device=None) -> MXFP4:
     """Room for a matrix or a batch of matrices (the ``out`` of
     :func:`mxfp4_quantize`)."""
-    shape = torch.Size(shape)
-    if len(shape) not in (2, 3):
-        raise GnsError(2, f"shape must be [rows, cols] or [batch, rows, cols], got {tuple(shape)}")
-    lead, (rows, cols) = shape[:-2], shape[-2:]
-    groups = -(-cols // 128)
-    device = torch.device("cuda") if device is None else device
-    return MXFP4(torch.empty(*lead, rows, groups * 64, dtype=torch.uint8, device=device),
-                 torch.empty(*lead, -(-rows // 32), groups, 32, 4, dtype=torch.uint8, device=device), shape)
+    device = torch.device("cuda" if device is None else device)
+    if device.type != "cuda":
+        raise GnsError(1, f"device must be a GPU, got {device}")
+    return _rooms([torch.Size(shape)], torch.cuda.current_device() if device.index is None else device.index)[0]
 
 
-def _matrix(name: str, x: torch.Tensor):
+def _matrix(x: torch.Tensor):
     """(batch, rows, cols, pitch, batch stride) of a [rows, cols] or
     [batch, rows, cols] tensor whose rows' elements are consecutive, or None."""
-    shape, st = x.shape, x.stride()
-    rows, cols = shape[-2:]
+    shape = x.shape
+    if len(shape) == 2:
+        batch, (rows, cols) = 1, shape
+    else:
+        batch, rows, cols = shape
+    if x.is_contiguous():
+        return batch, rows, cols, cols, rows * cols
+    st = x.stride()
     if cols > 1 and st[-1] != 1 and x.numel():
         return None
-    pitch = st[-2] if rows > 1 and cols else cols
-    if len(shape) == 2:
-        return 1, rows, cols, pitch, 0
-    return shape[0], rows, cols, pitch, st[0] if shape[0] > 1 else 0
+    return batch, rows, cols, st[-2] if rows > 1 and cols else cols, st[0] if batch > 1 and len(shape) == 3 else 0
 
 
-def _quantize(x, noise, straight, turned):
+def _quantize(x, noise, straight, turned, index: int) -> None:
     """Q(x) into ``straight`` and Q(x^T) into ``turned`` (either may be None:
     not wanted)."""
-    device = x.device
     code = _type("x", x)
-    form = _matrix("x", x)
+    form = _matrix(x)
     if form is None:
-        form = _matrix("x", x.mT)
+        form = _matrix(x.mT)
         if form is None:
             raise GnsError(2, f"x: elements of a row or of a column must be consecutive (strides {x.stride()})")
         straight, turned = turned, straight
         noise = None if noise is None else noise.mT
     if noise is not None:
-        _need("noise", noise, device)
+        _need("noise", noise, index)
         if noise.dtype != torch.uint8 or not noise.is_contiguous():
             raise GnsError(2, "noise must be uint8, contiguous in x's order")
-    batch, rows, cols, pitch, batch_stride = form
-    _check(lib().gns_mxfp4_quantize(x.data_ptr(), code, pitch, batch_stride, _ptr(noise),
+    _check(lib().gns_mxfp4_quantize(x.data_ptr(), code, form[3], form[4], None if noise is None else noise.data_ptr(),
                                     None if straight is None else straight._ref,
-                                    None if turned is None else turned._ref, _current_raw_stream(device.index)))
+                                    None if turned is None else turned._ref, _current_raw_stream(index)))
 
 
-def _quantize_args(x, noise):
-    _need("x", x)
-    if x.dim() not in (2, 3):
-        raise GnsError(2, f"x must be [rows, cols] or [batch, rows, cols], got {tuple(x.shape)}")
-    if noise is not None and (not isinstance(noise, torch.Tensor) or noise.shape != x.shape):
+def _quantize_shape(x, noise):
+    shape = x.shape
+    if len(shape) not in (2, 3):
+        raise GnsError(2, f"x must be [rows, cols] or [batch, rows, cols], got {tuple(shape)}")
+    if noise is not None and (not isinstance(noise, torch.Tensor) or noise.shape != shape):
         raise GnsError(2, "noise must have x's shape")
+    return shape, torch.Size((*shape[:-2], shape[-1], shape[-2]))
 
 
-def _quantized_out(out, shape, device) -> MXFP4:
-    if out is None:
-        return mxfp4_empty(shape, device)
-    if not isinstance(out, MXFP4) or out.shape != shape:
-        raise GnsError(2, f"out must be an MXFP4 of shape {tuple(shape)}, got {out!r}")
-    _device_tensor("out", out.codes, device)
-    return out
+def _check_room(q, shape, index: int) -> None:
+    if not isinstance(q, MXFP4) or q.shape != shape:
+        raise GnsError(2, f"out must be an MXFP4 of shape {tuple(shape)}, got {q!r}")
+    if q._index != index:
+        raise GnsError(1, f"out is on {q.device}, x on cuda:{index}")
 
 
-@_placed(0, "x")
 def mxfp4_quantize(x: torch.Tensor, *, transposed: bool = False, noise: Optional[torch.Tensor] = None,
-                   out: Optional[MXFP4] = None) -> MXFP4:
+                   out: Optional[MXFP4] = None, stream=None) -> MXFP4:
     """x ([rows, cols] or [batch, rows, cols]; fp32, bf16 or fp16; rows or
     columns of consecutive elements) in MXFP4 with blocks along its rows, or
     with ``transposed`` its transpose, with blocks along its columns
     (gns_mxfp4_quantize).  Values are rounded to nearest, or with ``noise``
     (random bytes of x's shape) up or down with their probability and nothing
     cut off."""
-    _quantize_args(x, noise)
-    shape = x.mT.shape if transposed else x.shape
-    out = _quantized_out(out, shape, x.device)
-    _quantize(x, noise, None if transposed else out, out if transposed else None)
+    index = _index_of("x", x)
+    if stream is not None or index != _current_device():
+        with _elsewhere(index, stream):
+            return mxfp4_quantize(x, transposed=transposed, noise=noise, out=out)
+    shape = _quantize_shape(x, noise)[1 if transposed else 0]
+    if out is None:
+        out, = _rooms((shape,), index)
+    else:
+        _check_room(out, shape, index)
+    _quantize(x, noise, None if transposed else out, out if transposed else None, index)
     return out
 
 
-@_placed(0, "x")
 def mxfp4_quantize_both(x: torch.Tensor, *, noise: Optional[torch.Tensor] = None,
-                        out: Optional[Tuple[MXFP4, MXFP4]] = None) -> Tuple[MXFP4, MXFP4]:
+                        out: Optional[Tuple[MXFP4, MXFP4]] = None, stream=None) -> Tuple[MXFP4, MXFP4]:
     """:func:`mxfp4_quantize` of x and of its transpose in one pass over x: what
     the products of the forward and the backward pass take."""
-    _quantize_args(x, noise)
-    a, b = (None, None) if out is None else out
-    a, b = _quantized_out(a, x.shape, x.device), _quantized_out(b, x.mT.shape, x.device)
-    _quantize(x, noise, a, b)
+    index = _index_of("x", x)
+    if stream is not None or index != _current_device():
+        with _elsewhere(index, stream):
+            return mxfp4_quantize_both(x, noise=noise, out=out)
+    shapes = _quantize_shape(x, noise)
+    if out is None:
+        a, b = _rooms(shapes, index)
+    else:
+        a, b = out
+        _check_room(a, shapes[0], index)
+        _check_room(b, shapes[1], index)
+    _quantize(x, noise, a, b, index)
     return a, b
 
 
-@_placed(0, "q")
-def mxfp4_dequantize(q: MXFP4, *, dtype: torch.dtype = torch.bfloat16,
-                     out: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """The values that q stands for (gns_mxfp4_dequantize): exact in fp32 and
-    bf16."""
+def mxfp4_dequantize(q: MXFP4, *, dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None,
+                     stream=None) -> torch.Tensor:
+    """The values that q stands for, in ``dtype`` (bf16 by default) or into
+    ``out`` (gns_mxfp4_dequantize): exact in fp32 and bf16."""
     if not isinstance(q, MXFP4):
         raise GnsError(1, f"q is not an MXFP4: {type(q).__name__}")
+    index = q._index
+    if stream is not None or index != _current_device():
+        with _elsewhere(index, stream):
+            return mxfp4_dequantize(q, dtype=dtype, out=out)
     if out is None:
+        dtype = dtype or torch.bfloat16
+        code = _type_of(dtype)
         out = torch.empty(q.shape, dtype=dtype, device=q.device)
     else:
-        _need("out", out, q.device)
+        _need("out", out, index)
+        code = _type("out", out)
         if out.shape != q.shape or not out.is_contiguous():
             raise GnsError(2, f"out must be contiguous {tuple(q.shape)}")
-    _check(lib().gns_mxfp4_dequantize(q._ref, out.data_ptr(), _type("out", out), _current_raw_stream(q.device.index)))
+        if dtype is not None and out.dtype != dtype:
+            raise GnsError(3, f"out has dtype {out.dtype}, dtype is {dtype}")
+    _check(lib().gns_mxfp4_dequantize(q._ref, out.data_ptr(), code, _current_raw_stream(index)))
     return out
 
 
+@functools.lru_cache(maxsize=1024)
 def mxfp4_matmul_workspace_bytes(batch: int, m: int, n: int, k: int, quantized: bool = True) -> int:
     """Bytes that :func:`mxfp4_matmul` needs for [batch, m, k] by [batch, n, k]
     (``quantized``: whether its first factor is)."""
@@ -334,70 +430,74 @@ def mxfp4_matmul_workspace_bytes(batch: int, m: int, n: int, k: int, quantized: 
     return int((L.gns_mxfp4_matmul_workspace_bytes if quantized else L.gns_mxfp4_linear_workspace_bytes)(batch, m, n, k))
 
 
-@_placed(1, "b")
 def mxfp4_matmul(a: Union[MXFP4, torch.Tensor], b: MXFP4, *, out: Optional[torch.Tensor] = None,
                  dtype: Optional[torch.dtype] = None, accumulate: bool = False,
-                 workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+                 workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """``a @ b^T`` ([m, k] by [n, k], or batches of them), with sums in fp32
     (gns_mxfp4_matmul), in ``dtype`` (a's, or bf16) or into ``out``;
     ``accumulate`` adds to ``out``.  A plain tensor ``a`` is quantised on the
     way (gns_mxfp4_linear); with one matrix b it may have any leading axes."""
     if not isinstance(b, MXFP4):
         raise GnsError(1, f"b is not an MXFP4: {type(b).__name__}")
-    device = b.device
-    n, k = b.shape[-2:]
+    index = b._index
+    if stream is not None or index != _current_device():
+        with _elsewhere(index, stream):
+            return mxfp4_matmul(a, b, out=out, dtype=dtype, accumulate=accumulate, workspace=workspace)
+    batch, n, k = b._dims
+    batched = len(b.shape) == 3
     quantized = isinstance(a, MXFP4)
+    shape = a.shape if quantized else None
     if quantized:
-        _device_tensor("a", a.codes, device)
-        m = a.shape[-2]
-        if a.shape[-1] != k or a.shape[:-2] != b.shape[:-2]:
-            raise GnsError(2, f"a is {tuple(a.shape)}, b {tuple(b.shape)}")
-        shape = (*a.shape[:-1], n)
+        if a._index != index:
+            raise GnsError(1, f"a is on {a.device}, b on {b.device}")
+        if shape[-1] != k or len(shape) != len(b.shape) or a._dims[0] != batch:
+            raise GnsError(2, f"a is {tuple(shape)}, b {tuple(b.shape)}")
+        m = a._dims[1]
     else:
-        _need("a", a, device)
-        if a.dim() == 0 or a.shape[-1] != k or (len(b.shape) == 3 and (a.dim() != 3 or a.shape[0] != b.shape[0])):
-            raise GnsError(2, f"a is {tuple(a.shape)}, b {tuple(b.shape)}")
-        shape = (*a.shape[:-1], n)
+        _need("a", a, index)
+        shape = a.shape
+        if len(shape) == 0 or shape[-1] != k or (batched and (len(shape) != 3 or shape[0] != batch)):
+            raise GnsError(2, f"a is {tuple(shape)}, b {tuple(b.shape)}")
         code = _type("a", a)
-        if len(b.shape) == 3:
-            form = _matrix("a", a)
+        if batched:
+            form = _matrix(a)
             if form is None:
                 raise GnsError(2, f"a: elements of a row must be consecutive (strides {a.stride()})")
             _, m, _, pitch, batch_stride = form
         else:
-            m = 1
-            for s in a.shape[:-1]:
-                m *= s
-            pitch, batch_stride = _rows_of("a", a, a.shape[:-1]), 0
-    batch = b._c.batch
+            m = math.prod(shape[:-1])
+            pitch, batch_stride = _rows_of("a", a, shape[:-1]), 0
+    made = (*shape[:-1], n)
     if out is None:
         if accumulate:
             raise GnsError(1, "accumulate needs out")
-        out = torch.empty(shape, dtype=dtype or (torch.bfloat16 if quantized else a.dtype), device=device)
+        dtype = dtype or (torch.bfloat16 if quantized else a.dtype)
+        out_code, out_pitch, out_stride = _type_of(dtype), n, m * n
+        out = torch.empty(made, dtype=dtype, device=b.device)
     else:
-        _need("out", out, device)
-        if tuple(out.shape) != tuple(shape):
-            raise GnsError(2, f"out has shape {tuple(out.shape)}, the product {tuple(shape)}")
+        _need("out", out, index)
+        out_code = _type("out", out)
+        if tuple(out.shape) != made:
+            raise GnsError(2, f"out has shape {tuple(out.shape)}, the product {made}")
         if dtype is not None and out.dtype != dtype:
             raise GnsError(3, f"out has dtype {out.dtype}, dtype is {dtype}")
-    if len(b.shape) == 3:
-        form = _matrix("out", out)
-        if form is None:
-            raise GnsError(2, f"out: elements of a row must be consecutive (strides {out.stride()})")
-        out_pitch, out_stride = form[3:]
-    else:
-        out_pitch, out_stride = _rows_of("out", out, shape[:-1]), 0
-    L = lib()
+        if batched:
+            form = _matrix(out)
+            if form is None:
+                raise GnsError(2, f"out: elements of a row must be consecutive (strides {out.stride()})")
+            out_pitch, out_stride = form[3:]
+        else:
+            out_pitch, out_stride = _rows_of("out", out, made[:-1]), 0
     if workspace is None:
-        need = (L.gns_mxfp4_matmul_workspace_bytes if quantized else L.gns_mxfp4_linear_workspace_bytes)(batch, m, n, k)
-        ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+        room = mxfp4_matmul_workspace_bytes(batch, m, n, k, quantized)
+        ws = torch.empty(room, dtype=torch.uint8, device=b.device) if room else None
     else:
-        ws = _workspace(0, device, workspace)
-    at, room = (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
-    tail = (out.data_ptr(), _type("out", out), out_pitch, out_stride, 1 if accumulate else 0, at, room,
-            _current_raw_stream(device.index))
+        ws = _workspace(0, b.device, workspace)
+        room = ws.numel() * ws.element_size()
+    tail = (out.data_ptr(), out_code, out_pitch, out_stride, 1 if accumulate else 0,
+            None if ws is None else ws.data_ptr(), room, _current_raw_stream(index))
     if quantized:
-        _check(L.gns_mxfp4_matmul(a._ref, b._ref, *tail))
+        _check(lib().gns_mxfp4_matmul(a._ref, b._ref, *tail))
     else:
-        _check(L.gns_mxfp4_linear(a.data_ptr(), code, pitch, batch_stride, m, b._ref, *tail))
+        _check(lib().gns_mxfp4_linear(a.data_ptr(), code, pitch, batch_stride, m, b._ref, *tail))
     return out
