@@ -284,8 +284,8 @@ __device__ __forceinline__ int64_t first_not_below(const uint32_t *keys, int64_t
 template <int N>
 __global__ void __launch_bounds__(1024)
 token_sort_once(Tokens tokens, int count, uint32_t vocab, int passes, int bits, uint32_t *keys, uint32_t *places,
-                uint32_t *joins, uint32_t *starts) {
-  if (joins && threadIdx.x < 2) joins[threadIdx.x] = 0;
+                uint32_t *joins) {
+  if (threadIdx.x < 2) joins[threadIdx.x] = 0;
   __shared__ uint16_t before[16 << kMaxBits];
   __shared__ uint32_t first[1 << kMaxBits], parts[16];
   __shared__ uint32_t key_at[1024 * N];
@@ -324,10 +324,6 @@ token_sort_once(Tokens tokens, int count, uint32_t vocab, int passes, int bits, 
       place[j] = place_at[mine + 64 * j];
     }
     __syncthreads();
-  }
-  if (starts) {
-    // where each row's tokens begin (key_at holds the sorted keys)
-    for (uint32_t v = tid; v <= vocab; v += 1024) starts[v] = static_cast<uint32_t>(first_not_below(key_at, count, v));
   }
 #pragma unroll
   for (int j = 0; j < N; ++j) {
@@ -578,7 +574,7 @@ __global__ void __launch_bounds__(256) embedding_join(Sums p, typename TW::S *we
     const Columns c(M, i % blocks, lane, lanes, p.width);
     const int64_t from = parts * mine / groups, to = parts * (mine + 1) / groups;
     float acc[kColumns] = {0, 0, 0, 0, 0, 0, 0, 0};
-    constexpr int kAhead = 4;
+    constexpr int kAhead = 8;
     for (int64_t k0 = from; k0 < to; k0 += kAhead) {
       float v[kAhead][kColumns];
 #pragma unroll
@@ -606,15 +602,49 @@ __global__ void __launch_bounds__(256) embedding_join(Sums p, typename TW::S *we
 }
 
 // Few tokens of a small vocabulary: a workgroup per row of the table and
-// kJoinLanes * 8 columns, its groups of threads adding up consecutive parts of
-// the row's tokens, and then theirs in order.  One launch instead of two (4096 x
-// 128 into 256 rows: 15 us with the sort, 21 in pieces).
+// kJoinLanes * 8 columns.  It looks through all tokens itself, each wave
+// through a quarter of them in order, and its groups of threads add up
+// consecutive parts of the row's gradients, and then theirs in order.  One
+// launch and no sort (4096 x 128 into 256 rows: 13 us, against 20 by the
+// way of the others).
+constexpr int kRowTokens = 4096;                       // at most
+constexpr int64_t kRowReads = int64_t(1) << 21;        // tokens read by all workgroups, at most
+constexpr int64_t kRowGroups = 4096;                   // workgroups, at most
+
 template <class TG, class TW, Spread M>
 __global__ void __launch_bounds__(256)
-embedding_row_sums(Sums p, const uint32_t *starts, const typename TG::S *grad, typename TW::S *weight) {
+embedding_row_sums(Tokens tokens, int count, Sums p, const typename TG::S *grad, typename TW::S *weight) {
+  constexpr int kQuarter = kRowTokens / 4;
+  __shared__ uint16_t found[4][kQuarter], list[kRowTokens];
+  __shared__ int found_n[4];
   __shared__ float sums[256][kColumns + 1];
-  const int64_t v = blockIdx.x / p.blocks, begin = starts[v];
-  const int n = static_cast<int>(starts[v + 1] - begin);
+  const uint32_t v = static_cast<uint32_t>(blockIdx.x / p.blocks);
+  {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int quarter = (count + 3) / 4, first = wave * quarter, end = min(first + quarter, count);
+    const uint64_t lower = (uint64_t(1) << lane) - 1;
+    int n = 0;
+    constexpr int kRounds = kQuarter / 64;
+    bool mine[kRounds];
+#pragma unroll
+    for (int k = 0; k < kRounds; ++k) {
+      const int i = first + 64 * k + lane;
+      mine[k] = i < end && tokens.key(i, p.vocab) == v;
+    }
+#pragma unroll
+    for (int k = 0; k < kRounds; ++k) {
+      const uint64_t with = __ballot(mine[k]);
+      if (mine[k]) found[wave][n + __popcll(with & lower)] = static_cast<uint16_t>(first + 64 * k + lane);
+      n += __popcll(with);
+    }
+    if (lane == 0) found_n[wave] = n;
+    __syncthreads();
+    int before = 0;
+    for (int w = 0; w < wave; ++w) before += found_n[w];
+    for (int k = lane; k < n; k += 64) list[before + k] = found[wave][k];
+    __syncthreads();
+  }
+  const int n = found_n[0] + found_n[1] + found_n[2] + found_n[3];
   if (n == 0 && p.accumulate) return;
   const int groups = 256 / p.lanes, lane = threadIdx.x % p.lanes, mine = threadIdx.x / p.lanes;
   const Columns c(M, blockIdx.x % p.blocks, lane, p.lanes, p.width);
@@ -625,7 +655,7 @@ embedding_row_sums(Sums p, const uint32_t *starts, const typename TG::S *grad, t
     float x[kAhead][kColumns];
 #pragma unroll
     for (int a = 0; a < kAhead; ++a)
-      if (i + a < to) load_columns<TG, M>(grad + static_cast<int64_t>(p.places[begin + i + a]) * p.grad_pitch, c, x[a]);
+      if (i + a < to) load_columns<TG, M>(grad + static_cast<int64_t>(list[i + a]) * p.grad_pitch, c, x[a]);
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
       if (i + a >= to) continue;
@@ -641,14 +671,12 @@ embedding_row_sums(Sums p, const uint32_t *starts, const typename TG::S *grad, t
 #pragma unroll
     for (int k = 0; k < kColumns; ++k) acc[k] += sums[g * p.lanes + lane][k];
   }
-  write_row<TW, M>(p, weight, static_cast<uint32_t>(v), c, acc);
+  write_row<TW, M>(p, weight, v, c, acc);
 }
 
 // ---------------------------------------------------------------------------
 // plan of a gradient call
 // ---------------------------------------------------------------------------
-constexpr int64_t kRowGroups = 4096;   // workgroups that go by rows, at most
-
 struct Plan {
   int passes, bits;                  // digits of the sort
   bool many;                         // more than one workgroup's
@@ -656,11 +684,11 @@ struct Plan {
   int64_t tiles;
   int lanes, piece;
   int64_t blocks, pieces;
-  size_t keys, places, keys2, places2, counts, joins, partials, starts, bytes;   // offsets in the workspace
+  size_t keys, places, keys2, places2, counts, joins, partials, bytes;   // offsets in the workspace
 };
 
 Plan plan_of(int64_t count, int64_t vocab, int64_t width) {
-  Plan p;
+  Plan p{};
   int bits = 1;
   while (vocab >> bits) ++bits;      // of 0 .. vocab, padding included
   p.passes = (bits + kMaxBits - 1) / kMaxBits;
@@ -668,12 +696,18 @@ Plan plan_of(int64_t count, int64_t vocab, int64_t width) {
   p.tiles = (count + kTile - 1) / kTile;
   p.many = count > kOnce * 1024;
   p.lanes = lanes_for(width, kJoinLanes);
-  p.by_row = !p.many && vocab * blocks_of(width, p.lanes) <= kRowGroups;
+  p.by_row = count <= kRowTokens &&
+             vocab * blocks_of(width, p.lanes) <= std::min(kRowGroups, kRowReads / std::max<int64_t>(count, 1));
   if (!p.by_row) p.lanes = lanes_for(width);
   p.blocks = blocks_of(width, p.lanes);
-  // pieces of 8 to 64 tokens (a lane each): about 2048 workgroups where there are so many
-  p.piece = static_cast<int>(std::clamp<int64_t>(count * p.blocks * p.lanes / 256 / 2048, 8, 64));
+  // pieces of 8 to 64 tokens (a lane each): about 1024 workgroups where there are so many
+  // (32768 x 4096 tokens: 199 us, with 2048 207)
+  p.piece = static_cast<int>(std::clamp<int64_t>(count * p.blocks * p.lanes / 256 / 1024, 8, 64));
   p.pieces = (count + p.piece - 1) / p.piece;
+  if (p.by_row) {
+    p.bytes = 0;
+    return p;
+  }
   size_t at = 0;
   auto take = [&](size_t n) {
     const size_t here = at;
@@ -685,9 +719,8 @@ Plan plan_of(int64_t count, int64_t vocab, int64_t width) {
   p.keys2 = p.many ? take(4 * count) : 0;
   p.places2 = p.many ? take(4 * count) : 0;
   p.counts = p.many ? take(4 * (p.tiles << p.bits)) : 0;
-  p.starts = p.by_row ? take(4 * (vocab + 1)) : 0;
-  p.joins = p.by_row ? 0 : take(4 * (2 + p.pieces));
-  p.partials = p.by_row ? 0 : take(8 * p.pieces * ((width + 3) / 4 * 4));
+  p.joins = take(4 * (2 + p.pieces));
+  p.partials = take(8 * p.pieces * ((width + 3) / 4 * 4));
   p.bytes = at;
   return p;
 }
@@ -724,11 +757,12 @@ hipError_t launch_embedding_grad(const void *tokens, int token_bits, int64_t cou
   const Tokens t{tokens, token_bits};
   const uint32_t v = static_cast<uint32_t>(vocab);
   uint32_t *keys = words(plan.keys), *places = words(plan.places), *joins = words(plan.joins);
-  if (count > 0 && !plan.many) {
+  if (plan.by_row) {
+    // no sort
+  } else if (!plan.many) {
     token_sort_once<kOnce><<<dim3(1), dim3(1024), 0, s>>>(t, static_cast<int>(count), v, plan.passes, plan.bits, keys,
-                                                         places, plan.by_row ? nullptr : joins,
-                                                         plan.by_row ? words(plan.starts) : nullptr);
-  } else if (count > 0) {
+                                                         places, joins);
+  } else {
     uint32_t *keys2 = words(plan.keys2), *places2 = words(plan.places2), *counts = words(plan.counts);
     for (int pass = 0; pass < plan.passes; ++pass) {
       const uint32_t *from = pass ? keys2 : nullptr;
@@ -758,8 +792,9 @@ hipError_t launch_embedding_grad(const void *tokens, int token_bits, int64_t cou
         using TW = decltype(tw);
         typename TW::S *w = static_cast<typename TW::S *>(grad_weight.data);
         const typename TG::S *g = static_cast<const typename TG::S *>(grad.data);
-        if (plan.by_row && count > 0) {
-          embedding_row_sums<TG, TW, m.value><<<dim3(vocab * plan.blocks), dim3(256), 0, s>>>(p, words(plan.starts), g, w);
+        if (plan.by_row) {
+          embedding_row_sums<TG, TW, m.value>
+              <<<dim3(vocab * plan.blocks), dim3(256), 0, s>>>(t, static_cast<int>(count), p, g, w);
           return hipGetLastError();
         }
         const dim3 grid = grid_of(clear + work);

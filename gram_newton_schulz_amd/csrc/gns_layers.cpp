@@ -183,7 +183,7 @@ gns_status gns_embedding(const void *tokens, int token_bits, int64_t count, cons
 
 size_t gns_embedding_grad_workspace_bytes(int64_t count, int64_t vocab, int64_t width) {
   if (!embedding_size(count, vocab, width)) return 0;
-  return std::max<size_t>(round_256(gns::embedding_grad_bytes(count, vocab, width)), 256);
+  return round_256(gns::embedding_grad_bytes(count, vocab, width));
 }
 
 gns_status gns_embedding_grad(const void *tokens, int token_bits, int64_t count, const void *grad,

@@ -339,29 +339,32 @@ __device__ __forceinline__ i32x8 fp4_operand(uint4 v) {
   return i32x8{static_cast<int>(v.x), static_cast<int>(v.y), static_cast<int>(v.z), static_cast<int>(v.w), 0, 0, 0, 0};
 }
 
-// C = A B^T in tiles of TILE x TILE, with 8 waves (256) in a 4 x 2 grid of 64 x
-// 128 wave tiles or 4 waves (128) in a 2 x 2 grid of 64 x 64.  An MFMA
-// multiplies 32 x 64 codes by 32 x 64: lane l holds one block of 32 codes of
-// row l % 32 of either factor, 16 bytes, and its scale.  A stage of the
-// contraction is 128 columns: 64 bytes of codes of every row, as four 16-byte
-// chunks, and one word of scales of every row.  Both come from HBM or L2
-// straight into LDS (LDS-DMA) into a ring of four stages.  The fragments of B
-// are the instruction's rows, so that a lane's accumulators are runs of four
-// consecutive columns of C.
-template <int TILE>
+// C = A B^T in tiles of TM x TN by WGM x WGN waves.  An MFMA multiplies 32 x 64
+// codes by 32 x 64: lane l holds one block of 32 codes of row l % 32 of either
+// factor, 16 bytes, and its scale.  A stage of the contraction is 128 columns:
+// 64 bytes of codes of every row, as four 16-byte chunks, and one word of
+// scales of every row.  Both come from HBM or L2 straight into LDS (LDS-DMA)
+// into a ring of stages.  The fragments of B are the instruction's rows, so
+// that a lane's accumulators are runs of four consecutive columns of C.
+template <int TM_, int TN_, int WGM_, int WGN_, int STAGES_>
 struct MxTile {
-  static constexpr int WGM = TILE == 256 ? 4 : 2, WGN = 2;       // waves along rows, columns
+  static constexpr int TM = TM_, TN = TN_, WGM = WGM_, WGN = WGN_, STAGES = STAGES_;
   static constexpr int NW = WGM * WGN, THREADS = 64 * NW;
-  static constexpr int WTM = TILE / WGM, WTN = TILE / WGN;
+  static constexpr int WTM = TM / WGM, WTN = TN / WGN;
   static constexpr int NBM = WTM / 32, NBN = WTN / 32;           // 32 x 32 blocks of a wave
-  static constexpr int CODES = TILE * 64;                        // bytes of one factor's codes in a stage
-  static constexpr int PIECES = TILE / 32;                       // 128-byte pieces of one factor's scales
-  static constexpr int STAGE = 2 * CODES + 2 * PIECES * 128;
-  static constexpr int STAGES = 4;
-  static constexpr int CODE_LOADS = TILE / 16 / NW;              // of 1 KiB, per wave and factor
-  static constexpr int LOADS = 2 * CODE_LOADS + 1;               // of a wave per stage
-  static_assert(CODE_LOADS * NW * 16 == TILE && 2 * NW == 2 * PIECES, "the waves' loads cover a stage");
-  static_assert(STAGES * STAGE <= 160 * 1024, "LDS");
+  static constexpr int CODES_A = TM * 64, CODES_B = TN * 64;     // bytes of codes in a stage
+  static constexpr int PIECES_A = TM / 32, PIECES_B = TN / 32;   // 128-byte pieces of scales
+  static constexpr int STAGE = CODES_A + CODES_B + (PIECES_A + PIECES_B) * 128;
+  static constexpr int LDS = STAGES * STAGE;
+  static constexpr int LOADS_A = TM / 16 / NW, LOADS_B = TN / 16 / NW;         // of 1 KiB, per wave
+  static constexpr int PAIRS = (PIECES_A + PIECES_B) / 2;                      // of pieces: a load of scales each
+  static constexpr int LOADS_S = (PAIRS + NW - 1) / NW;
+  static constexpr int LOADS = LOADS_A + LOADS_B + LOADS_S;      // of a wave per stage
+  // rows of results that go through LDS at a time, as fp32
+  static constexpr int ROWS_F32 = TM * (TN + 4) * 4 <= LDS ? TM : TM / 2 * (TN + 4) * 4 <= LDS ? TM / 2 : TM / 4;
+  static_assert(LOADS_A * NW * 16 == TM && LOADS_B * NW * 16 == TN && PIECES_A % 2 == 0, "whole loads");
+  static_assert(LDS <= 160 * 1024 && ROWS_F32 % 32 == 0 && ROWS_F32 * (TN + 4) * 4 <= LDS, "LDS");
+  static_assert(TM * (TN + 8) * 2 <= LDS, "LDS");
 };
 
 struct MxGemm {
@@ -370,7 +373,7 @@ struct MxGemm {
   int tiles_m, tiles_n;
   int run;             // consecutive tiles dealt to one XCD
   int parts;           // of the contraction
-  int64_t part_stride; // elements of o from one part's results to the next's
+  int64_t part_stride; // elements from one part's results to the next's
 };
 
 // chunk c of row r lies at chunk c ^ swizzle(r): rows that share a bank have
@@ -384,11 +387,10 @@ __device__ __forceinline__ i32x4 buffer_of(const uint8_t *at, int64_t bytes) {
                __builtin_amdgcn_readfirstlane(static_cast<int>(bytes)), 0x00020000};
 }
 
-template <class TO, int TILE>
-__global__ void __launch_bounds__((MxTile<TILE>::THREADS)) mx_gemm(MxGemm p) {
-  using L = MxTile<TILE>;
+template <class TO, class L>
+__global__ void __launch_bounds__((L::THREADS)) mx_gemm(MxGemm p) {
   using S = typename TO::S;
-  __shared__ __attribute__((aligned(16))) unsigned char lds[L::STAGES * L::STAGE];
+  __shared__ __attribute__((aligned(16))) unsigned char lds[L::LDS];
 
   // Workgroup -> tile: runs of tiles go to the XCDs in turn (workgroups do one
   // by one), and within a run 4 x 8 tiles share their panels.
@@ -423,15 +425,16 @@ __global__ void __launch_bounds__((MxTile<TILE>::THREADS)) mx_gemm(MxGemm p) {
   const int stages = min(groups - first, per_part);
 
   // this tile's rows of codes and scales; what lies past the last row reads as zero
-  auto panel = [&](const MxMatrix &q, int tile, i32x4 *codes, i32x4 *scales) {
-    const int64_t row = static_cast<int64_t>(tile) * TILE, blocks = q.row_blocks();
-    *codes = buffer_of(q.codes + (mat * q.rows + row) * pitch, min<int64_t>(TILE, q.rows - row) * pitch);
+  auto panel = [&](const MxMatrix &q, int64_t row, int high, i32x4 *codes, i32x4 *scales) {
+    const int64_t blocks = q.row_blocks();
+    *codes = buffer_of(q.codes + (mat * q.rows + row) * pitch, min<int64_t>(high, q.rows - row) * pitch);
     *scales = buffer_of(q.scales + (mat * blocks + row / 32) * groups * 128,
-                        min<int64_t>(L::PIECES, blocks - row / 32) * groups * 128);
+                        min<int64_t>(high / 32, blocks - row / 32) * groups * 128);
   };
+  const int64_t row0 = static_cast<int64_t>(ti) * L::TM, col0 = static_cast<int64_t>(tj) * L::TN;
   i32x4 ca, cb, sa, sb;
-  panel(p.a, ti, &ca, &sa);
-  panel(p.b, tj, &cb, &sb);
+  panel(p.a, row0, L::TM, &ca, &sa);
+  panel(p.b, col0, L::TN, &cb, &sb);
   const uint32_t lds_base =
       static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) unsigned char *)(lds)));
 
@@ -440,30 +443,41 @@ __global__ void __launch_bounds__((MxTile<TILE>::THREADS)) mx_gemm(MxGemm p) {
   const int dma_row = lane >> 2;
   const int code_at = dma_row * pitch + ((lane & 3) ^ swizzle(dma_row)) * 16;
   const int scale_at = lh * groups * 128 + lr * 4;
-  const bool scales_of_a = wave < L::NW / 2;
-  const int scale_piece = 2 * (scales_of_a ? wave : wave - L::NW / 2);
-  const i32x4 sx = scales_of_a ? sa : sb;
-  auto fetch = [&](int stage) {
+  auto fetch = [&](int stage, int slot) {
     // stages past the last one go through an empty range: every stage has the
     // same number of loads, and these fetch nothing
     const bool live = stage < stages;
     const int at = first + (live ? stage : 0);
-    const uint32_t to = lds_base + static_cast<uint32_t>((stage % L::STAGES) * L::STAGE);
-    i32x4 a = ca, b = cb, x = sx;
-    if (!live) a[2] = b[2] = x[2] = 0;
+    const uint32_t to = lds_base + static_cast<uint32_t>(slot * L::STAGE);
+    i32x4 a = ca, b = cb;
+    if (!live) a[2] = b[2] = 0;
 #pragma unroll
-    for (int q = 0; q < L::CODE_LOADS; ++q) {
-      const int blk = wave + q * L::NW, from = blk * 16 * pitch + at * 64;
+    for (int q = 0; q < L::LOADS_A; ++q) {
+      const int blk = wave + q * L::NW;
       asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(to + blk * 1024), "v"(code_at),
-                   "s"(a), "s"(from)
-                   : "memory", "m0");
-      asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(to + L::CODES + blk * 1024),
-                   "v"(code_at), "s"(b), "s"(from)
+                   "s"(a), "s"(blk * 16 * pitch + at * 64)
                    : "memory", "m0");
     }
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(to + 2 * L::CODES + wave * 256),
-                 "v"(scale_at), "s"(x), "s"(scale_piece * groups * 128 + at * 128)
-                 : "memory", "m0");
+#pragma unroll
+    for (int q = 0; q < L::LOADS_B; ++q) {
+      const int blk = wave + q * L::NW;
+      asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(to + L::CODES_A + blk * 1024),
+                   "v"(code_at), "s"(b), "s"(blk * 16 * pitch + at * 64)
+                   : "memory", "m0");
+    }
+#pragma unroll
+    for (int q = 0; q < L::LOADS_S; ++q) {
+      // (a wave with no pair left repeats the last one: the same bytes to the same place)
+      const int pair = min(wave + q * L::NW, L::PAIRS - 1);
+      const bool of_a = pair < L::PIECES_A / 2;
+      i32x4 x = of_a ? sa : sb;
+      if (!live) x[2] = 0;
+      const int piece = 2 * pair - (of_a ? 0 : L::PIECES_A);
+      asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+                   ::"s"(to + L::CODES_A + L::CODES_B + pair * 256), "v"(scale_at), "s"(x),
+                   "s"(piece * groups * 128 + at * 128)
+                   : "memory", "m0");
+    }
   };
 
   f32x16 acc[L::NBN][L::NBM];
@@ -489,15 +503,15 @@ __global__ void __launch_bounds__((MxTile<TILE>::THREADS)) mx_gemm(MxGemm p) {
         fa[s][i] = *reinterpret_cast<const uint4 *>(at + (wr + 32 * i + lr) * 64 + chunk);
 #pragma unroll
       for (int j = 0; j < L::NBN; ++j)
-        fb[s][j] = *reinterpret_cast<const uint4 *>(at + L::CODES + (wc + 32 * j + lr) * 64 + chunk);
+        fb[s][j] = *reinterpret_cast<const uint4 *>(at + L::CODES_A + (wc + 32 * j + lr) * 64 + chunk);
     }
-    const unsigned char *words = at + 2 * L::CODES + lr * 4;
+    const unsigned char *words = at + L::CODES_A + L::CODES_B + lr * 4;
 #pragma unroll
     for (int i = 0; i < L::NBM; ++i)
       xa[i] = *reinterpret_cast<const uint32_t *>(words + (wr / 32 + i) * 128) >> (8 * lh);
 #pragma unroll
     for (int j = 0; j < L::NBN; ++j)
-      xb[j] = *reinterpret_cast<const uint32_t *>(words + (L::PIECES + wc / 32 + j) * 128) >> (8 * lh);
+      xb[j] = *reinterpret_cast<const uint32_t *>(words + (L::PIECES_A + wc / 32 + j) * 128) >> (8 * lh);
   };
   auto multiply = [&]() {
 #pragma unroll
@@ -515,51 +529,53 @@ __global__ void __launch_bounds__((MxTile<TILE>::THREADS)) mx_gemm(MxGemm p) {
   };
 
 #pragma unroll
-  for (int i = 0; i < L::STAGES - 1; ++i) fetch(i);
+  for (int i = 0; i < L::STAGES - 1; ++i) fetch(i, i);
   constexpr int kWait = L::LOADS * (L::STAGES - 2);      // this wave's loads of later stages
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kWait) : "memory");
   __syncthreads();
+  // Stage i + STAGES - 1 goes to the place of stage i - 1, which every wave has
+  // finished reading.
+  int slot = 0, next = L::STAGES - 1;
   if constexpr (L::NW == 8) {
     // The two waves of a SIMD are one barrier apart: one multiplies while the
-    // other reads.  Stage i + 3 goes to the place of stage i - 1, which both
-    // have finished reading.
+    // other reads.
     const bool second = wave >= 4;
     if (second) __syncthreads();
     for (int i = 0; i < stages; ++i) {
-      read(i % L::STAGES);
-      fetch(i + L::STAGES - 1);
+      read(slot);
+      fetch(i + L::STAGES - 1, next);
       asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kWait) : "memory");
       __syncthreads();
       __builtin_amdgcn_s_setprio(1);
       multiply();
       __builtin_amdgcn_s_setprio(0);
       __syncthreads();
+      next = slot;
+      slot = slot == L::STAGES - 1 ? 0 : slot + 1;
     }
     if (!second) __syncthreads();
   } else {
     for (int i = 0; i < stages; ++i) {
-      read(i % L::STAGES);
-      fetch(i + L::STAGES - 1);
+      read(slot);
+      fetch(i + L::STAGES - 1, next);
       multiply();
       asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kWait) : "memory");
       __syncthreads();
+      next = slot;
+      slot = slot == L::STAGES - 1 ? 0 : slot + 1;
     }
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
   // Results go through LDS, so that the workgroup stores whole rows, 16 bytes
-  // per thread.  Rounded first where they are stored as they are; as fp32
-  // where they are added to what is there, half a tile of 256 at a time.
+  // per thread (which need no alignment beyond the element's).  Rounded first
+  // where they are stored as they are; as fp32, a part of the rows at a time,
+  // where they are added to what is there.
   S *const out = static_cast<S *>(p.o.out) + part * p.part_stride + mat * p.o.batch_stride;
-  const int64_t row0 = static_cast<int64_t>(ti) * TILE, col0 = static_cast<int64_t>(tj) * TILE;
   const int64_t rows = p.a.rows, cols = p.b.rows;
-  const bool whole_words = p.o.pitch * sizeof(S) % 16 == 0 && p.o.batch_stride * sizeof(S) % 16 == 0 &&
-                           reinterpret_cast<uintptr_t>(p.o.out) % 16 == 0;
-  constexpr int kPer = 16 / sizeof(S);                   // elements of 16 bytes
   if constexpr (sizeof(S) == 2) {
     if (!p.o.accumulate) {
-      constexpr int kPitch = TILE + 8;
-      static_assert(TILE * kPitch * 2 <= L::STAGES * L::STAGE, "LDS");
+      constexpr int kPitch = L::TN + 8;
       S *const staged = reinterpret_cast<S *>(lds);
       __syncthreads();
 #pragma unroll
@@ -572,59 +588,91 @@ __global__ void __launch_bounds__((MxTile<TILE>::THREADS)) mx_gemm(MxGemm p) {
                 make_uint2(TO::st2(acc[j][i][4 * g], acc[j][i][4 * g + 1]),
                            TO::st2(acc[j][i][4 * g + 2], acc[j][i][4 * g + 3]));
       __syncthreads();
-      for (int k = tid; k < TILE * TILE / kPer; k += L::THREADS) {
-        const int r = k / (TILE / kPer), c = k % (TILE / kPer) * kPer;
+#pragma unroll 4
+      for (int k = tid; k < L::TM * L::TN / 8; k += L::THREADS) {
+        const int r = k / (L::TN / 8), c = k % (L::TN / 8) * 8;
         const int64_t row = row0 + r, col = col0 + c;
         if (row >= rows || col >= cols) continue;
         const S *from = staged + r * kPitch + c;
         S *to = out + row * p.o.pitch + col;
-        if (whole_words && col + kPer <= cols) {
-          *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<const uint4 *>(from);
+        if (col + 8 <= cols) {
+          const uint4 v = *reinterpret_cast<const uint4 *>(from);
+          __builtin_memcpy(to, &v, 16);
         } else {
-          for (int e = 0; e < kPer && col + e < cols; ++e) to[e] = from[e];
+          for (int e = 0; col + e < cols; ++e) to[e] = from[e];
         }
       }
       return;
     }
   }
-  constexpr int kHalves = TILE / 128, kPitch = TILE + 4;
-  static_assert(128 * kPitch * 4 <= L::STAGES * L::STAGE, "LDS");
+  constexpr int kPitch = L::TN + 4, kRows = L::ROWS_F32;
   float *const staged = reinterpret_cast<float *>(lds);
-  for (int half = 0; half < kHalves; ++half) {
+#pragma unroll
+  for (int r0 = 0; r0 < L::TM; r0 += kRows) {
     __syncthreads();
-    if (wr / 128 == half) {
+#pragma unroll
+    for (int i = 0; i < L::NBM; ++i) {
+      if ((wr + 32 * i) / kRows != r0 / kRows) continue;
 #pragma unroll
       for (int j = 0; j < L::NBN; ++j)
 #pragma unroll
-        for (int i = 0; i < L::NBM; ++i)
-#pragma unroll
-          for (int g = 0; g < 4; ++g)
-            *reinterpret_cast<float4 *>(staged + (wr % 128 + 32 * i + lr) * kPitch + wc + 32 * j + 8 * g + 4 * lh) =
-                make_float4(acc[j][i][4 * g], acc[j][i][4 * g + 1], acc[j][i][4 * g + 2], acc[j][i][4 * g + 3]);
+        for (int g = 0; g < 4; ++g)
+          *reinterpret_cast<float4 *>(staged + (wr + 32 * i - r0 + lr) * kPitch + wc + 32 * j + 8 * g + 4 * lh) =
+              make_float4(acc[j][i][4 * g], acc[j][i][4 * g + 1], acc[j][i][4 * g + 2], acc[j][i][4 * g + 3]);
     }
     __syncthreads();
-    for (int k = tid; k < 128 * TILE / 4; k += L::THREADS) {
-      const int r = k / (TILE / 4), c = k % (TILE / 4) * 4;
-      const int64_t row = row0 + 128 * half + r, col = col0 + c;
+#pragma unroll 8
+    for (int k = tid; k < kRows * L::TN / 4; k += L::THREADS) {
+      const int r = k / (L::TN / 4), c = k % (L::TN / 4) * 4;
+      const int64_t row = row0 + r0 + r, col = col0 + c;
       if (row >= rows || col >= cols) continue;
       const float4 v = *reinterpret_cast<const float4 *>(staged + r * kPitch + c);
+      float x[4] = {v.x, v.y, v.z, v.w};
       S *to = out + row * p.o.pitch + col;
-      if (sizeof(S) == 4 && whole_words && col + 4 <= cols) {
-        float4 *at = reinterpret_cast<float4 *>(to);
-        float4 sum = v;
+      if (col + 4 <= cols) {
         if (p.o.accumulate) {
-          const float4 old = *at;
-          sum = make_float4(old.x + v.x, old.y + v.y, old.z + v.z, old.w + v.w);
-        }
-        *at = sum;
-      } else {
-        const float e4[4] = {v.x, v.y, v.z, v.w};
+          S old[4];
+          __builtin_memcpy(old, to, sizeof(old));
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (col + e < cols) to[e] = TO::st(p.o.accumulate ? TO::ld(to[e]) + e4[e] : e4[e]);
+          for (int e = 0; e < 4; ++e) x[e] += TO::ld(old[e]);
+        }
+        S sum[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[e] = TO::st(x[e]);
+        __builtin_memcpy(to, sum, sizeof(sum));
+      } else {
+        {
+#pragma unroll
+          for (int e = 0; e < 3; ++e)
+            if (col + e < cols) to[e] = TO::st(p.o.accumulate ? TO::ld(to[e]) + x[e] : x[e]);
+        }
       }
     }
   }
+}
+
+// out (+)= the sum of the parts of a contraction, in order; four columns per thread.
+template <class TO>
+__global__ void __launch_bounds__(256)
+mx_join(const float *parts, int n_parts, int64_t part_stride, int64_t rows_all, int64_t m, int64_t n, int64_t pitch,
+        MxOutput o) {
+  using S = typename TO::S;
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, row = at / (pitch / 4),
+                col = (at - row * (pitch / 4)) * 4;
+  if (row >= rows_all) return;
+  const float *from = parts + row * pitch + col;
+  float4 sum = *reinterpret_cast<const float4 *>(from);
+#pragma unroll 4
+  for (int k = 1; k < n_parts; ++k) {
+    const float4 v = *reinterpret_cast<const float4 *>(from + k * part_stride);
+    sum = make_float4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w);
+  }
+  const int64_t mat = row / m;
+  S *to = static_cast<S *>(o.out) + mat * o.batch_stride + (row - mat * m) * o.pitch + col;
+  const float x[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (col + e < n) to[e] = TO::st(o.accumulate ? TO::ld(to[e]) + x[e] : x[e]);
 }
 
 // Few rows of A, as when single tokens are answered: what counts is reading B
@@ -784,7 +832,44 @@ hipError_t launch_mx_dequantize(const MxMatrix &q, void *out, int dtype, hipStre
   });
 }
 
-size_t mx_matmul_bytes(int64_t, int64_t, int64_t, int64_t) { return 0; }
+// How a product of more than kThinRows rows runs.
+struct MxPlan {
+  enum Tile { T256, T128, T64 } tile;
+  int parts;                  // of the contraction
+};
+
+MxPlan mx_plan(int64_t batch, int64_t m, int64_t n, int64_t k) {
+  auto tiles = [&](int64_t tm, int64_t tn) { return batch * ((m + tm - 1) / tm) * ((n + tn - 1) / tn); };
+  // Few rows of A take a tile that wastes less of them, if it fills the GPU
+  // (64 matrices of 48 x 7168 by 2048 x 7168: 109 us, against 118 with 256 x 256).
+  if (m <= 64 && tiles(64, 256) >= 256) return {MxPlan::T64, 1};
+  if (tiles(256, 256) >= 192) return {MxPlan::T256, 1};
+  // Where tiles of 128 leave compute units idle, a long contraction may be cut
+  // into parts.  A stage takes 0.27 us of a workgroup; joining the parts takes a
+  // launch, 5 us, and their results written and read at about 5 TB/s.  (48 x
+  // 16384 by 4096 x 16384: 41.5 us whole, 22.4 in 16 parts; 1500 x 5000 by 1500 x
+  // 5000: 26 whole, 33 in three.)
+  const int64_t t = tiles(128, 128), stages = (k + kMxGroup - 1) / kMxGroup;
+  int parts = 1;
+  double best = 0.27 * stages;
+  for (int p = 2; p <= 16 && t * p <= 512 && p <= stages; p *= 2) {
+    const double us = 0.27 * stages / p + 5.0 + static_cast<double>(p) * batch * m * n * 8.0 / 5e6;
+    if (us < best) {
+      best = us;
+      parts = p;
+    }
+  }
+  const int64_t each = (stages + parts - 1) / parts;       // (no part without stages)
+  return {MxPlan::T128, parts == 1 ? 1 : static_cast<int>((stages + each - 1) / each)};
+}
+
+int64_t join_pitch(int64_t n) { return (n + 3) / 4 * 4; }
+
+size_t mx_matmul_bytes(int64_t batch, int64_t m, int64_t n, int64_t k) {
+  if (m <= kThinRows) return 0;
+  const int parts = mx_plan(batch, m, n, k).parts;
+  return parts > 1 ? static_cast<size_t>(parts) * batch * m * join_pitch(n) * 4 : 0;
+}
 
 bool mx_linear_quantizes(int64_t m, int64_t k) { return m <= 16 && m * ((k + kMxGroup - 1) / kMxGroup) * kMxGroup <= kThinValues; }
 
@@ -795,32 +880,41 @@ hipError_t launch_mx_linear(const MxInput &in, int64_t m, const MxMatrix &w, con
   });
 }
 
-hipError_t launch_mx_matmul(const MxMatrix &a, const MxMatrix &b, const MxOutput &out, void *, hipStream_t s) {
-  if (a.rows <= kThinRows)
-    return with_type(out.dtype, [&](auto t) {
-      using T = decltype(t);
-      const MxThin p{a, b, out, nullptr, 0, 0};
-      return a.rows <= 16 ? run_thin<EF32, T, 1, false>(p, s) : run_thin<EF32, T, 2, false>(p, s);
-    });
+template <class T, class L>
+hipError_t run_gemm(const MxMatrix &a, const MxMatrix &b, const MxOutput &out, int parts, hipStream_t s) {
+  MxGemm p{a, b, out, static_cast<int>((a.rows + L::TM - 1) / L::TM), static_cast<int>((b.rows + L::TN - 1) / L::TN), 1,
+           parts, a.batch * out.batch_stride};
+  const int64_t tiles = a.batch * p.tiles_m * p.tiles_n * parts;
+  // runs of up to 32 tiles, in whole runs per XCD
+  const int64_t each = tiles / 8;
+  for (int r = 32; r > 1; --r)
+    if (each % r == 0 && each > 0) {
+      p.run = r;
+      break;
+    }
+  mx_gemm<T, L><<<dim3(tiles), dim3(L::THREADS), 0, s>>>(p);
+  return hipGetLastError();
+}
+
+hipError_t launch_mx_matmul(const MxMatrix &a, const MxMatrix &b, const MxOutput &out, void *workspace, hipStream_t s) {
   return with_type(out.dtype, [&](auto t) {
     using T = decltype(t);
-    auto run = [&](auto tile) {
-      constexpr int TILE = decltype(tile)::value;
-      MxGemm p{a, b, out, static_cast<int>((a.rows + TILE - 1) / TILE), static_cast<int>((b.rows + TILE - 1) / TILE),
-               1, 1, 0};
-      const int64_t tiles = a.batch * p.tiles_m * p.tiles_n;
-      // runs of up to 32 tiles, in whole runs per XCD
-      const int64_t each = tiles / 8;
-      for (int r = 32; r > 1; --r)
-        if (each % r == 0 && each > 0) {
-          p.run = r;
-          break;
-        }
-      mx_gemm<T, TILE><<<dim3(tiles), dim3(MxTile<TILE>::THREADS), 0, s>>>(p);
-      return hipGetLastError();
-    };
-    const int64_t big = a.batch * ((a.rows + 255) / 256) * ((b.rows + 255) / 256);
-    return big >= 192 ? run(std::integral_constant<int, 256>{}) : run(std::integral_constant<int, 128>{});
+    if (a.rows <= kThinRows) {
+      const MxThin p{a, b, out, nullptr, 0, 0};
+      return a.rows <= 16 ? run_thin<EF32, T, 1, false>(p, s) : run_thin<EF32, T, 2, false>(p, s);
+    }
+    const MxPlan plan = mx_plan(a.batch, a.rows, b.rows, a.cols);
+    if (plan.tile == MxPlan::T64) return run_gemm<T, MxTile<64, 256, 1, 4, 3>>(a, b, out, 1, s);
+    if (plan.tile == MxPlan::T256) return run_gemm<T, MxTile<256, 256, 4, 2, 4>>(a, b, out, 1, s);
+    if (plan.parts == 1) return run_gemm<T, MxTile<128, 128, 2, 2, 4>>(a, b, out, 1, s);
+    const int64_t pitch = join_pitch(b.rows);
+    const MxOutput each{workspace, DT_F32, pitch, a.rows * pitch, false};
+    const hipError_t e = run_gemm<EF32, MxTile<128, 128, 2, 2, 4>>(a, b, each, plan.parts, s);
+    if (e != hipSuccess) return e;
+    const int64_t rows = a.batch * a.rows;
+    mx_join<T><<<dim3((rows * (pitch / 4) + 255) / 256), dim3(256), 0, s>>>(
+        static_cast<const float *>(workspace), plan.parts, rows * pitch, rows, a.rows, b.rows, pitch, out);
+    return hipGetLastError();
   });
 }
 

@@ -187,14 +187,14 @@ def embedding_grad(tokens: torch.Tensor, grad: torch.Tensor, grad_weight: torch.
         raise GnsError(2, f"grad has shape {tuple(grad.shape)}, rows of grad_weight have {width}")
     grad_pitch, count = _rows_of("grad", grad, tokens.shape), tokens.numel()
     if workspace is None:
-        need = embedding_grad_workspace_bytes(count, vocab, width)
-        ws = torch.empty(need, dtype=torch.uint8, device=tokens.device)
+        room = embedding_grad_workspace_bytes(count, vocab, width)
+        ws = torch.empty(room, dtype=torch.uint8, device=tokens.device) if room else None
     else:
         ws = _workspace(0, tokens.device, workspace)
-        need = ws.numel() * ws.element_size()
+        room = ws.numel() * ws.element_size()
     _check(lib().gns_embedding_grad(tokens.data_ptr(), bits, count, grad.data_ptr(), _type("grad", grad), grad_pitch,
                                     vocab, width, float(scale), grad_weight.data_ptr(), code, pitch, 1 if accumulate else 0,
-                                    ws.data_ptr(), need, _current_raw_stream(index)))
+                                    None if ws is None else ws.data_ptr(), room, _current_raw_stream(index)))
     return grad_weight
 
 

@@ -581,7 +581,8 @@ gns_status gns_embedding(const void *tokens, int token_bits, int64_t count, cons
  * an order that depends on the tokens alone: the result is the same in every
  * run.
  *   workspace    (device) >= gns_embedding_grad_workspace_bytes(count, vocab,
- *                width) bytes, 256-byte aligned, clobbered.
+ *                width) bytes, 256-byte aligned, clobbered; may be NULL where
+ *                that is 0.
  */
 size_t gns_embedding_grad_workspace_bytes(int64_t count, int64_t vocab, int64_t width);
 gns_status gns_embedding_grad(const void *tokens, int token_bits, int64_t count, const void *grad,
@@ -678,7 +679,8 @@ gns_status gns_mxfp4_matmul(const gns_mxfp4 *a, const gns_mxfp4 *b, void *out, g
  *   x            (device) [w.batch][m][w.cols] in dtype, as for
  *                gns_mxfp4_quantize.
  *   workspace    (device) >= gns_mxfp4_linear_workspace_bytes(w.batch, m,
- *                w.rows, w.cols) bytes, 256-byte aligned, clobbered.
+ *                w.rows, w.cols) bytes, 256-byte aligned, clobbered; may be NULL
+ *                where that is 0 (few rows are quantised by the product itself).
  */
 size_t gns_mxfp4_linear_workspace_bytes(int64_t batch, int64_t m, int64_t n, int64_t k);
 gns_status gns_mxfp4_linear(const void *x, gns_dtype dtype, int64_t pitch, int64_t batch_stride, int64_t m,
