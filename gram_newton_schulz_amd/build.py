@@ -71,7 +71,7 @@ def scratch_users(report: str) -> list:
     for line in report.splitlines():
         if "Function Name:" in line:
             name = line.split("Function Name:")[1].split("[")[0].strip()
-        elif name and "gemm_nt" in name and ("ScratchSize [bytes/lane]:" in line or "VGPRs Spill:" in line
+        elif name and ("gemm_nt" in name or "mx_gemm" in name) and ("ScratchSize [bytes/lane]:" in line or "VGPRs Spill:" in line
                                                or "SGPRs Spill:" in line):
             val = int(line.split(":")[-1].split("[")[0].strip())
             if val > 0 and name not in out:

@@ -269,9 +269,9 @@ struct MxOutput {
 hipError_t launch_mx_quantize(const MxInput &in, int64_t batch, int64_t rows, int64_t cols, const MxMatrix &by_rows,
                               const MxMatrix &by_columns, hipStream_t s);
 hipError_t launch_mx_dequantize(const MxMatrix &q, void *out, int dtype, hipStream_t s);
-// Whether Q(x) w^T of m rows of k values is one launch, launch_mx_linear; else
-// x is quantised first.
-bool mx_linear_quantizes(int64_t m, int64_t k);
+// Whether Q(x) w^T of [batch][m][k] by [batch][n][k] is one launch,
+// launch_mx_linear; else x is quantised first.
+bool mx_linear_quantizes(int64_t batch, int64_t m, int64_t n, int64_t k);
 hipError_t launch_mx_linear(const MxInput &in, int64_t m, const MxMatrix &w, const MxOutput &out, hipStream_t s);
 size_t mx_matmul_bytes(int64_t batch, int64_t m, int64_t n, int64_t k);
 hipError_t launch_mx_matmul(const MxMatrix &a, const MxMatrix &b, const MxOutput &out, void *workspace, hipStream_t s);

@@ -148,7 +148,7 @@ size_t round_256(size_t n) { return (n + 255) & ~size_t(255); }
 
 gns_status product(const MxMatrix &a, const MxMatrix &b, const gns::MxOutput &o, void *workspace, hipStream_t s) {
   const double m = a.rows, n = b.rows, each = gns::dtype_size(o.dtype);
-  LaunchScope ls(s, "mxfp4_matmul", "mx_matmul", 2.0 * a.batch * m * n * a.cols,
+  LaunchScope ls(s, "mxfp4_matmul", "mx_gemm", 2.0 * a.batch * m * n * a.cols,
                  mx_bytes(a) + mx_bytes(b) + a.batch * m * n * each * (o.accumulate ? 2 : 1));
   const hipError_t e = gns::launch_mx_matmul(a, b, o, workspace, s);
   ls.done();
@@ -207,7 +207,7 @@ gns_status gns_embedding_grad(const void *tokens, int token_bits, int64_t count,
     if (meet(written, r) || meet(scratch, r)) return GNS_E_ALIAS;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const double n = static_cast<double>(count) * width;
-  LaunchScope ls(s, "embedding_grad", "token_sort+embedding_sums", n,
+  LaunchScope ls(s, "embedding_grad", "embedding_sums", n,
                  n * ge + static_cast<double>(accumulate ? 2 * std::min(count, vocab) : vocab) * width * we);
   const hipError_t e = gns::launch_embedding_grad(
       tokens, token_bits, count, gns::TokenRows{const_cast<void *>(grad), grad_dtype, grad_pitch}, vocab, width,
@@ -315,7 +315,7 @@ gns_status gns_mxfp4_matmul(const gns_mxfp4 *a, const gns_mxfp4 *b, void *out, g
 
 size_t gns_mxfp4_linear_workspace_bytes(int64_t batch, int64_t m, int64_t n, int64_t k) {
   if (!mx_size(batch, m, k) || !mx_size(batch, n, k) || !grid_fits(batch, m, n)) return 0;
-  if (gns::mx_linear_quantizes(m, k)) return 0;
+  if (gns::mx_linear_quantizes(batch, m, n, k)) return 0;
   return round_256(gns_mxfp4_code_bytes(batch, m, k)) + round_256(gns_mxfp4_scale_bytes(batch, m, k)) +
          gns_mxfp4_matmul_workspace_bytes(batch, m, n, k);
 }
@@ -350,7 +350,7 @@ gns_status gns_mxfp4_linear(const void *x, gns_dtype dtype, int64_t pitch, int64
     if (meet(written, r) || meet(scratch, r)) return GNS_E_ALIAS;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const gns::MxInput in{x, dtype, pitch, batch_stride, nullptr};
-  if (gns::mx_linear_quantizes(m, k)) {
+  if (gns::mx_linear_quantizes(batch, m, n, k)) {
     const double each = static_cast<double>(batch) * m;
     LaunchScope ls(s, "mxfp4_matmul", "mx_thin", 2.0 * each * n * k,
                    each * k * elem + mx_bytes(mw) + each * n * gns::dtype_size(out_dtype) * (accumulate ? 2 : 1));

@@ -832,7 +832,7 @@ hipError_t launch_mx_dequantize(const MxMatrix &q, void *out, int dtype, hipStre
   });
 }
 
-// How a product of more than kThinRows rows runs.
+// How a product runs that mx_thin does not take.
 struct MxPlan {
   enum Tile { T256, T128, T64 } tile;
   int parts;                  // of the contraction
@@ -865,13 +865,20 @@ MxPlan mx_plan(int64_t batch, int64_t m, int64_t n, int64_t k) {
 
 int64_t join_pitch(int64_t n) { return (n + 3) / 4 * 4; }
 
+// (a grid holds 2^24 workgroups of 256 threads)
+bool thin(int64_t batch, int64_t m, int64_t n) {
+  return m <= kThinRows && batch < (int64_t(1) << 24) / ((n + 15) / 16 + 1);
+}
+
+bool mx_linear_quantizes(int64_t batch, int64_t m, int64_t n, int64_t k) {
+  return thin(batch, m, n) && m <= 16 && m * ((k + kMxGroup - 1) / kMxGroup) * kMxGroup <= kThinValues;
+}
+
 size_t mx_matmul_bytes(int64_t batch, int64_t m, int64_t n, int64_t k) {
-  if (m <= kThinRows) return 0;
+  if (thin(batch, m, n)) return 0;
   const int parts = mx_plan(batch, m, n, k).parts;
   return parts > 1 ? static_cast<size_t>(parts) * batch * m * join_pitch(n) * 4 : 0;
 }
-
-bool mx_linear_quantizes(int64_t m, int64_t k) { return m <= 16 && m * ((k + kMxGroup - 1) / kMxGroup) * kMxGroup <= kThinValues; }
 
 hipError_t launch_mx_linear(const MxInput &in, int64_t m, const MxMatrix &w, const MxOutput &out, hipStream_t s) {
   const MxThin p{MxMatrix{nullptr, nullptr, w.batch, m, w.cols}, w, out, in.x, in.pitch, in.batch_stride};
@@ -899,7 +906,7 @@ hipError_t run_gemm(const MxMatrix &a, const MxMatrix &b, const MxOutput &out, i
 hipError_t launch_mx_matmul(const MxMatrix &a, const MxMatrix &b, const MxOutput &out, void *workspace, hipStream_t s) {
   return with_type(out.dtype, [&](auto t) {
     using T = decltype(t);
-    if (a.rows <= kThinRows) {
+    if (thin(a.batch, a.rows, b.rows)) {
       const MxThin p{a, b, out, nullptr, 0, 0};
       return a.rows <= 16 ? run_thin<EF32, T, 1, false>(p, s) : run_thin<EF32, T, 2, false>(p, s);
     }
