@@ -140,40 +140,48 @@ struct MxQuantize {
   int tiles_r, tiles_c;
 };
 
-// A workgroup per 128 x 128 tile, the extent of one word of scales either way.
-// Along the rows 16 threads share a row, eight values each, and four of them a
-// block.  Along the columns the tile lies in LDS, and a thread takes 32 rows
-// of one column (of two neighbouring ones of a 16-bit type); the four threads
-// of a column are neighbours, so that they write its 64 bytes of codes
-// together.  A row of LDS has its 16-byte pieces exchanged by its block of 32
-// rows, which puts those four threads on different banks.
-template <class T, bool ROWS, bool COLS, bool NOISE>
+// A workgroup per tile of 128 rows and kCols columns.  Along the rows a thread
+// takes eight values, and four neighbours share a block.  Along the columns the
+// tile lies in LDS, and a thread takes 32 rows of one column (of two
+// neighbouring ones of a 16-bit type); the four threads of a column are
+// neighbours, so that they write its 64 bytes of codes together.  A row of LDS
+// has its 16-byte pieces exchanged by its block of 32 rows, which puts those
+// four threads on different banks.
+// kCols is 128, the extent of a word of scales, but for fp32 matrices of few
+// tiles, where tiles of 64 make twice the workgroups (both ways, 3 x 257 x 1531
+// with noise: 16.5 -> 9.8 us; 4096 x 16384: 71 -> 87, as its rows of codes are
+// written in halves).  Both ways, 8192 x 16384 bf16 take 97 us (4.2 TB/s).  With
+// 32 rows of four columns per thread in registers instead of LDS, fp32 4096 x
+// 16384 took 166: its stores along the columns are scattered.
+template <class T, bool ROWS, bool COLS, bool NOISE, int kCols>
 __global__ void __launch_bounds__(256) mx_quantize(MxQuantize p) {
   using S = typename T::S;
   constexpr bool k16 = sizeof(S) == 2;
-  constexpr int kRowWords = k16 ? 64 : 128;                  // of LDS
+  constexpr int kRowWords = kCols * sizeof(S) / 4;           // of LDS
+  constexpr int kLanes = kCols / 8, kRows = 256 / kLanes;    // threads to a row, rows at a time
+  constexpr int kNoiseWords = kCols / 4;
   __shared__ __attribute__((aligned(16))) uint32_t tile[COLS ? 128 * kRowWords : 4];
-  __shared__ __attribute__((aligned(16))) uint32_t noises[COLS && NOISE ? 128 * 32 : 4];
+  __shared__ __attribute__((aligned(16))) uint32_t noises[COLS && NOISE ? 128 * kNoiseWords : 4];
   const int tid = threadIdx.x, lane = tid & 63;
   const int64_t per_matrix = static_cast<int64_t>(p.tiles_r) * p.tiles_c;
   const int64_t mat = blockIdx.x / per_matrix;
   const int in = static_cast<int>(blockIdx.x - mat * per_matrix);
-  const int64_t row0 = static_cast<int64_t>(in / p.tiles_c) * 128, col0 = static_cast<int64_t>(in % p.tiles_c) * 128;
+  const int64_t row0 = static_cast<int64_t>(in / p.tiles_c) * 128, col0 = static_cast<int64_t>(in % p.tiles_c) * kCols;
   const S *x = static_cast<const S *>(p.x) + mat * p.batch_stride;
   const uint8_t *noise = NOISE ? p.noise + mat * p.rows * p.cols : nullptr;
-  const int r_in = tid >> 4, c_in = (tid & 15) * 8;
+  const int r_in = tid / kLanes, c_in = (tid % kLanes) * 8;
   const int64_t col = col0 + c_in;
   const int left = static_cast<int>(min<int64_t>(8, p.cols - col));       // of the eight
   const int64_t groups = p.by_rows.groups(), row_blocks = p.by_rows.row_blocks();
 
   constexpr int kAhead = 4;
   const int64_t last = COLS ? row0 + 128 : min<int64_t>(row0 + 128, (p.rows + 31) / 32 * 32);
-  for (int k0 = 0; k0 < 128 && row0 + k0 < last; k0 += 16 * kAhead) {
+  for (int k0 = 0; k0 < 128 && row0 + k0 < last; k0 += kRows * kAhead) {
     Octet<T> v[kAhead];
     uint32_t r[kAhead][2];
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
-      const int64_t row = row0 + k0 + 16 * a + r_in;
+      const int64_t row = row0 + k0 + kRows * a + r_in;
       const int here = row < p.rows ? left : 0;
       v[a].load(x + row * p.pitch + col, here);
       r[a][0] = r[a][1] = 0;
@@ -190,7 +198,7 @@ __global__ void __launch_bounds__(256) mx_quantize(MxQuantize p) {
     }
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
-      const int in_tile = k0 + 16 * a + r_in;
+      const int in_tile = k0 + kRows * a + r_in;
       const int64_t row = row0 + in_tile;
       if constexpr (COLS) {
         // (piece of 16 bytes ^ 4 x block of 32 rows)
@@ -198,9 +206,10 @@ __global__ void __launch_bounds__(256) mx_quantize(MxQuantize p) {
         const int turn = (in_tile >> 5) << 2;
 #pragma unroll
         for (int i = 0; i < (k16 ? 1 : 2); ++i)
-          to[((tid & 15) * (k16 ? 1 : 2) + i) ^ turn] = *reinterpret_cast<const uint4 *>(v[a].w + 4 * i);
+          to[((tid % kLanes) * (k16 ? 1 : 2) + i) ^ turn] = *reinterpret_cast<const uint4 *>(v[a].w + 4 * i);
         if constexpr (NOISE)
-          *reinterpret_cast<uint2 *>(noises + in_tile * 32 + ((2 * (tid & 15)) ^ (turn << 1))) = make_uint2(r[a][0], r[a][1]);
+          *reinterpret_cast<uint2 *>(noises + in_tile * kNoiseWords +
+                                     ((2 * (tid % kLanes)) ^ ((in_tile >> 5) * (kNoiseWords / 4)))) = make_uint2(r[a][0], r[a][1]);
       }
       if constexpr (ROWS) {
         uint32_t largest = v[a].largest();
@@ -214,17 +223,20 @@ __global__ void __launch_bounds__(256) mx_quantize(MxQuantize p) {
           bytes[i] = NOISE ? r[a][i / 4] >> (8 * (i & 3)) & 0xff : 0;
         }
         const uint32_t word = eight_codes<T, NOISE>(bits, bytes, s);
-        uint32_t scales = s << (8 * ((lane >> 2) & 3));
+        // a row's scales of this tile: a word, or half of one
+        uint32_t scales = s << (8 * (tid % kLanes / 4));
         scales |= other_lane<4>(scales);
-        scales |= other_lane<8>(scales);
+        if constexpr (kCols == 128) scales |= other_lane<8>(scales);
         if (row < p.rows) {
           *reinterpret_cast<uint32_t *>(p.by_rows.codes + (mat * p.rows + row) * (groups * 64) + (col0 + c_in) / 2) = word;
         } else {
           scales = 0;
         }
-        if ((tid & 15) == 0 && row < row_blocks * 32)
-          *reinterpret_cast<uint32_t *>(p.by_rows.scales + (((mat * row_blocks + row / 32) * groups + col0 / 128) * 32 +
-                                                            row % 32) * 4) = scales;
+        if (tid % kLanes == 0 && row < row_blocks * 32) {
+          uint8_t *to = p.by_rows.scales + (((mat * row_blocks + row / 32) * groups + col0 / 128) * 32 + row % 32) * 4;
+          if constexpr (kCols == 128) *reinterpret_cast<uint32_t *>(to) = scales;
+          else *reinterpret_cast<uint16_t *>(to + col0 % 128 / 32) = static_cast<uint16_t>(scales);
+        }
       }
     }
   }
@@ -234,7 +246,7 @@ __global__ void __launch_bounds__(256) mx_quantize(MxQuantize p) {
     const int rb = lane & 3, turn = rb << 4;
     constexpr int kSub = k16 ? 2 : 1;                        // columns of a thread at a time
 #pragma unroll 1
-    for (int it = 0; it < (k16 ? 1 : 2); ++it) {
+    for (int it = 0; it < kRowWords / 64; ++it) {
       const int c = (lane >> 2) + 16 * (tid >> 6) + 64 * it; // column, or pair of columns
       uint32_t raw[32];
 #pragma unroll
@@ -248,7 +260,7 @@ __global__ void __launch_bounds__(256) mx_quantize(MxQuantize p) {
           bits[i] = k16 ? raw[i] >> (16 * h) & 0xffff : raw[i];
           largest = max(largest, bits[i] & (k16 ? 0x7fffu : 0x7fffffffu));
           const int b = c * kSub + h;                        // its byte of noise
-          bytes[i] = NOISE ? noises[(32 * rb + i) * 32 + ((b >> 2) ^ (rb << 3))] >> (8 * (b & 3)) & 0xff : 0;
+          bytes[i] = NOISE ? noises[(32 * rb + i) * kNoiseWords + ((b >> 2) ^ (rb * (kNoiseWords / 4)))] >> (8 * (b & 3)) & 0xff : 0;
         }
         if constexpr (k16) largest = __float_as_uint(T::ld(static_cast<S>(largest)));
         const uint32_t s = scale_byte(largest, NOISE);
@@ -807,17 +819,24 @@ hipError_t launch_mx_quantize(const MxInput &in, int64_t batch, int64_t rows, in
   MxQuantize p{in.x, in.pitch, in.batch_stride, in.noise, rows, cols, by_rows, by_columns,
                static_cast<int>((rows + 127) / 128), static_cast<int>((cols + 127) / 128)};
   const int64_t tiles = batch * p.tiles_r * p.tiles_c;
+  const bool narrow = in.dtype == DT_F32 && tiles < 512;
+  if (narrow) p.tiles_c *= 2;
   return with_type(in.dtype, [&](auto t) {
     using T = decltype(t);
     return with_flag(in.noise != nullptr, [&](auto noise) {
-      auto run = [&](auto kernel) {
-        kernel<<<dim3(tiles), dim3(256), 0, s>>>(p);
+      constexpr bool N = decltype(noise)::value;
+      auto run = [&](auto wide) {
+        constexpr int kCols = decltype(wide)::value;
+        const dim3 grid(static_cast<unsigned>(tiles * (128 / kCols)));
+        if (!by_columns.codes) mx_quantize<T, true, false, N, kCols><<<grid, dim3(256), 0, s>>>(p);
+        else if (!by_rows.codes) mx_quantize<T, false, true, N, kCols><<<grid, dim3(256), 0, s>>>(p);
+        else mx_quantize<T, true, true, N, kCols><<<grid, dim3(256), 0, s>>>(p);
         return hipGetLastError();
       };
-      constexpr bool N = decltype(noise)::value;
-      if (!by_columns.codes) return run(mx_quantize<T, true, false, N>);
-      if (!by_rows.codes) return run(mx_quantize<T, false, true, N>);
-      return run(mx_quantize<T, true, true, N>);
+      if constexpr (T::code == DT_F32) {
+        if (narrow) return run(std::integral_constant<int, 64>{});
+      }
+      return run(std::integral_constant<int, 128>{});
     });
   });
 }
