@@ -881,17 +881,22 @@ MxPlan mx_plan(int64_t batch, int64_t m, int64_t n, int64_t k) {
 
 int64_t join_pitch(int64_t n) { return (n + 3) / 4 * 4; }
 
-// (a grid holds 2^24 workgroups of 256 threads)
-bool thin(int64_t batch, int64_t m, int64_t n) {
-  return m <= kThinRows && batch < (int64_t(1) << 24) / ((n + 15) / 16 + 1);
+// Whether mx_thin takes a product: up to 16 rows of A, and up to kThinRows by a
+// B of up to 2^25 values.  Beyond those its workgroups' reads of A cost more
+// than the others' tiles waste (32 x 4096 by 4096 x 4096: 12.8 us, in tiles 16.7;
+// 32 x 16384 by 16384 x 16384: 54 and 33).  (A grid holds 2^24 workgroups of 256
+// threads.)
+bool thin(int64_t batch, int64_t m, int64_t n, int64_t k) {
+  return m <= kThinRows && batch < (int64_t(1) << 24) / ((n + 15) / 16 + 1) &&
+         (m <= 16 || k == 0 || batch * n <= (int64_t(1) << 25) / k);
 }
 
 bool mx_linear_quantizes(int64_t batch, int64_t m, int64_t n, int64_t k) {
-  return thin(batch, m, n) && m <= 16 && m * ((k + kMxGroup - 1) / kMxGroup) * kMxGroup <= kThinValues;
+  return thin(batch, m, n, k) && m <= 16 && m * ((k + kMxGroup - 1) / kMxGroup) * kMxGroup <= kThinValues;
 }
 
 size_t mx_matmul_bytes(int64_t batch, int64_t m, int64_t n, int64_t k) {
-  if (thin(batch, m, n)) return 0;
+  if (thin(batch, m, n, k)) return 0;
   const int parts = mx_plan(batch, m, n, k).parts;
   return parts > 1 ? static_cast<size_t>(parts) * batch * m * join_pitch(n) * 4 : 0;
 }
@@ -922,7 +927,7 @@ hipError_t run_gemm(const MxMatrix &a, const MxMatrix &b, const MxOutput &out, i
 hipError_t launch_mx_matmul(const MxMatrix &a, const MxMatrix &b, const MxOutput &out, void *workspace, hipStream_t s) {
   return with_type(out.dtype, [&](auto t) {
     using T = decltype(t);
-    if (thin(a.batch, a.rows, b.rows)) {
+    if (thin(a.batch, a.rows, b.rows, a.cols)) {
       const MxThin p{a, b, out, nullptr, 0, 0};
       return a.rows <= 16 ? run_thin<EF32, T, 1, false>(p, s) : run_thin<EF32, T, 2, false>(p, s);
     }
