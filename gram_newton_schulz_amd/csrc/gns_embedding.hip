@@ -497,23 +497,26 @@ embedding_sums(Sums p, const typename TG::S *grad, typename TW::S *weight) {
   // from there; narrow rows' groups share waves and read them one by one.
   const int at = static_cast<int>(min<int64_t>(threadIdx.x & 63, n - 1));
   const uint32_t my_key = p.keys[begin + at], my_place = p.places[begin + at];
+  const uint32_t before = begin > 0 ? p.keys[begin - 1] : p.vocab, behind = end < p.count ? p.keys[end] : p.vocab;
   auto key_of = [&](int i) -> uint32_t {
-    return WAVE ? static_cast<uint32_t>(__builtin_amdgcn_readlane(my_key, i)) : p.keys[begin + i];
+    return WAVE ? static_cast<uint32_t>(__builtin_amdgcn_readlane(my_key, i)) : p.keys[begin + min(i, n - 1)];
   };
   auto place_of = [&](int i) -> uint32_t {
-    return WAVE ? static_cast<uint32_t>(__builtin_amdgcn_readlane(my_place, i)) : p.places[begin + i];
+    return WAVE ? static_cast<uint32_t>(__builtin_amdgcn_readlane(my_place, i)) : p.places[begin + min(i, n - 1)];
   };
   uint32_t run = key_of(0);
-  bool reaches_in = begin > 0 && p.keys[begin - 1] == run;
+  bool reaches_in = before == run;
   float acc[kColumns] = {0, 0, 0, 0, 0, 0, 0, 0};
   constexpr int kAhead = 8;
   for (int i = 0; i < n; i += kAhead) {
-    uint32_t key[kAhead];
+    uint32_t key[kAhead], place[kAhead];
     float v[kAhead][kColumns];
 #pragma unroll
+    for (int a = 0; a < kAhead; ++a) key[a] = key_of(i + a), place[a] = place_of(i + a);
+#pragma unroll
     for (int a = 0; a < kAhead; ++a) {
-      key[a] = i + a < n ? key_of(i + a) : p.vocab;
-      if (key[a] < p.vocab) load_columns<TG, M>(grad + static_cast<int64_t>(place_of(i + a)) * p.grad_pitch, c, v[a]);
+      if (i + a >= n) key[a] = p.vocab;
+      if (key[a] < p.vocab) load_columns<TG, M>(grad + static_cast<int64_t>(place[a]) * p.grad_pitch, c, v[a]);
     }
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
@@ -532,7 +535,7 @@ embedding_sums(Sums p, const typename TG::S *grad, typename TW::S *weight) {
     }
   }
   if (run >= p.vocab) return;                          // padding
-  const bool reaches_out = end < p.count && p.keys[end] == run;
+  const bool reaches_out = behind == run;
   if (reaches_out && !reaches_in && lane == 0 && unit % p.blocks == 0) {
     const int64_t far = begin + static_cast<int64_t>(kShortRun) * p.piece;
     const bool is_long = far < p.count && p.keys[far] == run;
@@ -573,7 +576,8 @@ __global__ void __launch_bounds__(256) embedding_join(Sums p, typename TW::S *we
     }
     const int lane = threadIdx.x % lanes, mine = threadIdx.x / lanes;
     const Columns c(M, i % blocks, lane, lanes, p.width);
-    const int64_t from = parts * mine / groups, to = parts * (mine + 1) / groups;
+    const int used = static_cast<int>(min<int64_t>(groups, parts));     // groups with a share
+    const int64_t from = parts * min(mine, used) / used, to = parts * min(mine + 1, used) / used;
     float acc[kColumns] = {0, 0, 0, 0, 0, 0, 0, 0};
     constexpr int kAhead = 8;
     for (int64_t k0 = from; k0 < to; k0 += kAhead) {
@@ -592,7 +596,7 @@ __global__ void __launch_bounds__(256) embedding_join(Sums p, typename TW::S *we
     for (int k = 0; k < kColumns; ++k) sums[threadIdx.x][k] = acc[k];
     __syncthreads();
     if (mine == 0) {
-      for (int g = 1; g < groups; ++g) {
+      for (int g = 1; g < used; ++g) {
 #pragma unroll
         for (int k = 0; k < kColumns; ++k) acc[k] += sums[g * lanes + lane][k];
       }
