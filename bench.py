@@ -49,6 +49,8 @@ def flops_standard_sym(n, m, T):
 # --------------------------------------------------------------------------
 KERNEL_SRC = os.path.join(ROOT, "gram_newton_schulz_amd", "csrc", "gns_kernels.hip")
 PROFILES = os.path.join(ROOT, "profiles")
+LAYER_KERNELS = ("embedding_rows", "token_sort_once", "token_count", "token_scan", "token_scatter", "embedding_sums",
+                 "embedding_join", "embedding_row_sums", "mx_quantize", "mx_dequantize", "mx_thin", "mx_gemm", "mx_join")
 
 
 def short_kernel(name):
@@ -72,7 +74,7 @@ def short_kernel(name):
               "norm_finish", "row_l1",
               "select_topk", "check_rows", "momentum_l1", "row_sumsq", "normuon_factors",
               "dion3_update", "list_partials", "list_norm_once", "list_finish", "list_scale", "list_adamw",
-              "adamw_count"):
+              "adamw_count", *LAYER_KERNELS):
         if k in name:
             return k
     return name.split("(")[0][:60]
@@ -274,7 +276,8 @@ def summarize_pmc(fetch_dir, write_dir, calib_mib, workload):
 HBM_KERNELS = ("norm_partial", "row_partials", "scale_transpose", "scale_rows_f32", "transpose_sumsq", "norm_finish",
                "momentum_l1",
                "row_sumsq", "normuon_factors", "dion3_update", "select_topk",
-               "list_partials", "list_norm_once", "list_finish", "list_scale", "list_adamw", "adamw_count")
+               "list_partials", "list_norm_once", "list_finish", "list_scale", "list_adamw", "adamw_count",
+               *LAYER_KERNELS)
 
 
 def mfma_from_profile(kernel, workload):
@@ -594,6 +597,81 @@ def bench_lists(gns, torch, steps):
     return out
 
 
+def bench_layers(gns, torch, steps):
+    """The layers' operators: ms per call, the GB/s of the bytes that each
+    cannot do without (gradients, tables and matrices once, results once) and
+    for products TFLOP/s.  Calls go round three copies of their tensors, so that
+    none finds its own data in the last-level cache."""
+    gen = torch.Generator(device="cuda").manual_seed(11)
+
+    def tensor(*shape, dtype=torch.bfloat16):
+        return torch.empty(*shape, device="cuda").normal_(0.0, 1.0, generator=gen).to(dtype)
+
+    def tokens(n, vocab):
+        return torch.randint(0, vocab, (n,), device="cuda", generator=gen)
+
+    def lookup(n, vocab, width, dtype):
+        t, w = tokens(n, vocab), tensor(vocab, width, dtype=dtype)
+        out = torch.empty(n, width, dtype=torch.bfloat16, device="cuda")
+        rows = min(n, vocab * (1 - (1 - 1 / vocab) ** n))
+        return lambda: gns.embedding(t, w, scale=2.0, out=out), rows * width * w.element_size() + 2.0 * n * width, 0
+
+    def embedding_grad(n, vocab, width):
+        t, g = tokens(n, vocab), tensor(n, width)
+        into = torch.empty(vocab, width, device="cuda")
+        return lambda: gns.embedding_grad(t, g, into), 2.0 * n * width + 4.0 * vocab * width, 0
+
+    def quantize(rows, cols, dtype):
+        x = tensor(rows, cols, dtype=dtype)
+        out = gns.mxfp4_empty((rows, cols)), gns.mxfp4_empty((cols, rows))
+        return lambda: gns.mxfp4_quantize_both(x, out=out), rows * cols * (x.element_size() + 2 * 17 / 32), 0
+
+    def dequantize(rows, cols):
+        q = gns.mxfp4_quantize(tensor(rows, cols))
+        out = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda")
+        return lambda: gns.mxfp4_dequantize(q, out=out), rows * cols * (2 + 17 / 32), 0
+
+    def linear(batch, m, n, k):
+        lead = (batch,) if batch > 1 else ()
+        x, w = tensor(*lead, m, k), gns.mxfp4_quantize(tensor(*lead, n, k))
+        out = torch.empty(*lead, m, n, dtype=torch.bfloat16, device="cuda")
+        return (lambda: gns.mxfp4_matmul(x, w, out=out),
+                batch * (2.0 * m * k + 2.0 * m * n + n * k * 17 / 32), 2.0 * batch * m * n * k)
+
+    out = {}
+    for name, make in (
+            ("embedding 16 of 32768x4096 bf16", lambda: lookup(16, 32768, 4096, torch.bfloat16)),
+            ("embedding 32768 of 32768x4096 fp32 to bf16", lambda: lookup(32768, 32768, 4096, torch.float32)),
+            ("embedding_grad 4096 into 256x128", lambda: embedding_grad(4096, 256, 128)),
+            ("embedding_grad 1000 into 32768x1024", lambda: embedding_grad(1000, 32768, 1024)),
+            ("embedding_grad 32768 into 32768x4096", lambda: embedding_grad(32768, 32768, 4096)),
+            ("mxfp4_quantize_both 4096x16384 fp32", lambda: quantize(4096, 16384, torch.float32)),
+            ("mxfp4_quantize_both 8192x16384 bf16", lambda: quantize(8192, 16384, torch.bfloat16)),
+            ("mxfp4_dequantize 4096x16384", lambda: dequantize(4096, 16384)),
+            ("mxfp4_matmul 1x16384 by 4096x16384", lambda: linear(1, 1, 4096, 16384)),
+            ("mxfp4_matmul 64 x 48x7168 by 2048x7168", lambda: linear(64, 48, 2048, 7168)),
+            ("mxfp4_matmul 48x16384 by 4096x16384", lambda: linear(1, 48, 4096, 16384)),
+            ("mxfp4_matmul 8192x4096 by 16384x4096", lambda: linear(1, 8192, 16384, 4096))):
+        log(f"timing {name}")
+        calls = [make() for _ in range(3)]
+        for f, _, _ in calls:
+            f()
+        torch.cuda.synchronize()
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        e0.record()
+        for i in range(steps):
+            calls[i % 3][0]()
+        e1.record()
+        torch.cuda.synchronize()
+        s = e0.elapsed_time(e1) / steps / 1e3
+        out[name] = {"ms": round(s * 1e3, 4), "gbs": round(calls[0][1] / s / 1e9, 1)}
+        if calls[0][2]:
+            out[name]["tflops"] = round(calls[0][2] / s / 1e12, 1)
+        del calls
+        torch.cuda.empty_cache()
+    return out
+
+
 def desc_of(cfg):
     return {
         2: "16 x 1024x4096 bf16, log-uniform spectrum [1e-4,1]",
@@ -620,6 +698,8 @@ def main():
                     help="skip the timing of the whole Dion3 update (f = 1/4) on the workload's shape")
     ap.add_argument("--only-lists", action="store_true",
                     help="time only the operators over lists of tensors (gradient norm, clipping, AdamW)")
+    ap.add_argument("--only-layers", action="store_true",
+                    help="time only the layers' operators (embedding, its gradient, MXFP4)")
     ap.add_argument("--only-dion3", action="store_true",
                     help="time only the whole Dion3 update on the workload's shape (for profiles)")
     ap.add_argument("--calib-copy-mib", type=int, default=0,
@@ -689,6 +769,9 @@ def main():
 
     if args.only_lists:
         print(json.dumps({"lists": bench_lists(gns, torch, args.steps)}), flush=True)
+        return
+    if args.only_layers:
+        print(json.dumps({"layers": bench_layers(gns, torch, args.steps)}), flush=True)
         return
     if args.only_dion3:
         print(json.dumps({"dion3_step": bench_dion3_step(gns, synth, torch, w, coeffs, restarts,
