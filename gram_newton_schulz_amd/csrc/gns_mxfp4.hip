@@ -146,14 +146,21 @@ struct MxQuantize {
   const uint8_t *noise;
   int64_t rows, cols;
   MxMatrix by_rows, by_columns;
+  int64_t batch;
   int tiles_r, tiles_c;
   int once;                     // x is read with the streaming hint
+  int dealt;                    // XCDs take squares of four tiles
 };
 // A matrix that fills the last-level cache has the hint, so that its codes stay
 // there for the product (the layer gradients of 8192 x 16384 bf16: 704 -> 693 us,
 // quantising 4096 x 16384 fp32 both ways and back 157 -> 140); a smaller one may
 // still lie there itself (8192 x 4096 bf16 through a layer: 304 us, 308 with it).
 constexpr int64_t kLastLevelCache = int64_t(256) << 20;
+// Half of a line of codes belongs to each of two neighbouring tiles, in both
+// orders.  Squares of four tiles go to one XCD, whose L2 joins the halves (8192 x
+// 16384 bf16 both ways 106 -> 94 us, 4096 x 16384 fp32 78.3 -> 77.6); few tiles
+// are spread over the GPU instead, one by one.
+constexpr int64_t kDealtTiles = 512, kMaxDealt = int64_t(1) << 22;   // (a grid holds 2^24 workgroups)
 
 // A workgroup per tile of 128 rows and kCols columns.  Along the rows a thread
 // takes eight values, and four neighbours share a block.  Along the columns the
@@ -165,7 +172,7 @@ constexpr int64_t kLastLevelCache = int64_t(256) << 20;
 // kCols is 128, the extent of a word of scales, but for fp32 matrices of few
 // tiles, where tiles of 64 make twice the workgroups (both ways, 3 x 257 x 1531
 // with noise: 16.5 -> 9.8 us; 4096 x 16384: 71 -> 87, as its rows of codes are
-// written in halves).  Both ways, 8192 x 16384 bf16 take 97 us (4.2 TB/s).  With
+// written in halves).  Both ways, 8192 x 16384 bf16 take 94 us (4.4 TB/s).  With
 // 32 rows of four columns per thread in registers instead of LDS, fp32 4096 x
 // 16384 took 166: its stores along the columns are scattered.
 template <class T, bool ROWS, bool COLS, bool NOISE, int kCols>
@@ -178,10 +185,24 @@ __global__ void __launch_bounds__(256) mx_quantize(MxQuantize p) {
   __shared__ __attribute__((aligned(16))) uint32_t tile[COLS ? 128 * kRowWords : 4];
   __shared__ __attribute__((aligned(16))) uint32_t noises[COLS && NOISE ? 128 * kNoiseWords : 4];
   const int tid = threadIdx.x, lane = tid & 63;
-  const int64_t per_matrix = static_cast<int64_t>(p.tiles_r) * p.tiles_c;
-  const int64_t mat = blockIdx.x / per_matrix;
-  const int in = static_cast<int>(blockIdx.x - mat * per_matrix);
-  const int64_t row0 = static_cast<int64_t>(in / p.tiles_c) * 128, col0 = static_cast<int64_t>(in % p.tiles_c) * kCols;
+  int64_t tile_index = blockIdx.x;
+  int tiles_r = p.tiles_r, tiles_c = p.tiles_c;
+  if (p.dealt) {
+    tile_index = static_cast<int64_t>(blockIdx.x / 32) * 8 + blockIdx.x % 8;   // of the square
+    tiles_r = (tiles_r + 1) / 2;
+    tiles_c = (tiles_c + 1) / 2;
+  }
+  const int64_t per_matrix = static_cast<int64_t>(tiles_r) * tiles_c;
+  const int64_t mat = tile_index / per_matrix;
+  const int in = static_cast<int>(tile_index - mat * per_matrix);
+  int tile_r = in / tiles_c, tile_c = in % tiles_c;
+  if (p.dealt) {
+    const int corner = blockIdx.x / 8 % 4;
+    tile_r = tile_r * 2 + corner / 2;
+    tile_c = tile_c * 2 + corner % 2;
+    if (mat >= p.batch || tile_r >= p.tiles_r || tile_c >= p.tiles_c) return;
+  }
+  const int64_t row0 = static_cast<int64_t>(tile_r) * 128, col0 = static_cast<int64_t>(tile_c) * kCols;
   const S *x = static_cast<const S *>(p.x) + mat * p.batch_stride;
   const uint8_t *noise = NOISE ? p.noise + mat * p.rows * p.cols : nullptr;
   const int r_in = tid / kLanes, c_in = (tid % kLanes) * 8;
@@ -301,20 +322,24 @@ __global__ void __launch_bounds__(256) mx_quantize(MxQuantize p) {
   }
 }
 
-// The values of a 128 x 128 tile, eight per thread.
+// The values of a tile of 64 rows and 256 columns, eight per thread: whole lines
+// of codes (4096 x 16384: 39 us, 4.4 TB/s; 41 in tiles of 128 columns).
+constexpr int64_t kTilesX = int64_t(1) << 23;   // of a grid's first dimension
 template <class T>
 __global__ void __launch_bounds__(256) mx_dequantize(MxMatrix q, typename T::S *out, int tiles_r, int tiles_c) {
   using S = typename T::S;
   typedef float f32x2 __attribute__((ext_vector_type(2)));
   const int tid = threadIdx.x;
-  const int64_t per_matrix = static_cast<int64_t>(tiles_r) * tiles_c, mat = blockIdx.x / per_matrix;
-  const int in = static_cast<int>(blockIdx.x - mat * per_matrix);
-  const int64_t row0 = static_cast<int64_t>(in / tiles_c) * 128, group = in % tiles_c, groups = q.groups();
-  const int64_t col = group * 128 + (tid & 15) * 8;
+  const int64_t per_matrix = static_cast<int64_t>(tiles_r) * tiles_c, tile = blockIdx.y * kTilesX + blockIdx.x,
+                mat = tile / per_matrix;
+  if (mat >= q.batch) return;
+  const int in = static_cast<int>(tile - mat * per_matrix);
+  const int64_t row0 = static_cast<int64_t>(in / tiles_c) * 64, groups = q.groups();
+  const int64_t col = static_cast<int64_t>(in % tiles_c) * 256 + (tid & 31) * 8, group = col / 128;
   if (col >= q.cols) return;
 #pragma unroll
-  for (int k = 0; k < 128; k += 16) {
-    const int64_t row = row0 + k + (tid >> 4);
+  for (int k = 0; k < 64; k += 8) {
+    const int64_t row = row0 + k + (tid >> 5);
     if (row >= q.rows) return;
     const uint32_t w = *reinterpret_cast<const uint32_t *>(q.codes + (mat * q.rows + row) * q.pitch() + col / 2);
     const uint32_t s =
@@ -813,9 +838,13 @@ hipError_t run_thin(const MxThin &p, hipStream_t s) {
 hipError_t launch_mx_quantize(const MxInput &in, int64_t batch, int64_t rows, int64_t cols, const MxMatrix &by_rows,
                               const MxMatrix &by_columns, hipStream_t s) {
   MxQuantize p{in.x, in.pitch, in.batch_stride, in.noise, rows, cols, by_rows, by_columns,
-               static_cast<int>((rows + 127) / 128), static_cast<int>((cols + 127) / 128),
-               batch * rows * cols * dtype_size(in.dtype) >= kLastLevelCache};
-  const int64_t tiles = batch * p.tiles_r * p.tiles_c;
+               batch, static_cast<int>((rows + 127) / 128), static_cast<int>((cols + 127) / 128),
+               batch * rows * cols * dtype_size(in.dtype) >= kLastLevelCache, 0};
+  int64_t tiles = batch * p.tiles_r * p.tiles_c;
+  if (tiles >= kDealtTiles && tiles <= kMaxDealt && std::min(p.tiles_r, p.tiles_c) >= 8) {
+    p.dealt = 1;
+    tiles = (batch * ((p.tiles_r + 1) / 2) * ((p.tiles_c + 1) / 2) + 7) / 8 * 32;
+  }
   const bool narrow = in.dtype == DT_F32 && tiles < 512;
   if (narrow) p.tiles_c *= 2;
   return with_type(in.dtype, [&](auto t) {
@@ -839,11 +868,11 @@ hipError_t launch_mx_quantize(const MxInput &in, int64_t batch, int64_t rows, in
 }
 
 hipError_t launch_mx_dequantize(const MxMatrix &q, void *out, int dtype, hipStream_t s) {
-  const int tiles_r = static_cast<int>((q.rows + 127) / 128), tiles_c = static_cast<int>((q.cols + 127) / 128);
+  const int tiles_r = static_cast<int>((q.rows + 63) / 64), tiles_c = static_cast<int>((q.cols + 255) / 256);
   const int64_t tiles = q.batch * tiles_r * tiles_c;
   return with_type(dtype, [&](auto t) {
     using T = decltype(t);
-    mx_dequantize<T><<<dim3(tiles), dim3(256), 0, s>>>(q, static_cast<typename T::S *>(out), tiles_r, tiles_c);
+    mx_dequantize<T><<<dim3(std::min(tiles, kTilesX), (tiles + kTilesX - 1) / kTilesX), dim3(256), 0, s>>>(q, static_cast<typename T::S *>(out), tiles_r, tiles_c);
     return hipGetLastError();
   });
 }
