@@ -337,13 +337,18 @@ __global__ void __launch_bounds__(256) mx_dequantize(MxMatrix q, typename T::S *
   const int64_t row0 = static_cast<int64_t>(in / tiles_c) * 64, groups = q.groups();
   const int64_t col = static_cast<int64_t>(in % tiles_c) * 256 + (tid & 31) * 8, group = col / 128;
   if (col >= q.cols) return;
+  uint32_t words[8], bytes[8];                               // (all loads before the first store)
 #pragma unroll
-  for (int k = 0; k < 64; k += 8) {
-    const int64_t row = row0 + k + (tid >> 5);
+  for (int k = 0; k < 8; ++k) {
+    const int64_t row = min(row0 + 8 * k + (tid >> 5), q.rows - 1);
+    words[k] = *reinterpret_cast<const uint32_t *>(q.codes + (mat * q.rows + row) * q.pitch() + col / 2);
+    bytes[k] = q.scales[(((mat * q.row_blocks() + row / 32) * groups + group) * 32 + row % 32) * 4 + ((tid >> 2) & 3)];
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int64_t row = row0 + 8 * k + (tid >> 5);
     if (row >= q.rows) return;
-    const uint32_t w = *reinterpret_cast<const uint32_t *>(q.codes + (mat * q.rows + row) * q.pitch() + col / 2);
-    const uint32_t s =
-        q.scales[(((mat * q.row_blocks() + row / 32) * groups + group) * 32 + row % 32) * 4 + ((tid >> 2) & 3)];
+    const uint32_t w = words[k], s = bytes[k];
     const float scale = s == 255 ? __uint_as_float(0x7fc00000u) : scale_of(s);
     float v[8];
     const auto two = [&](int i, f32x2 x) {
@@ -361,8 +366,8 @@ __global__ void __launch_bounds__(256) mx_dequantize(MxMatrix q, typename T::S *
       if constexpr (sizeof(S) == 4) {
         __builtin_memcpy(to, v, 32);
       } else {
-        const uint32_t words[4] = {T::st2(v[0], v[1]), T::st2(v[2], v[3]), T::st2(v[4], v[5]), T::st2(v[6], v[7])};
-        __builtin_memcpy(to, words, 16);
+        const uint32_t pairs[4] = {T::st2(v[0], v[1]), T::st2(v[2], v[3]), T::st2(v[4], v[5]), T::st2(v[6], v[7])};
+        __builtin_memcpy(to, pairs, 16);
       }
     } else {
 #pragma unroll
