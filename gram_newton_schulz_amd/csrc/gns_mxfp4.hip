@@ -16,6 +16,8 @@ typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));   // anywhere
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
@@ -428,6 +430,7 @@ struct MxGemm {
   int run;             // consecutive tiles dealt to one XCD
   int parts;           // of the contraction
   int64_t part_stride; // elements from one part's results to the next's
+  int once;            // results that are there are read with the streaming hint
 };
 
 // chunk c of row r lies at chunk c ^ swizzle(r): rows that share a bank have
@@ -621,12 +624,14 @@ __global__ void __launch_bounds__((L::THREADS)) mx_gemm(MxGemm p) {
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
-  // 16-bit results are rounded and go through LDS, so that the workgroup stores
-  // whole rows (8192 x 4096 by 16384 x 4096: 312 us with the quantisation, 325
-  // straight from registers).  fp32 ones, and those that are added to what is
-  // there, go straight from registers, where a lane has runs of four columns
-  // (the layer gradients of that product: 717 us, 727 through LDS).  Accesses of
-  // 16 bytes need no alignment beyond the element's.
+  // Results leave in whole rows, which takes a way through LDS: 16-bit ones of the
+  // whole workgroup (8192 x 4096 by 16384 x 4096: 312 us with the quantisation, 325
+  // straight from registers), fp32 ones and those that are added to what is there
+  // 32 rows of a wave at a time (4096 x 8192 by 16384 x 8192 into fp32 285 us,
+  // added 332; straight from registers 341 and 373, as a lane has four columns).
+  // Tiles of four waves, whose results are small, store the latter straight from
+  // registers (1000 x 777 x 513: 26.5 us for both gradients, 27.6 through LDS).
+  // Accesses of 16 bytes need no alignment beyond the element's.
   S *const out = static_cast<S *>(p.o.out) + part * p.part_stride + mat * p.o.batch_stride;
   const int64_t rows = p.a.rows, cols = p.b.rows;
   if constexpr (sizeof(S) == 2) {
@@ -661,6 +666,75 @@ __global__ void __launch_bounds__((L::THREADS)) mx_gemm(MxGemm p) {
       }
       return;
     }
+  }
+  if constexpr (L::NW == 8) {
+    constexpr int kPitch = L::WTN + 4, kLanes = L::WTN / 4, kAt = 64 / kLanes, kSteps = 32 / kAt;
+    static_assert(L::NW * 32 * kPitch * 4 <= L::LDS, "LDS");
+    float *const staged = reinterpret_cast<float *>(lds) + wave * 32 * kPitch;
+    const int c = lane % kLanes * 4;
+    const int64_t col = col0 + wc + c;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < L::NBM; ++i) {
+      const int64_t first_row = row0 + wr + 32 * i + lane / kLanes;
+      uint32_t old[kSteps][sizeof(S)] = {};                  // four values each
+      if (p.o.accumulate) {
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+          const int64_t row = first_row + k * kAt;
+          const S *from = out + row * p.o.pitch + col;
+          if (row < rows && col + 4 <= cols) {
+            // (results of 256 MiB, whose streaming hint leaves the L2 to the factors'
+            // panels: the layer gradients of that product 667 -> 654 us)
+            using W = std::conditional_t<sizeof(S) == 4, f32x4_any, u32x2_any>;
+            const W v = p.once ? __builtin_nontemporal_load(reinterpret_cast<const W *>(from))
+                               : *reinterpret_cast<const W *>(from);
+            __builtin_memcpy(old[k], &v, sizeof(v));
+          } else if (row < rows) {
+            S few[4] = {};
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+              if (col + e < cols) few[e] = from[e];
+            __builtin_memcpy(old[k], few, sizeof(few));
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < L::NBN; ++j)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          *reinterpret_cast<float4 *>(staged + lr * kPitch + 32 * j + 8 * g + 4 * lh) =
+              make_float4(acc[j][i][4 * g], acc[j][i][4 * g + 1], acc[j][i][4 * g + 2], acc[j][i][4 * g + 3]);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) {
+        const int64_t row = first_row + k * kAt;
+        const float4 v = *reinterpret_cast<const float4 *>(staged + (k * kAt + lane / kLanes) * kPitch + c);
+        const float x[4] = {v.x, v.y, v.z, v.w};
+        S before[4], sum[4];
+        __builtin_memcpy(before, old[k], sizeof(before));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[e] = TO::st(p.o.accumulate ? TO::ld(before[e]) + x[e] : x[e]);
+        S *to = out + row * p.o.pitch + col;
+        if (row < rows && col + 4 <= cols) {
+          if constexpr (sizeof(S) == 4) {
+            __builtin_nontemporal_store(f32x4_any{sum[0], sum[1], sum[2], sum[3]}, reinterpret_cast<f32x4_any *>(to));
+          } else {
+            u32x2_any v;
+            __builtin_memcpy(&v, sum, sizeof(v));
+            __builtin_nontemporal_store(v, reinterpret_cast<u32x2_any *>(to));
+          }
+        } else if (row < rows) {
+#pragma unroll
+          for (int e = 0; e < 3; ++e)
+            if (col + e < cols) to[e] = sum[e];
+        }
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    }
+    return;
   }
 #pragma unroll
   for (int i = 0; i < L::NBM; ++i) {
@@ -945,7 +1019,8 @@ hipError_t launch_mx_linear(const MxInput &in, int64_t m, const MxMatrix &w, con
 template <class T, class L>
 hipError_t run_gemm(const MxMatrix &a, const MxMatrix &b, const MxOutput &out, int parts, hipStream_t s) {
   MxGemm p{a, b, out, static_cast<int>((a.rows + L::TM - 1) / L::TM), static_cast<int>((b.rows + L::TN - 1) / L::TN), 1,
-           parts, a.batch * out.batch_stride};
+           parts, a.batch * out.batch_stride,
+           static_cast<int64_t>(sizeof(typename T::S)) * a.batch * a.rows * b.rows >= kLastLevelCache};
   const int64_t tiles = a.batch * p.tiles_m * p.tiles_n * parts;
   // runs of up to 32 tiles, in whole runs per XCD
   const int64_t each = tiles / 8;

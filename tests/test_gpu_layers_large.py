@@ -95,3 +95,18 @@ def test_runs_of_every_length(width, accumulate):
     say("runs", width, accumulate)
     got = gns.embedding_grad(tokens.cuda(), g.cuda(), into, scale=0.5, accumulate=accumulate)
     check_grad(got, tokens, g, vocab, 0.5, None if old is None else f64(old), torch.float32)
+
+
+@pytest.mark.parametrize("dtype,m,n", [(torch.float32, 8200, 8211), (torch.bfloat16, 8199, 16401), (torch.float32, 4000, 4001)])
+def test_accumulated_results_larger_than_the_cache(dtype, m, n):
+    """The sum of what is there and the product's fp32 result, rounded once."""
+    gns = need_gpu()
+    gen = torch.Generator(device="cuda").manual_seed(52)
+    a, b = (gns.mxfp4_quantize(torch.empty(rows, 65, device="cuda").normal_(0.0, 1.0, generator=gen)) for rows in (m, n))
+    old = torch.empty(m, n + 3, device="cuda").normal_(0.0, 1.0, generator=gen).to(dtype)
+    say("accumulate large", dtype, m, n)
+    product = gns.mxfp4_matmul(a, b, dtype=torch.float32)
+    into = old.clone()
+    gns.mxfp4_matmul(a, b, out=into[:, 2:n + 2], accumulate=True)
+    assert torch.equal(into[:, 2:n + 2], (old[:, 2:n + 2].float() + product).to(dtype))
+    assert torch.equal(into[:, :2], old[:, :2]) and torch.equal(into[:, n + 2:], old[:, n + 2:])
