@@ -9,6 +9,8 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -32,8 +34,8 @@ def hipcc() -> str:
 def build(verbose: bool = False, timeline: bool = False) -> str:
     target = TIMELINE_LIB if timeline else LIB
     tmp = target + ".tmp"
-    cmd = [
-        hipcc(), f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-shared",
+    flags = [
+        f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
         # packed fp32 instructions are kept out of all generated code
         "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
         # the epilogues index the accumulator tiles with unrolled loop
@@ -41,18 +43,26 @@ def build(verbose: bool = False, timeline: bool = False) -> str:
         "-mllvm", "-pragma-unroll-threshold=200000",
         "-I", INCLUDE, "-I", CSRC,
         *(["-DGNS_TIMELINE"] if timeline else []),
-        *[os.path.join(CSRC, s) for s in SOURCES],
-        "-o", tmp,
+        # the compiler's resource report of every kernel (checked below)
+        "-Rpass-analysis=kernel-resource-usage",
     ]
-    # the compiler's resource report of every kernel (checked below)
-    cmd.insert(-2, "-Rpass-analysis=kernel-resource-usage")
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        sys.stderr.write(res.stdout + res.stderr)
-        raise RuntimeError(f"hipcc failed with exit code {res.returncode}")
-    spills = scratch_users(res.stderr)
+
+    def run(cmd) -> str:
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            sys.stderr.write(res.stdout + res.stderr)
+            raise RuntimeError(f"hipcc failed with exit code {res.returncode}")
+        return res.stderr
+
+    # the sources side by side (one after another they take 130 s), then the library
+    with tempfile.TemporaryDirectory() as objects, ThreadPoolExecutor(4) as pool:
+        made = [os.path.join(objects, s + ".o") for s in SOURCES]
+        report = "\n".join(pool.map(run, ([hipcc(), "-c", *flags, os.path.join(CSRC, s), "-o", o]
+                                          for s, o in zip(SOURCES, made))))
+        run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *made, "-o", tmp])
+    spills = scratch_users(report)
     if spills:
         raise RuntimeError("GEMM kernels that use scratch memory: " + ", ".join(spills))
     os.replace(tmp, target)
