@@ -4,7 +4,7 @@
 //
 // * mx_quantize   -- codes and scales of a matrix, of its transpose, or of both
 //                    from one read of it.  HBM-bound: 8192 x 16384 bf16 both
-//                    ways in 94 us.
+//                    ways in 90 us (4.6 TB/s).
 // * mx_dequantize -- the values back.  HBM-bound.
 // * mx_gemm       -- C = A B^T of two quantised matrices by scaled MFMA.  Bound by
 //                    power where it is large (8192^3: 272 us, 4.0 PFLOP/s; 190 us
@@ -176,10 +176,12 @@ struct MxQuantize {
 // still lie there itself (8192 x 4096 bf16 through a layer: 304 us, 308 with it).
 constexpr int64_t kLastLevelCache = int64_t(256) << 20;
 // Half of a line of codes belongs to each of two neighbouring tiles, in both
-// orders.  Squares of four tiles go to one XCD, whose L2 joins the halves (8192 x
-// 16384 bf16 both ways 106 -> 94 us, 4096 x 16384 fp32 78.3 -> 77.6); few tiles
-// are spread over the GPU instead, one by one.
-constexpr int64_t kDealtTiles = 512, kMaxDealt = int64_t(1) << 22;   // (a grid holds 2^24 workgroups)
+// orders.  Squares of four tiles go to one XCD, whose L2 joins the halves, where
+// there are many tiles (both ways: 8192 x 16384 bf16 103 -> 90 us, 32768 x 4096 bf16
+// 93 -> 82, 16389 x 8330 bf16 129 -> 113, 4096 x 16384 fp32 76.5 -> 74.6); fewer
+// are spread over the GPU one by one (8192 x 4096 bf16 by rows: 15.4 us, 16.7 in
+// squares).
+constexpr int64_t kDealtTiles = 4096, kMaxDealt = int64_t(1) << 22;   // (a grid holds 2^24 workgroups)
 
 // A workgroup per tile of 128 rows and kCols columns.  Along the rows a thread
 // takes eight values, and four neighbours share a block.  Along the columns the
@@ -191,7 +193,7 @@ constexpr int64_t kDealtTiles = 512, kMaxDealt = int64_t(1) << 22;   // (a grid 
 // kCols is 128, the extent of a word of scales, but for fp32 matrices of few
 // tiles, where tiles of 64 make twice the workgroups (both ways, 3 x 257 x 1531
 // with noise: 16.5 -> 9.8 us; 4096 x 16384: 71 -> 87, as its rows of codes are
-// written in halves).  Both ways, 8192 x 16384 bf16 take 94 us (4.4 TB/s).  With
+// written in halves).  Both ways, 8192 x 16384 bf16 take 90 us (4.6 TB/s).  With
 // 32 rows of four columns per thread in registers instead of LDS, fp32 4096 x
 // 16384 took 166: its stores along the columns are scattered.
 template <class T, bool ROWS, bool COLS, bool NOISE, int kCols>
