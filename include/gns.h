@@ -565,7 +565,8 @@ gns_status gns_adamw_step_counted(const gns_tensor_list *list, const void *table
  * Buffers need the alignment of their elements, no more.  A pitch is at least
  * the width where rows are written; rows that are read may share memory.
  * GNS_E_SHAPE (a negative size, count > 2^30, vocab >= 2^31, width > 2^24, more
- * than 2^42 elements, or such a pitch), GNS_E_DTYPE, GNS_E_NULL, GNS_E_PARAM (token_bits, a scale
+ * than 2^42 elements, a smaller pitch, or one above 2^25 of a table and 2^26 of
+ * rows), GNS_E_DTYPE, GNS_E_NULL, GNS_E_PARAM (token_bits, a scale
  * that is not finite, a misaligned address), GNS_E_ALIAS (written memory that
  * may be read or written as another argument, too).
  */
