@@ -4,7 +4,7 @@
 //                       elements per thread in 16-byte accesses.
 // * token_sort_once, token_count, token_scan, token_scatter
 //                    -- a stable sort of the tokens by radix, with the
-//                       position of each: up to 4096 tokens in one workgroup,
+//                       position of each: up to 6144 tokens in one workgroup,
 //                       more of them in three launches per digit.
 // * embedding_sums   -- the sorted tokens are cut into pieces of equal length,
 //                       whatever their runs: a group of threads adds the
@@ -199,7 +199,7 @@ embedding_rows(Tokens tokens, int64_t count, const typename TW::S *weight, int64
 // ---------------------------------------------------------------------------
 // sort
 // ---------------------------------------------------------------------------
-constexpr int kOnce = 4;               // tokens per thread of 1024: of the sort in one workgroup
+constexpr int kOnce = 6;               // tokens per thread of 1024: of the sort in one workgroup, at most
 constexpr int kEach = 2;               // ... and of a tile
 constexpr int kTile = kEach * 1024;
 constexpr int kFewTiles = 32;          // so few are summed by every workgroup itself
@@ -280,7 +280,8 @@ __device__ __forceinline__ int64_t first_not_below(const uint32_t *keys, int64_t
   return low;
 }
 
-// Up to 1024 N tokens: all digits in one workgroup.
+// Up to 1024 N tokens: all digits in one workgroup.  (4739 tokens into 2420 x 42:
+// 30.0 us, 33.9 by the launches below; 8192 tokens into 32768 x 128: 35.2 and 33.9.)
 template <int N>
 __global__ void __launch_bounds__(1024)
 token_sort_once(Tokens tokens, int count, uint32_t vocab, int passes, int bits, uint32_t *keys, uint32_t *places,
@@ -765,8 +766,17 @@ hipError_t launch_embedding_grad(const void *tokens, int token_bits, int64_t cou
   if (plan.by_row) {
     // no sort
   } else if (!plan.many) {
-    token_sort_once<kOnce><<<dim3(1), dim3(1024), 0, s>>>(t, static_cast<int>(count), v, plan.passes, plan.bits, keys,
-                                                         places, joins);
+    const int n = static_cast<int>(count);
+    auto sort = [&](auto each) {
+      token_sort_once<decltype(each)::value>
+          <<<dim3(1), dim3(1024), 0, s>>>(t, n, v, plan.passes, plan.bits, keys, places, joins);
+    };
+    // (its time goes with the tokens per thread: 1000 into 30000 x 300 26.3 us, 29.1
+    // with four of them)
+    if (n <= 1024) sort(std::integral_constant<int, 1>{});
+    else if (n <= 2048) sort(std::integral_constant<int, 2>{});
+    else if (n <= 4096) sort(std::integral_constant<int, 4>{});
+    else sort(std::integral_constant<int, kOnce>{});
   } else {
     uint32_t *keys2 = words(plan.keys2), *places2 = words(plan.places2), *counts = words(plan.counts);
     for (int pass = 0; pass < plan.passes; ++pass) {

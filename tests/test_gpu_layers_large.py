@@ -110,3 +110,17 @@ def test_accumulated_results_larger_than_the_cache(dtype, m, n):
     gns.mxfp4_matmul(a, b, out=into[:, 2:n + 2], accumulate=True)
     assert torch.equal(into[:, 2:n + 2], (old[:, 2:n + 2].float() + product).to(dtype))
     assert torch.equal(into[:, :2], old[:, :2]) and torch.equal(into[:, n + 2:], old[:, n + 2:])
+
+
+# the numbers of tokens at which the sort has another form, and one more
+@pytest.mark.parametrize("count", [1023, 1024, 1025, 2047, 2048, 2049, 4095, 4096, 4097, 6143, 6144, 6145, 8192, 8193])
+@pytest.mark.parametrize("kind", ["zipf", "all", "padded"])
+def test_sorts_of_every_length(count, kind):
+    gns = need_gpu()
+    rng = np.random.default_rng(count)
+    vocab, width = 70001, 5
+    tokens = ids(rng, count, vocab, kind)
+    g = torch.from_numpy(rng.normal(size=(count, width))).to(torch.float32)
+    say("sorts", count, kind)
+    got = gns.embedding_grad(tokens.cuda(), g.cuda(), torch.full((vocab, width), float("nan"), device="cuda"))
+    check_grad(got, tokens, g, vocab, 1.0, None, torch.float32)
