@@ -654,6 +654,8 @@ gemm_nt(GemmParams p) {
       rBz[pl] = rB[pl];
       rBz[pl][2] = 0;
     }
+    // (A load into LDS needs a wait state after a write of m0, its address;
+    // inside a block of assembly the compiler inserts none.)
     auto dma_stage = [&](int stage) {
       const uint32_t buf_lds = lds_base + static_cast<uint32_t>((stage % NST) * STB);
       const bool live = stage < nk;
@@ -667,11 +669,13 @@ gemm_nt(GemmParams p) {
         for (int pl = 0; pl < PL; ++pl) {
           asm volatile(
               "s_mov_b32 m0, %0\n\t"
+              "s_nop 0\n\t"
               "buffer_load_dwordx4 %1, %2, %3 offen lds"
               :: "s"(buf_lds + pl * OPB + blk * 1024), "v"(vA), "s"(live ? rA[pl] : rAz[pl]), "s"(soA)
               : "memory", "m0");
           asm volatile(
               "s_mov_b32 m0, %0\n\t"
+              "s_nop 0\n\t"
               "buffer_load_dwordx4 %1, %2, %3 offen lds"
               :: "s"(buf_lds + (PL + pl) * OPB + blk * 1024), "v"(vB), "s"(live ? rB[pl] : rBz[pl]), "s"(soB)
               : "memory", "m0");

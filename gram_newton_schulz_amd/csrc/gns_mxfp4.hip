@@ -501,6 +501,7 @@ __global__ void __launch_bounds__((L::THREADS)) mx_gemm(MxGemm p) {
   const int stages = min(groups - first, per_part);
 
   // this tile's rows of codes and scales; what lies past the last row reads as zero
+  // (the range check counts the scalar offset, too)
   auto panel = [&](const MxMatrix &q, int64_t row, int high, i32x4 *codes, i32x4 *scales) {
     const int64_t blocks = q.row_blocks();
     *codes = buffer_of(q.codes + (mat * q.rows + row) * pitch, min<int64_t>(high, q.rows - row) * pitch);
@@ -514,6 +515,8 @@ __global__ void __launch_bounds__((L::THREADS)) mx_gemm(MxGemm p) {
   const uint32_t lds_base =
       static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) unsigned char *)(lds)));
 
+  // (A load into LDS needs a wait state after a write of m0, its address; inside
+  // a block of assembly the compiler inserts none.)
   // Lane l of a load of codes fills 16 bytes of row l / 4 of its 16 rows, at
   // chunk l % 4; a load of scales fills two pieces, a word per lane.
   const int dma_row = lane >> 2;
@@ -530,14 +533,14 @@ __global__ void __launch_bounds__((L::THREADS)) mx_gemm(MxGemm p) {
 #pragma unroll
     for (int q = 0; q < L::LOADS_A; ++q) {
       const int blk = wave + q * L::NW;
-      asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(to + blk * 1024), "v"(code_at),
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(to + blk * 1024), "v"(code_at),
                    "s"(a), "s"(blk * 16 * pitch + at * 64)
                    : "memory", "m0");
     }
 #pragma unroll
     for (int q = 0; q < L::LOADS_B; ++q) {
       const int blk = wave + q * L::NW;
-      asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(to + L::CODES_A + blk * 1024),
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(to + L::CODES_A + blk * 1024),
                    "v"(code_at), "s"(b), "s"(blk * 16 * pitch + at * 64)
                    : "memory", "m0");
     }
@@ -549,7 +552,7 @@ __global__ void __launch_bounds__((L::THREADS)) mx_gemm(MxGemm p) {
       i32x4 x = of_a ? sa : sb;
       if (!live) x[2] = 0;
       const int piece = 2 * pair - (of_a ? 0 : L::PIECES_A);
-      asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
                    ::"s"(to + L::CODES_A + L::CODES_B + pair * 256), "v"(scale_at), "s"(x),
                    "s"(piece * groups * 128 + at * 128)
                    : "memory", "m0");
