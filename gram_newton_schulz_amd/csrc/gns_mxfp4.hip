@@ -1012,7 +1012,9 @@ MxPlan mx_plan(int64_t batch, int64_t m, int64_t n, int64_t k) {
   // Few rows of A take a tile that wastes less of them, if it fills the GPU
   // (64 matrices of 48 x 7168 by 2048 x 7168: 109 us, against 118 with 256 x 256).
   if (m <= 64 && tiles(64, 256) >= 256) return {MxPlan::T64, 1};
-  if (tiles(256, 256) >= 192) return {MxPlan::T256, 1};
+  // (A grid holds fewer than 2^32 threads: of these tiles, 512 to one, half as
+  // many as the calls let through of the smaller ones.)
+  if (tiles(256, 256) >= 192 && tiles(256, 256) < int64_t(1) << 23) return {MxPlan::T256, 1};
   // Where tiles of 128 leave compute units idle, a long contraction may be cut
   // into parts.  A stage takes 0.27 us of a workgroup; joining the parts takes a
   // launch, 5 us, and their results written and read at about 5 TB/s.  (48 x
