@@ -131,7 +131,12 @@ bool strides_ok(int64_t batch, int64_t rows, int64_t pitch, int64_t batch_stride
 gns_status check_out(const gns::MxOutput &o, gns_dtype dtype, int64_t batch, int64_t m, int64_t n, int accumulate) {
   if (!valid_dtype(dtype)) return GNS_E_DTYPE;
   if (!strides_ok(batch, m, o.pitch, o.batch_stride) || (m > 1 && o.pitch < n)) return GNS_E_SHAPE;
-  if (batch > 1 && m > 0 && o.batch_stride < (m - 1) * o.pitch + n) return GNS_E_SHAPE;
+  if (batch > 1 && m > 0) {
+    // matrices one behind the other, or their rows beside one another
+    const bool behind = o.batch_stride >= (m - 1) * o.pitch + n;
+    const bool beside = o.batch_stride >= n && o.pitch >= (batch - 1) * o.batch_stride + n;
+    if (!behind && !beside) return GNS_E_SHAPE;
+  }
   if (accumulate != 0 && accumulate != 1) return GNS_E_PARAM;
   if (batch == 0 || m == 0 || n == 0) return GNS_OK;
   if (!o.out) return GNS_E_NULL;

@@ -659,7 +659,8 @@ gns_status gns_mxfp4_dequantize(const gns_mxfp4 *q, void *out, gns_dtype dtype, 
  * out = a b^T for every matrix of the batch: [a.rows][b.rows], summed over
  * cols.  Products are exact, sums are fp32, and a result is rounded once.
  *   out          (device) rows `out_pitch` (>= b.rows) and matrices
- *                `out_batch_stride` elements apart, in out_dtype.
+ *                `out_batch_stride` elements apart, in out_dtype: one matrix
+ *                behind the other, or their rows beside one another.
  *   accumulate   1: out += a b^T, the sum in fp32 rounded once.
  *   workspace    (device) >= gns_mxfp4_matmul_workspace_bytes(batch, a.rows,
  *                b.rows, cols) bytes, 256-byte aligned, clobbered; may be NULL
