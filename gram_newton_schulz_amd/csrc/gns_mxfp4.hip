@@ -1010,8 +1010,11 @@ struct MxPlan {
 MxPlan mx_plan(int64_t batch, int64_t m, int64_t n, int64_t k) {
   auto tiles = [&](int64_t tm, int64_t tn) { return batch * ((m + tm - 1) / tm) * ((n + tn - 1) / tn); };
   // Few rows of A take a tile that wastes less of them, if it fills the GPU
-  // (64 matrices of 48 x 7168 by 2048 x 7168: 109 us, against 118 with 256 x 256).
-  if (m <= 64 && tiles(64, 256) >= 256) return {MxPlan::T64, 1};
+  // (64 matrices of 48 x 7168 by 2048 x 7168: 109 us, against 118 with 256 x 256.
+  // 48 x 4096 by 50257 x 4096, 197 tiles: 31.0 us, 32.2 with 256- and 32.1 with
+  // 128-edge ones; 48 x 2048 by 63000 x 2048: 20.2, 21.9 and 21.3; 48 x 4096 by 32768 x
+  // 4096, 128 tiles: 27.0, 28.1 and 18.5).
+  if (m <= 64 && tiles(64, 256) >= 192) return {MxPlan::T64, 1};
   // (A grid holds fewer than 2^32 threads: of these tiles, 512 to one, half as
   // many as the calls let through of the smaller ones.)
   if (tiles(256, 256) >= 192 && tiles(256, 256) < int64_t(1) << 23) return {MxPlan::T256, 1};

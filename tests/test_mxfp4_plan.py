@@ -49,3 +49,12 @@ def test_plans_of_ordinary_sizes():
     assert plan(64, 48, 2048, 7168) == (T64, 1)
     tile, parts = plan(1, 48, 4096, 16384)
     assert tile == T128 and parts > 1
+
+
+@pytest.mark.parametrize("m", [33, 40, 48, 63, 64])
+def test_few_rows_never_run_in_the_largest_tiles(m):
+    """Three quarters of whose rows they would waste: 192 tiles of 64 x 256 and
+    more are taken, fewer are 128-edge ones."""
+    for batch, n in [(1, 256 * t) for t in range(150, 300)] + [(1, 50257), (1, 63000), (28, 2048), (200, 100), (255, 256)]:
+        tile, _ = plan(batch, m, n, 4096)
+        assert tile == (T64 if batch * up(n, 256) >= 192 else T128), (batch, n)
