@@ -840,7 +840,7 @@ mx_join(const float *parts, int n_parts, int64_t part_stride, int64_t rows_all, 
 // With QUANTIZE the workgroup quantises A itself, as mx_quantize would, which
 // saves a launch, while the first loads of B are on their way.
 constexpr int kThinRows = 32;               // of A
-constexpr int kThinValues = 64 * 1024;      // of A that a workgroup quantises (up to 16 rows)
+constexpr int kThinValues = 64 * 1024;      // of A that a workgroup quantises at most: 34 KiB of LDS
 
 struct MxThin {
   MxMatrix a, b;                            // a: without codes where x is quantised here
@@ -1049,8 +1049,22 @@ bool thin(int64_t batch, int64_t m, int64_t n, int64_t k) {
          (m <= 16 || k == 0 || batch * n <= (int64_t(1) << 25) / k);
 }
 
+// Whether the product quantises A: each of its workgroups of 16 rows of B does
+// then, which costs more than the launch that it saves where rows and workgroups
+// are many.  (us in the product and before it, captured, K = 4096, bf16:
+//     rows of A by  1024         4096         16384        65536        131072
+//     1             3.7   6.2    5.1   7.8    9.5  12.5    30   37      55   65
+//     2             4.1   6.2    5.3   7.9    10.8 12.5    36   38      67   67
+//     4             4.6   6.4    6.0   8.1    13.5 12.8    45   40      84   70
+//     8             6.0   6.5    7.5   8.3    19.0 13.2    64   42      118  74
+//     16            9.0   6.9    10.8  8.9    29.6 14.5    102  46      190  84
+// Calls that are not captured pay the host for both launches, 11.5 us whatever the
+// size: 16 by 4096 take 10.2 and 11.3, 8 x 8192 by 4096 x 8192 12.7 and 11.5, 12 x
+// 2048 by 8192 x 2048 9.5 and 11.4.)
 bool mx_linear_quantizes(int64_t batch, int64_t m, int64_t n, int64_t k) {
-  return thin(batch, m, n, k) && m <= 16 && m * ((k + kMxGroup - 1) / kMxGroup) * kMxGroup <= kThinValues;
+  const int64_t values = m * ((k + kMxGroup - 1) / kMxGroup) * kMxGroup;
+  if (!thin(batch, m, n, k) || m > 16 || values > kThinValues) return false;
+  return m == 1 || values * batch * ((n + 15) / 16) <= int64_t(1) << (m == 2 ? 25 : 24);
 }
 
 size_t mx_matmul_bytes(int64_t batch, int64_t m, int64_t n, int64_t k) {

@@ -58,3 +58,14 @@ def test_few_rows_never_run_in_the_largest_tiles(m):
     for batch, n in [(1, 256 * t) for t in range(150, 300)] + [(1, 50257), (1, 63000), (28, 2048), (200, 100), (255, 256)]:
         tile, _ = plan(batch, m, n, 4096)
         assert tile == (T64 if batch * up(n, 256) >= 192 else T128), (batch, n)
+
+
+@pytest.mark.parametrize("batch,m,n,k,in_the_product", [
+    (1, 1, 4096, 16384, True), (1, 1, 131072, 4096, True), (64, 1, 2048, 2048, True), (1, 2, 65536, 4096, True),
+    (1, 8, 4096, 4096, True), (1, 16, 4096, 1024, True), (1, 16, 4096, 4096, True), (1, 16, 131072, 4096, False), (1, 8, 16384, 4096, False),
+    (1, 4, 16384, 16384, False), (1, 16, 4112, 4096, False), (64, 4, 1024, 2048, False), (1, 2, 131072, 4096, False)])
+def test_rows_that_many_workgroups_would_quantise_are_quantised_once(batch, m, n, k, in_the_product):
+    """... in the workspace, which only that needs at up to 16 rows."""
+    need = gns.mxfp4_matmul_workspace_bytes(batch, m, n, k, quantized=False)
+    assert (need == 0) == in_the_product
+    assert gns.mxfp4_matmul_workspace_bytes(batch, m, n, k) == 0
