@@ -597,11 +597,18 @@ def bench_lists(gns, torch, steps):
     return out
 
 
+def layer_copies(nbytes):
+    """Copies of a call's tensors of so many bytes: twice the last-level cache
+    (256 MiB) in all, three at least and sixteen at most."""
+    return min(16, max(3, -(-(512 << 20) // max(1, int(nbytes)))))
+
+
 def bench_layers(gns, torch, steps):
     """The layers' operators: ms per call, the GB/s of the bytes that each
     cannot do without (gradients, tables and matrices once, results once) and
-    for products TFLOP/s.  Calls go round three copies of their tensors, so that
-    none finds its own data in the last-level cache."""
+    for products TFLOP/s.  Calls go round as many copies of their tensors as keep
+    their data out of the last-level cache; calls of a few megabytes, whose times
+    are those of launches, may find theirs there."""
     gen = torch.Generator(device="cuda").manual_seed(11)
 
     def tensor(*shape, dtype=torch.bfloat16):
@@ -653,14 +660,15 @@ def bench_layers(gns, torch, steps):
             ("mxfp4_matmul 48x16384 by 4096x16384", lambda: linear(1, 48, 4096, 16384)),
             ("mxfp4_matmul 8192x4096 by 16384x4096", lambda: linear(1, 8192, 16384, 4096))):
         log(f"timing {name}")
-        calls = [make() for _ in range(3)]
+        calls = [make()]
+        calls += [make() for _ in range(layer_copies(calls[0][1]) - 1)]
         for f, _, _ in calls:
             f()
         torch.cuda.synchronize()
         e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
         e0.record()
         for i in range(steps):
-            calls[i % 3][0]()
+            calls[i % len(calls)][0]()
         e1.record()
         torch.cuda.synchronize()
         s = e0.elapsed_time(e1) / steps / 1e3
