@@ -611,9 +611,16 @@ __global__ void __launch_bounds__(256) embedding_join(Sums p, typename TW::S *we
 // kJoinLanes * 8 columns.  It looks through all tokens itself, each wave
 // through a quarter of them in order, and its groups of threads add up
 // consecutive parts of the row's gradients, and then theirs in order.  One
-// launch and no sort (4096 x 128 into 256 rows: 13 us, against 20 by the
-// way of the others).
-constexpr int kRowTokens = 4096;                       // at most
+// launch and no sort (us in this way and the others', bf16 into fp32 of 128 columns:
+//     4096 tokens into   256         512         1024        2048        4096 rows
+//     uniform            7.1  20.6   7.2  23.2   8.0  25.2   13   25     22   24
+//     by falling rank    16   20     16   22     15   23     15   23     22   24
+//     half of them one   47   23     47   24     48   26     49   25     52   25
+//     64 tokens          5.2  13.7   5.4  11.9   5.9  12.1   8.4  12.1   13   12.5
+// The tokens' frequencies are not known here: the bounds leave out sizes that
+// would gain if no token were frequent, and do not shut out a token that fills
+// the batch, whose row one workgroup adds up: 4096 of one into 256 rows 88 and 22.)
+constexpr int kRowTokens = 4096;                       // at most: their places fit 16 KiB of LDS
 constexpr int64_t kRowReads = int64_t(1) << 21;        // tokens read by all workgroups, at most
 constexpr int64_t kRowGroups = 4096;                   // workgroups, at most
 

@@ -6,9 +6,11 @@
 //                    from one read of it.  HBM-bound: 8192 x 16384 bf16 both
 //                    ways in 90 us (4.6 TB/s).
 // * mx_dequantize -- the values back.  HBM-bound.
-// * mx_gemm       -- C = A B^T of two quantised matrices by scaled MFMA.  Bound by
-//                    power where it is large (8192^3: 272 us, 4.0 PFLOP/s; 190 us
-//                    with codes of zero).
+// * mx_gemm       -- C = A B^T of two quantised matrices by scaled MFMA.  Where it is
+//                    large the matrix cores are busy 57% of the time at the clock
+//                    that the power leaves, 1.63 GHz (8192^3: 272 us, 4.0 PFLOP/s);
+//                    codes of zero take 190 us at a higher clock and about the same
+//                    share.
 // * mx_join       -- the sum of such a product's parts of the contraction.
 // * mx_thin       -- C = A B^T of few rows of A: bound by the bytes of B.  It can
 //                    quantise A itself.
@@ -194,6 +196,8 @@ constexpr int64_t kDealtTiles = 4096, kMaxDealt = int64_t(1) << 22;   // (a grid
 // tiles, where tiles of 64 make twice the workgroups (both ways, 3 x 257 x 1531
 // with noise: 16.5 -> 9.8 us; 4096 x 16384: 71 -> 87, as its rows of codes are
 // written in halves).  Both ways, 8192 x 16384 bf16 take 90 us (4.6 TB/s).  With
+// noise the arithmetic bounds it, twice the vector instructions: 185 us there, 136
+// against 76 for 4096 x 16384 fp32.  With
 // 32 rows of four columns per thread in registers instead of LDS, fp32 4096 x
 // 16384 took 166: its stores along the columns are scattered.
 template <class T, bool ROWS, bool COLS, bool NOISE, int kCols>
@@ -950,7 +954,11 @@ __global__ void __launch_bounds__(64 * W) mx_thin(MxThin p) {
 
 template <class TX, class TO, int MB, bool QUANTIZE>
 hipError_t run_thin(const MxThin &p, hipStream_t s) {
-  // about 4096 waves, at most 16 to a workgroup
+  // about 4096 waves, at most 16 to a workgroup (one row, 16 waves and four: 4096 x
+  // 4096 4.6 and 6.3 us, 4096 x 16384 10.1 and 16.7, 8192 x 16384 20.1 and 22.4; where
+  // a compute unit has more than one workgroup, between 256 and 512 of them, short
+  // contractions lose: 8192 x 4096 7.4 and 7.3, 8192 x 2048 5.7 and 5.0; beyond all do:
+  // 16384 x 4096 12.8 and 9.6)
   const int64_t grid = p.b.batch * ((p.b.rows + 15) / 16);
   if (grid <= 512 && p.b.groups() >= 16) mx_thin<TX, TO, MB, 16, QUANTIZE><<<dim3(grid), dim3(1024), 0, s>>>(p);
   else mx_thin<TX, TO, MB, 4, QUANTIZE><<<dim3(grid), dim3(256), 0, s>>>(p);
@@ -1015,6 +1023,11 @@ MxPlan mx_plan(int64_t batch, int64_t m, int64_t n, int64_t k) {
   // 128-edge ones; 48 x 2048 by 63000 x 2048: 20.2, 21.9 and 21.3; 48 x 4096 by 32768 x
   // 4096, 128 tiles: 27.0, 28.1 and 18.5).
   if (m <= 64 && tiles(64, 256) >= 192) return {MxPlan::T64, 1};
+  // Many tiles of 256 x 256 keep the GPU busy (k = 4096: 2048 x 6144 in 192 of them
+  // 32.2 us, 36.4 with 128-edge ones; 4096 x 4096 in 256 39.6 and 47.9).  The bound
+  // is on the safe side: 128 of them are 512 of the others, which fit at once (2048
+  // x 4096: 28.7 and 26.4), 160 would gain already (2560 x 4096: 29.5 and 35.6), 272
+  // start a second round that is nearly empty (4096 x 4352: 61.6 and 55.6).
   // (A grid holds fewer than 2^32 threads: of these tiles, 512 to one, half as
   // many as the calls let through of the smaller ones.)
   if (tiles(256, 256) >= 192 && tiles(256, 256) < int64_t(1) << 23) return {MxPlan::T256, 1};
@@ -1042,8 +1055,9 @@ int64_t join_pitch(int64_t n) { return (n + 3) / 4 * 4; }
 // Whether mx_thin takes a product: up to 16 rows of A, and up to kThinRows by a
 // B of up to 2^25 values.  Beyond those its workgroups' reads of A cost more
 // than the others' tiles waste (32 x 4096 by 4096 x 4096: 12.8 us, in tiles 16.7;
-// 32 x 16384 by 16384 x 16384: 54 and 33).  (A grid holds 2^24 workgroups of 256
-// threads.)
+// 32 x 16384 by 16384 x 16384: 54 and 33.  16 x 8192 by 16384 x 8192: 23.3 and 24.0; 16 x
+// 16384 by 16384 x 16384, the largest, 43.5 and 37.6).  (A grid holds 2^24 workgroups
+// of 256 threads.)
 bool thin(int64_t batch, int64_t m, int64_t n, int64_t k) {
   return m <= kThinRows && batch < (int64_t(1) << 24) / ((n + 15) / 16 + 1) &&
          (m <= 16 || k == 0 || batch * n <= (int64_t(1) << 25) / k);

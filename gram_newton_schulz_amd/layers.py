@@ -138,7 +138,8 @@ def embedding(tokens: torch.Tensor, weight: torch.Tensor, *, scale: float = 1.0,
     """``scale * weight[tokens]`` in one pass (gns_embedding): tokens (int32 or
     int64, any shape) into rows of weight ([vocab, width]), in ``dtype``
     (weight's by default) or into ``out`` ([*tokens.shape, width]).  A token
-    outside the vocabulary is padding and gives a row of zeros."""
+    outside the vocabulary is padding and gives a row of zeros.  No graph is
+    recorded: the gradient is :func:`embedding_grad`."""
     index = _index_of("tokens", tokens)
     if stream is not None or index != _current_device():
         with _elsewhere(index, stream):
@@ -436,7 +437,9 @@ def mxfp4_matmul(a: Union[MXFP4, torch.Tensor], b: MXFP4, *, out: Optional[torch
     """``a @ b^T`` ([m, k] by [n, k], or batches of them), with sums in fp32
     (gns_mxfp4_matmul), in ``dtype`` (a's, or bf16) or into ``out``;
     ``accumulate`` adds to ``out``.  A plain tensor ``a`` is quantised on the
-    way (gns_mxfp4_linear); with one matrix b it may have any leading axes."""
+    way (gns_mxfp4_linear); with one matrix b it may have any leading axes.  No
+    graph is recorded: a layer's gradients are two more products, of its
+    factors quantised along the other axis."""
     if not isinstance(b, MXFP4):
         raise GnsError(1, f"b is not an MXFP4: {type(b).__name__}")
     index = b._index
