@@ -628,10 +628,12 @@ def bench_layers(gns, torch, steps):
         into = torch.empty(vocab, width, device="cuda")
         return lambda: gns.embedding_grad(t, g, into), 2.0 * n * width + 4.0 * vocab * width, 0
 
-    def quantize(rows, cols, dtype):
+    def quantize(rows, cols, dtype, noisy=False):
         x = tensor(rows, cols, dtype=dtype)
+        noise = torch.randint(0, 256, (rows, cols), dtype=torch.uint8, device="cuda", generator=gen) if noisy else None
         out = gns.mxfp4_empty((rows, cols)), gns.mxfp4_empty((cols, rows))
-        return lambda: gns.mxfp4_quantize_both(x, out=out), rows * cols * (x.element_size() + 2 * 17 / 32), 0
+        return (lambda: gns.mxfp4_quantize_both(x, noise=noise, out=out),
+                rows * cols * (x.element_size() + noisy + 2 * 17 / 32), 0)
 
     def dequantize(rows, cols):
         q = gns.mxfp4_quantize(tensor(rows, cols))
@@ -654,6 +656,8 @@ def bench_layers(gns, torch, steps):
             ("embedding_grad 32768 into 32768x4096", lambda: embedding_grad(32768, 32768, 4096)),
             ("mxfp4_quantize_both 4096x16384 fp32", lambda: quantize(4096, 16384, torch.float32)),
             ("mxfp4_quantize_both 8192x16384 bf16", lambda: quantize(8192, 16384, torch.bfloat16)),
+            ("mxfp4_quantize_both 4096x16384 fp32, noise", lambda: quantize(4096, 16384, torch.float32, True)),
+            ("mxfp4_quantize_both 8192x16384 bf16, noise", lambda: quantize(8192, 16384, torch.bfloat16, True)),
             ("mxfp4_dequantize 4096x16384", lambda: dequantize(4096, 16384)),
             ("mxfp4_matmul 1x16384 by 4096x16384", lambda: linear(1, 1, 4096, 16384)),
             ("mxfp4_matmul 64 x 48x7168 by 2048x7168", lambda: linear(64, 48, 2048, 7168)),
